@@ -26,6 +26,7 @@ __all__ = [
     "gq_mxfp4_grouped_gemv_swiglu", "gq_mxfp4_grouped_gemm_scaled_swiglu",
     "gq_mxfp4_grouped_gemm_scaled_swiglu_split",
     "gq_mxfp4_grouped_gemv_down_combine", "gq_nf4_grouped_gemv_host", "gq_mxfp4_grouped_gemv_host",
+    "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward",
     "OSS_ALPHA", "OSS_LIMIT", "Route",
 ]
 
@@ -43,6 +44,7 @@ EXPORTED_SYMBOLS = (
     "gq_mxfp4_grouped_gemv_swiglu", "gq_mxfp4_grouped_gemm_scaled_swiglu",
     "gq_mxfp4_grouped_gemm_scaled_swiglu_split",
     "gq_mxfp4_grouped_gemv_down_combine", "gq_nf4_grouped_gemv_host", "gq_mxfp4_grouped_gemv_host",
+    "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward",
 )
 
 _i32, _i64, _p, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -89,6 +91,10 @@ _SIGNATURES = {
                                                                  _i32, _i32, _i32, _f32, _f32,
                                                                  _p, _p, _p, _p, _i32, _i32, _p,
                                                                  _p, _p]),
+    "gq_mxfp4_quantize": (ctypes.c_int, [_p, _i32, _i64, _i32, _i64, _p, _p, _p, _p]),
+    "gq_moe_topk": (ctypes.c_int, [_p, _i32, _i64, _i32, _i64, _i32, _i32, _p, _p, _p]),
+    "gq_moe_topk_backward": (ctypes.c_int, [_p, _p, _i32, _i64, _i32, _i64, _p, _i32, _i32, _p,
+                                            _p]),
 }
 
 _lib = None
@@ -659,3 +665,136 @@ def gq_mxfp4_grouped_gemm_scaled_swiglu_split(x_split, blocks, scales, route, al
         float(alpha), float(limit), *_route_ptrs(route), _ptr(oq), _ptr(osc), _stream(xq))
     _check(st, "gq_mxfp4_grouped_gemm_scaled_swiglu_split")
     return oq, osc
+
+
+# ---- MXFP4 quantisation --------------------------------------------------------
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}    # GQ_F32, GQ_BF16, GQ_F16
+
+
+def _typed(t, name):
+    """Type code of a device tensor of one of the three float types."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    return code
+
+
+def _beside(dev, **tensors):
+    """Every tensor of a call lies on the device that it runs on."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _on(dev, fn, what, *args):
+    """Call the library on ``dev``'s current stream, with ``dev`` current."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        _check(st, what)
+
+
+def _rows(t, name):
+    """(rows, width, row stride) of a tensor [..., width] whose leading
+    dimensions lie at one stride."""
+    if t.dim() < 1 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.shape[-1]) if t.shape[-1] else t.reshape(0, 0)
+        except RuntimeError:
+            raise ValueError(f"the leading dimensions of {name} must lie at one stride") from None
+    rows, width = t.shape
+    return rows, width, t.stride(0) if rows > 1 else width
+
+
+def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
+    """MXFP4 of x [..., K] (float32, bfloat16 or float16, any row stride):
+    returns (blocks uint8 [..., K/32, 16], scales uint8 [..., K/32]), the
+    layout that the MXFP4 entry points take.  ``values``: True or a bf16
+    tensor of x's shape also returns the values that the codes stand for."""
+    lib = load_library()
+    code = _typed(x, "x")
+    dev = x.device
+    rows, K, stride = _rows(x, "x")
+    lead = tuple(x.shape[:-1])
+    bshape, sshape = lead + (K // 32, 16), lead + (K // 32,)
+    if blocks is None:
+        blocks = torch.empty(bshape, dtype=torch.uint8, device=dev)
+    elif tuple(_dev(blocks, "blocks", torch.uint8).shape) != bshape:
+        raise ValueError(f"blocks must be {bshape}")
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
+    elif tuple(_dev(scales, "scales", torch.uint8).shape) != sshape:
+        raise ValueError(f"scales must be {sshape}")
+    if values is True:
+        values = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    elif values is False:
+        values = None
+    elif values is not None and _dev(values, "values", torch.bfloat16).shape != x.shape:
+        raise ValueError("values must have x's shape")
+    _beside(dev, blocks=blocks, scales=scales, values=values)
+    _on(dev, lib.gq_mxfp4_quantize, "gq_mxfp4_quantize", x.data_ptr(), code, rows, K, stride,
+        blocks.data_ptr(), scales.data_ptr(), None if values is None else values.data_ptr())
+    return (blocks, scales) if values is None else (blocks, scales, values)
+
+
+# ---- expert routing --------------------------------------------------------------
+def gq_moe_topk(logits, topk, renormalize=True, topk_ids=None, topk_weights=None):
+    """The ``topk`` largest logits [rows, E] (float32, bfloat16 or float16) of
+    each row, largest first, equal ones by lower index: (topk_ids int32 [rows,
+    topk], topk_weights float32 [rows, topk]), the weights a softmax over the
+    chosen logits (``renormalize``) or over all.  A logit of -inf is never
+    chosen; a slot left without an expert has id -1 and weight 0."""
+    lib = load_library()
+    code = _typed(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
+    rows, E, stride = _rows(logits, "logits")
+    dev, topk = logits.device, int(topk)
+    if topk < 1:
+        raise ValueError("topk must be at least 1")
+    shape = (rows, topk)
+    if topk_ids is None:
+        topk_ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    elif tuple(_dev(topk_ids, "topk_ids", torch.int32).shape) != shape:
+        raise ValueError(f"topk_ids must be {shape}")
+    if topk_weights is None:
+        topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    elif tuple(_dev(topk_weights, "topk_weights", torch.float32).shape) != shape:
+        raise ValueError(f"topk_weights must be {shape}")
+    _beside(dev, topk_ids=topk_ids, topk_weights=topk_weights)
+    _on(dev, lib.gq_moe_topk, "gq_moe_topk", logits.data_ptr(), code, rows, E, stride, topk,
+        1 if renormalize else 0, topk_ids.data_ptr(), topk_weights.data_ptr())
+    return topk_ids, topk_weights
+
+
+def gq_moe_topk_backward(d_weights, logits, topk_ids, renormalize=True, out=None):
+    """Gradient of ``gq_moe_topk``'s weights to its logits, the selection held
+    fixed: d_weights float32 [rows, topk] -> [rows, E] of the logits' type."""
+    lib = load_library()
+    code = _typed(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
+    rows, E, stride = _rows(logits, "logits")
+    dev = logits.device
+    _dev(d_weights, "d_weights", torch.float32, 2)
+    _dev(topk_ids, "topk_ids", torch.int32, 2)
+    if topk_ids.shape[0] != rows or d_weights.shape != topk_ids.shape:
+        raise ValueError("d_weights and topk_ids must both be [rows, topk]")
+    if out is None:
+        out = torch.empty((rows, E), dtype=logits.dtype, device=dev)
+    elif tuple(_dev(out, "out", logits.dtype).shape) != (rows, E):
+        raise ValueError("out must be [rows, E]")
+    _beside(dev, d_weights=d_weights, topk_ids=topk_ids, out=out)
+    _on(dev, lib.gq_moe_topk_backward, "gq_moe_topk_backward", d_weights.data_ptr(),
+        logits.data_ptr(), code, rows, E, stride, topk_ids.data_ptr(), topk_ids.shape[1],
+        1 if renormalize else 0, out.data_ptr())
+    return out

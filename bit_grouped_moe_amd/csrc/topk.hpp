@@ -1,0 +1,87 @@
+// Selection of the largest logits of a row by one wave, shared by the router
+// kernels and the decode layer.
+#pragma once
+
+#include <type_traits>
+
+#include "gq_device.hpp"
+
+namespace gq {
+
+constexpr int kTopkMax = 64;                 // slots: one per lane
+constexpr int kTopkMaxExperts = 1024;        // 16 logits per lane
+
+// Order-preserving key of a logit: larger logit, larger key; -0 and +0 are
+// one value; NaN is above every number (a NaN logit is chosen and makes its
+// row's weights NaN: it is never hidden); -inf, a masked expert, is kDeadKey
+// and is never chosen.  A slot past the row's experts has key 0.
+constexpr uint32_t kDeadKey = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t logit_key(float z) {
+  const uint32_t b = __float_as_uint(z + 0.0f);
+  const uint32_t k = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  return z != z ? 0xFFFFFFFFu : k;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  if (k == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
+}
+
+// Maximum over the wave, in every lane's scalar (uniform) result.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  auto step = [&](auto ctrl, auto mask) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value,
+                                                     decltype(mask)::value, 0xF, false));
+  };
+  step(std::integral_constant<int, 0xB1>{}, std::integral_constant<int, 0xF>{});
+  step(std::integral_constant<int, 0x4E>{}, std::integral_constant<int, 0xF>{});
+  step(std::integral_constant<int, 0x141>{}, std::integral_constant<int, 0xF>{});
+  step(std::integral_constant<int, 0x140>{}, std::integral_constant<int, 0xF>{});
+  step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+  step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0x8>{});
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Sum over the wave in a fixed order, the same value in every lane.
+__device__ __forceinline__ float wave_fsum(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(group_sum_last(v, 64)), 63));
+}
+
+// The topk largest of the row's logits, largest first, equal ones by lower
+// index.  Lane l holds experts 64 c + l in key[c]; lane s < topk receives
+// slot s (id -1 where only masked experts are left).  One wave maximum and
+// at most C ballots a slot, no memory.
+template <int C>
+__device__ __forceinline__ void wave_topk(uint32_t (&key)[C], int topk, int lane, int& id,
+                                          float& logit) {
+  id = -1;
+  logit = -__builtin_inff();
+  for (int s = 0; s < topk; ++s) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int c = 1; c < C; ++c) best = max(best, key[c]);
+    const uint32_t m = wave_umax(best);
+    if (m <= kDeadKey) break;                            // uniform
+    bool open = true;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint64_t at = __ballot(key[c] == m);
+      if (open && at) {
+        open = false;
+        const int l = __builtin_ctzll(at);
+        if (lane == l) key[c] = 0u;
+        if (lane == s) {
+          id = 64 * c + l;
+          logit = key_logit(m);
+        }
+      }
+    }
+  }
+}
+
+// The row's largest logit (slot 0's); 0 where every expert is masked.
+__device__ __forceinline__ float row_peak(float logit, int id) {
+  const float p = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(logit), 0));
+  return __builtin_amdgcn_readlane(id, 0) < 0 ? 0.0f : p;
+}
+
+}  // namespace gq

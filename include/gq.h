@@ -444,6 +444,69 @@ int gq_mxfp4_grouped_gemv_down_combine(const uint16_t* act, int32_t rows, int32_
 int gq_moe_combine(const uint16_t* y_pairs, int32_t rows, int32_t topk, int32_t H,
                    int64_t stride, const float* topk_weights, uint16_t* y, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Element types of entry points that take more than one.
+ */
+enum { GQ_F32 = 0, GQ_BF16 = 1, GQ_F16 = 2 };
+
+/* ------------------------------------------------------------------------
+ * MXFP4 quantisation on the device: the bytes that every MXFP4 entry point
+ * reads, from rows of values.  [P1] "Try the packers and byte checks on CPU"
+ * (packed shapes, round trip), [P2] summary (OCP e2m1 codes, e8m0 scales).
+ *   x       x_dtype [rows, K], row stride x_stride elements (any >= K, any
+ *           alignment of one element)
+ *   blocks  uint8 [rows, K/32, 16], scales uint8 [rows, K/32]         out
+ *   values  uint16 bf16 [rows, K] or NULL: the values that the codes stand
+ *           for (exact), the forward value of quantisation-aware training
+ *           (whose gradient passes straight through)                   out
+ * Per block of 32: X = clamp(floor(log2 amax) - 2, -127, 127), -127 for a
+ * zero block; code = sign and the nearest e2m1 magnitude of |v| 2^-X, ties
+ * to the even code, above 6 becomes 6; scale byte X + 127.  A block with an
+ * infinity or NaN stores scale 255 and codes 0: it decodes to NaN.
+ * Re-quantising decoded values reproduces the bytes.
+ * InvalidValue: null pointer (values may be NULL), unknown x_dtype, rows < 0,
+ *   K not a positive multiple of 32, x_stride < K, x not aligned to its
+ *   element, blocks or values not 16-byte aligned.
+ * NotSupported: more than 2^31 workgroups.  rows == 0 enqueues nothing.
+ */
+int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int64_t x_stride,
+                      uint8_t* blocks, uint8_t* scales, uint16_t* values, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Expert routing ([P4] "Functions": the routing tensor [M, top_k] and its
+ * weights, which the other entry points take).
+ *
+ * gq_moe_topk: the topk largest logits of each row, largest first, equal
+ * ones by lower index, with float32 softmax weights
+ *   w_s = exp(z_s - peak) / sum exp(z - peak)
+ * where the sum runs over the chosen logits (renormalize != 0) or over all
+ * of the row's.  A logit of -inf is a masked expert: it is never chosen, and
+ * a slot that only masked experts are left for gets id -1 and weight 0 (a
+ * dropped pair for every other entry point).  A NaN or +inf logit is chosen
+ * first and makes its row's weights NaN.
+ *   logits       dtype [rows, E], row stride `stride` elements
+ *   topk_ids     int32 [rows, topk], topk_weights float [rows, topk]   out
+ *
+ * gq_moe_topk_backward: gradient of the weights to the logits, through the
+ * same softmax, the selection held fixed:
+ *   d_logits[j] = p_j (G_j - sum_i p_i G_i),   G_j = sum of d_weights over
+ * the slots that name expert j; p the softmax over the chosen logits (0 for
+ * the others) or over all.  Ids outside [0, E) and masked experts take no
+ * gradient; an id that stands in several slots counts once per slot (so
+ * topk may exceed E here).
+ *   d_weights    float [rows, topk]
+ *   d_logits     dtype [rows, E], contiguous                           out
+ * InvalidValue: null pointer, unknown dtype, rows < 0, E < 1, topk < 1,
+ *   forward: topk > E, stride < E, misaligned pointers.
+ * NotSupported: E > 1024, topk > 64, rows > 2^33.  rows == 0 enqueues nothing.
+ */
+int gq_moe_topk(const void* logits, int32_t dtype, int64_t rows, int32_t num_experts,
+                int64_t stride, int32_t topk, int32_t renormalize, int32_t* topk_ids,
+                float* topk_weights, hipStream_t stream);
+int gq_moe_topk_backward(const float* d_weights, const void* logits, int32_t dtype, int64_t rows,
+                         int32_t num_experts, int64_t stride, const int32_t* topk_ids,
+                         int32_t topk, int32_t renormalize, void* d_logits, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

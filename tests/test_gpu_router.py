@@ -1,0 +1,239 @@
+"""Expert routing on the GPU against its definition in float64: the chosen
+experts exactly, weights and gradients to float32 rounding."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_grouped_moe_amd as gq
+from tests.gpu_common import device, say
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+U = 2.0 ** -24                                  # half a float32 step
+
+
+def _select(z, topk):
+    """Ids by a stable sort of the float64 logits (-inf never chosen)."""
+    order = np.argsort(-z, axis=1, kind="stable")[:, :topk]
+    live = np.take_along_axis(z, order, 1) > -np.inf
+    return np.where(live, order, -1)
+
+
+def _weights(z, ids, renorm):
+    """float64 weights of given slots."""
+    rows, E = z.shape
+    ok = (ids >= 0) & (ids < E)
+    zs = np.where(ok, np.take_along_axis(z, np.clip(ids, 0, E - 1), 1), -np.inf)
+    pool = zs if renorm else z
+    peak = pool.max(axis=1, keepdims=True)
+    peak = np.where(np.isfinite(peak), peak, 0.0)
+    total = np.exp(pool - peak).sum(axis=1, keepdims=True)
+    return np.exp(zs - peak) / np.where(total > 0, total, 1.0), peak - zs
+
+
+def _grad(z, ids, dw, renorm):
+    """The softmax Jacobian applied slot by slot, float64."""
+    rows, E = z.shape
+    w, _ = _weights(z, ids, renorm)
+    out = np.zeros_like(z)
+    for r in range(rows):
+        for s in range(ids.shape[1]):
+            j = ids[r, s]
+            if not 0 <= j < E or w[r, s] == 0:
+                continue
+            out[r, j] += dw[r, s] * w[r, s]
+            if renorm:
+                for q in range(ids.shape[1]):
+                    if 0 <= ids[r, q] < E:
+                        out[r, ids[r, q]] -= dw[r, s] * w[r, s] * w[r, q]
+            else:
+                peak = z[r].max()
+                p = np.exp(z[r] - peak)
+                out[r] -= dw[r, s] * w[r, s] * p / p.sum()
+    return out
+
+
+def _logits(g, rows, E, dtype, kind):
+    z = torch.randn(rows, E, generator=g) * 3
+    if kind == "ties":
+        z = (z * 2).round() / 2
+        z[z == 0] = -0.0
+        z[:, ::2][z[:, ::2] == 0] = 0.0                  # -0 and +0 are equal
+    if kind == "masked":
+        z[torch.rand(rows, E, generator=g) < 0.5] = -float("inf")
+        z[0] = -float("inf")
+        if rows > 1:
+            z[1] = torch.finfo(dtype).min                # the lowest value is a value
+    return z.to(dtype)
+
+
+def _check_forward(z, ids, w, topk, renorm):
+    z64 = z.double().cpu().numpy()
+    ref = _select(z64, topk)
+    assert np.array_equal(ids.cpu().numpy(), ref)
+    rw, gap = _weights(z64, ref, renorm)
+    # the exponent's argument is off by half a step of its size, exp, sum
+    # (at most 16 + 6 additions) and quotient by a few steps more
+    tol = (np.where(np.isfinite(gap), np.abs(gap), 0) + 40) * U * rw + 1e-37
+    assert (np.abs(w.double().cpu().numpy() - rw) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["plain", "ties", "masked"])
+@pytest.mark.parametrize("rows,E,topk", [(1, 1, 1), (1, 128, 8), (7, 5, 5), (33, 32, 4),
+                                         (5, 64, 64), (6, 65, 3), (130, 129, 8), (9, 300, 10),
+                                         (4, 512, 2), (3, 1024, 33)])
+def test_forward_and_backward(dtype, kind, rows, E, topk):
+    dev = device()
+    g = torch.Generator().manual_seed(rows * 1000 + E + topk)
+    z = _logits(g, rows, E, dtype, kind)
+    dw = torch.randn(rows, topk, generator=g)
+    zd, dwd = z.to(dev), dw.to(dev)
+    for renorm in (True, False):
+        say("router", dtype, kind, rows, E, topk, renorm)
+        ids, w = gq.gq_moe_topk(zd, topk, renormalize=renorm)
+        dz = gq.gq_moe_topk_backward(dwd, zd, ids, renormalize=renorm)
+        torch.cuda.synchronize()
+        _check_forward(z, ids, w, topk, renorm)
+        assert dz.dtype == dtype and dz.shape == z.shape
+        z64, d64, i64 = z.double().numpy(), dw.double().numpy(), ids.cpu().numpy()
+        ref = _grad(z64, i64, d64, renorm)
+        w64, gap = _weights(z64, i64, renorm)
+        # each term p (g - sum p g) at the rounding of p, one product and a
+        # sum of at most 64 slots; then one rounding to the output's type
+        big = (np.abs(d64).max(axis=1) * 2)[:, None]
+        pool = np.where(np.isfinite(z64), z64, -np.inf)
+        peak = pool.max(axis=1, keepdims=True)
+        p = np.where(np.isfinite(peak), np.exp(pool - np.where(np.isfinite(peak), peak, 0)), 0)
+        p = p / np.maximum(p.sum(axis=1, keepdims=True), 1e-300)
+        if renorm:                                       # chosen experts only, larger weights
+            p = np.zeros_like(p)
+            for r in range(rows):
+                for s in range(topk):
+                    if i64[r, s] >= 0:
+                        p[r, i64[r, s]] += w64[r, s]
+        spread = np.where(np.isfinite(z64), np.abs(peak - z64), 0)
+        spread = np.where(np.isfinite(spread) & (p > 0), spread, 0)
+        tol = p * big * (spread + 120) * U
+        # (below its normal range an output type has a fixed step)
+        tol = tol + np.abs(ref) * torch.finfo(dtype).eps / 2 + (
+            2.0 ** -25 if dtype == torch.float16 else 1e-37)
+        assert (np.abs(dz.double().cpu().numpy() - ref) <= tol * 1.0001).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_against_differences(renorm):
+    """The kernel's gradient against central differences of the float64
+    weights, the selection held fixed: truncation h^2 / 6 times the third
+    derivative (below 6 for a softmax) and rounding 1e-16 / h."""
+    dev = device()
+    g = torch.Generator().manual_seed(17)
+    rows, E, topk, h = 4, 24, 5, 1e-4
+    z = torch.randn(rows, E, generator=g)
+    dw = torch.randn(rows, topk, generator=g)
+    say("router differences", renorm)
+    ids, _ = gq.gq_moe_topk(z.to(dev), topk, renormalize=renorm)
+    dz = gq.gq_moe_topk_backward(dw.to(dev), z.to(dev), ids, renormalize=renorm)
+    torch.cuda.synchronize()
+    z64, i64, d64 = z.double().numpy(), ids.cpu().numpy(), dw.double().numpy()
+    num = np.zeros_like(z64)
+    for j in range(E):
+        up, dn = z64.copy(), z64.copy()
+        up[:, j] += h
+        dn[:, j] -= h
+        num[:, j] = ((_weights(up, i64, renorm)[0] - _weights(dn, i64, renorm)[0]) * d64).sum(
+            axis=1) / (2 * h)
+    big = np.abs(d64).sum(axis=1, keepdims=True)
+    assert (np.abs(dz.double().cpu().numpy() - num) <= big * (h * h + 1e-11 + 200 * U)).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_backward_of_given_ids(renorm):
+    """Ids of the caller's own: an expert named twice, ids outside [0, E), a
+    masked expert."""
+    dev = device()
+    z = torch.tensor([[0.5, -1.0, 2.0, -float("inf"), 0.25], [-float("inf")] * 5])
+    ids = torch.tensor([[2, 2, -1, 3, 7, 0], [0, 1, 2, 3, 4, -1]], dtype=torch.int32)
+    dw = torch.tensor([[1.0, -2.0, 5.0, 7.0, 9.0, 0.5], [1.0] * 6])
+    say("router given ids", renorm)
+    dz = gq.gq_moe_topk_backward(dw.to(dev), z.to(dev), ids.to(dev), renormalize=renorm)
+    torch.cuda.synchronize()
+    z64, d64, i64 = z.double().numpy(), dw.double().numpy(), ids.numpy()
+    ref = np.zeros((2, 5))
+    slots = [(2, 1.0), (2, -2.0), (0, 0.5)]
+    if renorm:
+        e = np.exp(np.array([z64[0, j] for j, _ in slots]) - 2.0)
+        p = e / e.sum()
+        dot = sum(pi * d for pi, (_, d) in zip(p, slots))
+        for pi, (j, d) in zip(p, slots):
+            ref[0, j] += pi * (d - dot)
+    else:
+        p = np.exp(z64[0] - 2.0)
+        p = p / p.sum()
+        dot = sum(p[j] * d for j, d in slots)
+        G = np.zeros(5)
+        for j, d in slots:
+            G[j] += d
+        ref[0] = p * (G - dot)
+    assert np.abs(dz.double().cpu().numpy() - ref).max() <= 100 * U * np.abs(d64).max()
+    assert not dz[1].any() and dz[0, 3] == 0
+
+
+def test_nan_and_infinite_logits_are_not_hidden():
+    dev = device()
+    nan, inf = float("nan"), float("inf")
+    z = torch.tensor([[0.0, nan, 1.0, nan], [inf, 0.0, 1.0, 2.0], [0.0, 1.0, 2.0, 3.0],
+                      [-nan, -inf, -inf, -inf]])
+    say("router nan")
+    ids, w = gq.gq_moe_topk(z.to(dev), 2)
+    torch.cuda.synchronize()
+    assert ids.tolist() == [[1, 3], [0, 3], [3, 2], [0, -1]]
+    w = w.cpu()
+    assert w[0].isnan().all() and w[1, 0].isnan() and w[3, 0].isnan() and w[3, 1] == 0
+    assert abs(float(w[2].sum()) - 1) < 1e-6
+
+
+def test_strided_rows_empty_and_large():
+    dev = device()
+    g = torch.Generator().manual_seed(3)
+    z = torch.randn(50, 200, generator=g).to(torch.bfloat16)
+    part = z.to(dev)[::2, 3:67]
+    say("router strided")
+    ids, w = gq.gq_moe_topk(part, 6)
+    dz = gq.gq_moe_topk_backward(torch.ones(25, 6, device=dev), part, ids)
+    torch.cuda.synchronize()
+    _check_forward(z[::2, 3:67], ids, w, 6, True)
+    assert dz.shape == (25, 64)
+    # all weights of a row up together: the softmax does not move
+    assert float(dz.float().abs().max()) <= 64 * U
+    ids, w = gq.gq_moe_topk(part[:0], 6)
+    assert ids.shape == (0, 6) and w.shape == (0, 6)
+    assert gq.gq_moe_topk_backward(w, part[:0], ids).shape == (0, 64)
+    big = torch.randn(100003, 32, generator=g)
+    ids, w = gq.gq_moe_topk(big.to(dev), 4, renormalize=False)
+    torch.cuda.synchronize()
+    _check_forward(big, ids, w, 4, False)
+    with pytest.raises(gq.GQError):
+        gq.gq_moe_topk(part, 65)
+    with pytest.raises(ValueError):
+        gq.gq_moe_topk(part, 0)
+    with pytest.raises(ValueError):
+        gq.gq_moe_topk_backward(w, part, ids)
+
+
+def test_routing_feeds_the_sort():
+    """Slots without an expert become dropped pairs of the grouping."""
+    dev = device()
+    z = torch.randn(70, 16, generator=torch.Generator().manual_seed(4))
+    z[::5] = -float("inf")
+    z[1::5, 1:] = -float("inf")
+    say("router into sort")
+    ids, w = gq.gq_moe_topk(z.to(dev), 3)
+    route = gq.gq_route_sort(ids, 16)
+    torch.cuda.synchronize()
+    live = int((ids >= 0).sum())
+    assert live == 42 * 3 + 14
+    assert int(route.expert_offsets[-1]) == live
+    assert not w.cpu()[::5].any() and (w.cpu()[1::5, 0] == 1).all()
