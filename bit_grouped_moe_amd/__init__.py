@@ -26,7 +26,8 @@ __all__ = [
     "gq_mxfp4_grouped_gemv_swiglu", "gq_mxfp4_grouped_gemm_scaled_swiglu",
     "gq_mxfp4_grouped_gemm_scaled_swiglu_split",
     "gq_mxfp4_grouped_gemv_down_combine", "gq_nf4_grouped_gemv_host", "gq_mxfp4_grouped_gemv_host",
-    "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward",
+    "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward", "gq_moe_layer",
+    "gq_moe_decode_workspace", "gq_moe_decode",
     "OSS_ALPHA", "OSS_LIMIT", "Route",
 ]
 
@@ -44,7 +45,8 @@ EXPORTED_SYMBOLS = (
     "gq_mxfp4_grouped_gemv_swiglu", "gq_mxfp4_grouped_gemm_scaled_swiglu",
     "gq_mxfp4_grouped_gemm_scaled_swiglu_split",
     "gq_mxfp4_grouped_gemv_down_combine", "gq_nf4_grouped_gemv_host", "gq_mxfp4_grouped_gemv_host",
-    "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward",
+    "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward", "gq_moe_decode_workspace",
+    "gq_moe_decode",
 )
 
 _i32, _i64, _p, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -95,6 +97,8 @@ _SIGNATURES = {
     "gq_moe_topk": (ctypes.c_int, [_p, _i32, _i64, _i32, _i64, _i32, _i32, _p, _p, _p]),
     "gq_moe_topk_backward": (ctypes.c_int, [_p, _p, _i32, _i64, _i32, _i64, _p, _i32, _i32, _p,
                                             _p]),
+    "gq_moe_decode_workspace": (_i64, [_p, _i32]),
+    "gq_moe_decode": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _i64, _p, _p]),
 }
 
 _lib = None
@@ -797,4 +801,96 @@ def gq_moe_topk_backward(d_weights, logits, topk_ids, renormalize=True, out=None
     _on(dev, lib.gq_moe_topk_backward, "gq_moe_topk_backward", d_weights.data_ptr(),
         logits.data_ptr(), code, rows, E, stride, topk_ids.data_ptr(), topk_ids.shape[1],
         1 if renormalize else 0, out.data_ptr())
+    return out
+
+
+# ---- a whole layer for a few tokens ------------------------------------------------
+class _LayerStruct(ctypes.Structure):
+    """gq_moe_layer of include/gq.h."""
+    _fields_ = ([(n, _i32) for n in ("format", "num_experts", "topk", "hidden", "inner",
+                                     "renormalize")]
+                + [("alpha", _f32), ("limit", _f32)]
+                + [(n, _p) for n in ("router_weight", "router_bias", "gate_up_codes",
+                                     "gate_up_scales", "gate_up_bias", "down_codes",
+                                     "down_scales", "down_bias")])
+
+
+class MoeLayer:
+    """A layer's checked weights, made by ``gq_moe_layer``; keeps its tensors."""
+
+    def __init__(self, struct, tensors, device):
+        self._struct, self._tensors, self.device = struct, tensors, device
+        self._ref = ctypes.addressof(struct)
+        self.hidden, self.topk = struct.hidden, struct.topk
+        self._bytes = {}                         # workspace bytes by token count
+
+
+def gq_moe_layer(router_weight, gate_up, down, topk, router_bias=None, gate_up_bias=None,
+                 down_bias=None, renormalize=True, alpha=OSS_ALPHA, limit=OSS_LIMIT):
+    """The weights of one mixture-of-experts layer, for ``gq_moe_decode``.
+
+    ``router_weight`` bf16 [E, H]; ``gate_up`` and ``down`` are (codes, absmax)
+    of NF4 experts [E, 2I, H] and [E, H, I] (SwiGLU, gate rows first) or
+    (blocks, scales) of MXFP4 experts (the clamped unit, gate and up rows
+    interleaved); the optional biases are bf16 [E], [E, 2I] and [E, H].  The
+    layer refers to these tensors: what is written into them later counts."""
+    load_library()
+    _dev(router_weight, "router_weight", torch.bfloat16, 2)
+    E, H = router_weight.shape
+    dev = router_weight.device
+    mx = isinstance(gate_up[0], torch.Tensor) and gate_up[0].dim() == 4
+    bank = _mx_bank if mx else _nf4_bank
+    Eg, N, K = bank(*gate_up)
+    Ed, Hd, inner = bank(*down)
+    if (Eg, Ed, K, Hd, N) != (E, E, H, H, 2 * inner):
+        raise ValueError(f"router [{E}, {H}], gate_up [{Eg}, {N}, {K}] and down [{Ed}, {Hd}, "
+                         f"{inner}] are not one layer's")
+    for name, b, shape in (("router_bias", router_bias, (E,)),
+                           ("gate_up_bias", gate_up_bias, (E, N)), ("down_bias", down_bias, (E, H))):
+        if b is not None and tuple(_dev(b, name, torch.bfloat16).shape) != shape:
+            raise ValueError(f"{name} must be {shape}")
+    tensors = (router_weight, router_bias, *gate_up, gate_up_bias, *down, down_bias)
+    for t in tensors:
+        _beside(dev, weight=t)
+    ptr = [None if t is None else t.data_ptr() for t in tensors]
+    struct = _LayerStruct(1 if mx else 0, E, int(topk), H, inner, 1 if renormalize else 0,
+                          float(alpha), float(limit), *ptr)
+    layer = MoeLayer(struct, tensors, dev)
+    if gq_moe_decode_workspace(layer, 0) < 0:
+        raise GQError(f"gq_moe_layer: not supported (E {E}, topk {topk}, H {H}, I {inner}, "
+                      f"alpha {alpha}, limit {limit})", 1)
+    return layer
+
+
+def gq_moe_decode_workspace(layer, rows):
+    """Bytes of workspace for ``rows`` tokens; -1 where gq_moe_decode does not take them."""
+    return int(load_library().gq_moe_decode_workspace(layer._ref, rows))
+
+
+def gq_moe_decode(layer, x, out=None, workspace=None):
+    """The whole layer for x bf16 [rows, H], at most 8 tokens and 64 (token,
+    expert) pairs: bf16 [rows, H].  ``workspace``: a uint8 tensor of at least
+    gq_moe_decode_workspace bytes (allocated when None)."""
+    lib = load_library()
+    rows, H, stride = _x_args(x)
+    dev = x.device
+    if H != layer.hidden:
+        raise ValueError(f"x must be [rows, {layer.hidden}]")
+    need = layer._bytes.get(rows)
+    if need is None:
+        need = layer._bytes[rows] = gq_moe_decode_workspace(layer, rows)
+    if need < 0:
+        raise GQError(f"gq_moe_decode: {rows} tokens of {layer.topk} experts are not supported "
+                      "(at most 8 tokens and 64 pairs)", 801)
+    if out is None:
+        out = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
+    elif tuple(_dev(out, "out", torch.bfloat16).shape) != (rows, H):
+        raise ValueError(f"out must be [{rows}, {H}]")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    _beside(layer.device, x=x, out=out, workspace=workspace)
+    _on(dev, lib.gq_moe_decode, "gq_moe_decode", layer._ref, x.data_ptr(), rows,
+        stride if rows > 1 else H, workspace.data_ptr(), workspace.numel(), out.data_ptr())
     return out

@@ -1,0 +1,549 @@
+// A whole mixture-of-experts layer for a few tokens (at most 8 tokens and 64
+// routed pairs): router product, selection, the experts' gated products and
+// the weighted combine, in three launches without a host round trip.
+//
+//   z = x Wr^T + br                                         (launch 1)
+//   e_s, w_s = the topk largest logits of a token, softmax   (launch 2)
+//   a_s = unit(Wgu[e_s] x + bgu[e_s])                        (launch 2)
+//   y = sum_s w_s (Wd[e_s] a_s + bd[e_s])                    (launch 3)
+//
+// Everything between the bf16 input and the bf16 output is float32 (logits,
+// weights, gated products: the workspace holds them).  Bound by the latency
+// of the dependent round trips for one token and by the active experts'
+// bytes for several.
+//
+// The launches are the dependencies between workgroups: the logits need
+// every hidden element and are spread over the chip (one workgroup per
+// expert); the gate_up product needs the selection, the down product whole
+// activation rows.  The selection itself is a wave's work on E logits, so
+// each gate_up workgroup makes it again for itself instead of waiting for a
+// launch of its own.
+#include <algorithm>
+#include <type_traits>
+
+#include "gemv_common.hpp"
+#include "topk.hpp"
+#include "gq_host.hpp"
+#include "../../include/gq.h"
+
+namespace gq {
+
+constexpr int kMoeMaxRows = 8;
+constexpr int kMoeMaxPairs = 64;             // a wave's lanes
+constexpr int kMoeMaxExperts = 512;          // logits of a token: 8 per lane
+constexpr int kMoeMaxHidden = 8192;          // 256 segments of 32 weights
+constexpr int kMoeMaxInner = 128 * 32;       // two segments per lane
+constexpr int kMoeThreads = 256;
+constexpr int kDownWaves = 8;
+
+__device__ __forceinline__ float bf16_at(const uint16_t* p, int64_t i) {
+  return __uint_as_float((uint32_t)p[i] << 16);
+}
+
+// ---- launch 1: logits of one expert for every token -------------------------
+// Workgroup e; thread t takes the 16-byte pieces t, t + 256, ... of the
+// expert's row and of each token's.
+template <int kRows>
+__global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ w, int H, int x_stride, int rows,
+    int E, const uint16_t* __restrict__ bias, float* __restrict__ logits) {
+  __shared__ float part[kMoeThreads / kWave][kRows];
+  const int e = blockIdx.x, tid = threadIdx.x;
+  const int wave = tid / kWave, lane = tid & (kWave - 1);
+  const float b = bias && tid < rows ? bf16_at(bias, e) : 0.f;
+  float acc[kRows];
+#pragma unroll
+  for (int t = 0; t < kRows; ++t) acc[t] = 0.f;
+  const u32x4* wr = reinterpret_cast<const u32x4*>(w + (int64_t)e * H);
+  for (int c = tid; c < H / 8; c += kMoeThreads) {
+    const u32x4 wv = wr[c];
+    u32x4 xv[kRows];
+#pragma unroll
+    for (int t = 0; t < kRows; ++t)
+      xv[t] = *reinterpret_cast<const u32x4*>(x + (int64_t)min(t, rows - 1) * x_stride + c * 8);
+#pragma unroll
+    for (int t = 0; t < kRows; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[t] = __builtin_fmaf(bf16lo_to_f32(wv[i]), bf16lo_to_f32(xv[t][i]), acc[t]);
+        acc[t] = __builtin_fmaf(bf16hi_to_f32(wv[i]), bf16hi_to_f32(xv[t][i]), acc[t]);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < kRows; ++t) {
+    const float s = group_sum_last(acc[t], kWave);
+    if (lane == kWave - 1) part[wave][t] = s;
+  }
+  lds_barrier();
+  if (tid < rows) {
+    float s = part[0][tid];
+#pragma unroll
+    for (int i = 1; i < kMoeThreads / kWave; ++i) s += part[i][tid];
+    logits[(int64_t)tid * E + e] = s + b;
+  }
+}
+
+// ---- launch 2: selection, gate_up product and gated unit ---------------------
+// Grid (column chunks, pairs), the row layout of the decode GEMV: workgroup
+// (x, p) computes output columns [n0, n0 + R/2) of pair p's expert for every
+// pair that shares it, if p is the first of them; the others end after the
+// selection.  NF4: gate row j, up row I + j, SwiGLU; MXFP4: gate row 2j, up
+// row 2j + 1, the clamped unit.  Workgroup (0, 0) writes the selection for
+// launch 3.
+template <bool kMx, int kIter, bool kWaveRows, int C>
+__global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
+    const float* __restrict__ logits, const uint16_t* __restrict__ x,
+    const uint8_t* __restrict__ codes, const void* __restrict__ scl, int H, int I, int E,
+    int x_stride, int topk, int rows, const uint16_t* __restrict__ bias, float alpha, float limit,
+    int renorm, int32_t* __restrict__ ids_out, float* __restrict__ w_out,
+    float* __restrict__ act) {
+  constexpr int kHalf = kIter / 2;
+  __shared__ __attribute__((aligned(4096))) LutT lut[kLutN];
+  __shared__ float red[kWaveRows ? 1 : kIter * (kMoeThreads + 32)];
+  __shared__ int ids_s[kMoeMaxPairs];
+
+  const int N = 2 * I, P = rows * topk;
+  const int S = H >> 5;
+  int W, G, NT;
+  if constexpr (kWaveRows) {
+    const int lgW = S > 1 ? 32 - __builtin_clz(S - 1) : 0;
+    W = 1 << lgW;
+    G = kMoeThreads >> lgW;
+    NT = kMoeThreads;
+  } else {
+    W = S;
+    G = S >= kMoeThreads ? 1 : kMoeThreads / S;
+    NT = ((S * G + kWave - 1) / kWave) * kWave;
+  }
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int p0 = blockIdx.y;
+  const int R = G * kIter, Rout = R / 2;
+  const int n0 = blockIdx.x * Rout;
+  const int g = tid / W, s = tid - g * W;
+  const bool active = kWaveRows ? s < S : tid < S * G;
+
+  // p0's activations and the table, ahead of the selection
+  u32x4 xr[4];
+  auto load_x = [&](int p) {
+    const u32x4* xp = reinterpret_cast<const u32x4*>(x + (int64_t)(p / topk) * x_stride +
+                                                      (active ? s : 0) * 32);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) xr[v] = xp[v];
+  };
+  load_x(p0);
+  if constexpr (!kMx) lut_init(lut, tid, NT);
+
+  // ---- selection: a wave per token ----
+  const bool writer = blockIdx.x == 0 && blockIdx.y == 0;
+  for (int t = wave; t < rows; t += NT / kWave) {
+    uint32_t key[C], all[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = 64 * c + lane;
+      const float z = logits[(int64_t)t * E + min(e, E - 1)];
+      key[c] = all[c] = e < E ? logit_key(z) : 0u;
+    }
+    int id;
+    float z;
+    wave_topk<C>(key, topk, lane, id, z);
+    if (lane < topk) ids_s[t * topk + lane] = id;
+    if (writer) {
+      const float peak = row_peak(z, id);
+      const float part = id >= 0 ? expf(z - peak) : 0.f;
+      float total = part;
+      if (!renorm) {
+        total = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          total += all[c] > kDeadKey ? expf(key_logit(all[c]) - peak) : 0.f;
+      }
+      total = wave_fsum(total);
+      if (lane < topk) {
+        ids_out[t * topk + lane] = id;
+        w_out[t * topk + lane] = id >= 0 ? part / total : 0.f;
+      }
+    }
+  }
+  lds_barrier();
+  const int e = __builtin_amdgcn_readfirstlane(ids_s[p0]);
+  const int idl = ids_s[min(lane, P - 1)];
+  uint64_t same = __ballot(idl == e && lane < P);
+  // no expert, or an earlier pair's workgroup computes this one (uniform)
+  if (e < 0 || (same & ((1ull << p0) - 1ull))) return;
+
+  // ---- weight bytes: all of a thread's loads before their first use ----
+  auto wrow = [&](int gg, int i) -> int {
+    if constexpr (!kMx) {
+      const int j = min(n0 + gg + G * (i % kHalf), I - 1);
+      return i < kHalf ? j : I + j;
+    } else {
+      if constexpr (!kWaveRows) return min(2 * n0 + gg + G * i, N - 1);
+      const int j = min(n0 + gg + G * (i % kHalf), I - 1);
+      return 2 * j + (i < kHalf ? 0 : 1);
+    }
+  };
+  const uint32_t row_bytes = (uint32_t)H / 2;
+  const uint32_t s_cl = active ? s : 0;
+  constexpr uint32_t kScaleBytes = kMx ? 1u : 4u;
+  const uint32_t spr = kMx ? (uint32_t)(H / 32) : (uint32_t)(H / 64);
+  const uint8_t* cbase = codes + (size_t)e * ((size_t)N * row_bytes);
+  const uint8_t* sbase =
+      static_cast<const uint8_t*>(scl) + (size_t)e * ((size_t)N * spr * kScaleBytes);
+  u32x4 cw[kIter];
+  float am[kIter], bv[kIter];
+  uint32_t sb[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const uint32_t r = (uint32_t)wrow(g, i);
+    cw[i] = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x4*>(cbase + (__umul24(r, row_bytes) + s_cl * 16u)));
+    const uint32_t so = (__umul24(r, spr) + (kMx ? s_cl : s_cl / 2)) * kScaleBytes;
+    if constexpr (kMx) {
+      sb[i] = (uint32_t)sbase[so];
+      am[i] = 0.f;
+    } else {
+      am[i] = *reinterpret_cast<const float*>(sbase + so);
+      sb[i] = 0u;
+    }
+    bv[i] = 0.f;
+  }
+  // biases: in-wave rows, each row's on its lanes; LDS rows, gate and up of
+  // output column n0 + tid in bv[0], bv[1]
+  if (bias) {
+    const uint16_t* be = bias + (size_t)e * N;
+    if constexpr (kWaveRows) {
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) bv[i] = bf16_at(be, wrow(g, i));
+    } else {
+      const int n = min(n0 + tid, I - 1);
+      bv[0] = bf16_at(be, kMx ? 2 * n : n);
+      bv[1] = bf16_at(be, kMx ? 2 * n + 1 : I + n);
+    }
+  }
+
+  auto unit = [&](float gate, float up) {
+    if constexpr (kMx) {
+      const float gc = fminf(gate, limit);
+      const float uc = fminf(fmaxf(up, -limit), limit);
+      const float a = gc * sigmoid_f32(alpha * gc) * (uc + 1.0f);
+      // the minimum and maximum drop a NaN; the unit does not
+      return gate != gate || up != up ? gate + up : a;
+    } else {
+      return silu_f32(gate) * up;
+    }
+  };
+  while (same) {                              // p0 first, then ascending
+    const int p = __builtin_ctzll(same);
+    same &= same - 1ull;
+    if (p != p0) load_x(p);
+    float xf[32];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        xf[8 * v + 2 * cc] = bf16lo_to_f32(xr[v][cc]);
+        xf[8 * v + 2 * cc + 1] = bf16hi_to_f32(xr[v][cc]);
+      }
+    if constexpr (kWaveRows) {
+      float vals[kIter];
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const float part = active ? segment_dot<kMx>(lut, cw[i], am[i], sb[i], xf, xr) : 0.f;
+        vals[i] = group_sum_last(part, W) + bv[i];             // total on lane s == W - 1
+      }
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const int n = n0 + g + G * i;
+        if (s == W - 1 && n < I) act[(int64_t)p * I + n] = unit(vals[i], vals[i + kHalf]);
+      }
+    } else {
+      constexpr int kStride = kMoeThreads + 32;                // pad: spreads banks
+#pragma unroll
+      for (int i = 0; i < kIter; ++i)
+        red[i * kStride + tid] = active ? segment_dot<kMx>(lut, cw[i], am[i], sb[i], xf, xr) : 0.f;
+      lds_barrier();
+      // each row's segments by L threads (8 where the workgroup has them),
+      // then an L-lane sum; the totals go through LDS to the output columns
+      const int L = 8 * R <= NT ? 8 : 1;
+      const int rr = L == 8 ? tid >> 3 : tid, k = L == 8 ? tid & 7 : 0;
+      float v = 0.f;
+      if (rr < R) {
+        const int gg = rr % G, ii = rr / G;                    // weight row wrow(gg, ii)
+        const float* src = red + ii * kStride + gg * S;
+        for (int j = k; j < S; j += L) v += src[j];
+      }
+      if (L == 8) v = group_sum_last(v, 8);                    // in every lane of the group
+      lds_barrier();                                           // every partial read
+      if (rr < R && k == 0) red[rr] = v;
+      lds_barrier();
+      if (tid < Rout && n0 + tid < I)
+        act[(int64_t)p * I + n0 + tid] =
+            kMx ? unit(red[2 * tid] + bv[0], red[2 * tid + 1] + bv[1])
+                : unit(red[tid] + bv[0], red[tid + Rout] + bv[1]);
+      lds_barrier();                                           // before the next pair's partials
+    }
+  }
+}
+
+// ---- launch 3: down product and combine ----------------------------------------
+// Workgroup: output rows [n0, n0 + Rb) for every pair, so a token's products
+// meet in LDS.  Wave w takes pairs w, w + waves, ...; its lane groups (W
+// lanes, one or two 32-weight segments a lane) take kR rows each.
+template <bool kMx>
+__device__ __forceinline__ float segment_dot_f32(const LutT* lut, u32x4 c, float am, uint32_t sb,
+                                                 const f32x4 (&xv)[8]) {
+  float acc = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t d = c[w];
+    float q[8];
+    if constexpr (kMx) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const f32x2 v = e2m1_pair_f32(d, b);
+        q[2 * b] = v.x;
+        q[2 * b + 1] = v.y;
+      }
+    } else {
+      nf4_pairs8(lut, d, q);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc = __builtin_fmaf(q[j], xv[2 * w + j / 4][j % 4], acc);
+  }
+  if constexpr (kMx) return e8m0_apply(acc, sb);
+  else return acc * am;
+}
+
+template <bool kMx, int kR, int kSeg>
+__global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
+    const int32_t* __restrict__ ids, const float* __restrict__ act,
+    const uint8_t* __restrict__ codes, const void* __restrict__ scl, int I, int H, int topk,
+    int rows, const float* __restrict__ weights, const uint16_t* __restrict__ bias,
+    uint16_t* __restrict__ y) {
+  __shared__ __attribute__((aligned(4096))) LutT lut[kMx ? 1 : kLutN];
+  extern __shared__ float ys[];                            // [P][Rb]
+
+  const int P = rows * topk;
+  const int S = I >> 5;
+  const int W = kSeg == 2 ? kWave : (S > 1 ? 1 << (32 - __builtin_clz(S - 1)) : 1);
+  const int waves = min(P, kDownWaves);
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int Rb = (kWave / W) * kR;
+  const int n0 = blockIdx.x * Rb;
+  const int g = lane / W, s = lane - g * W;
+  bool active[kSeg];
+  int s_cl[kSeg];
+#pragma unroll
+  for (int j = 0; j < kSeg; ++j) {
+    active[j] = s + kWave * j < S;
+    s_cl[j] = active[j] ? s + kWave * j : 0;
+  }
+  const int idl = lane < P ? ids[lane] : -1;
+  if constexpr (!kMx) {
+    lut_init(lut, tid, kWave * waves);
+    lds_barrier();
+  }
+  for (int p = wave; p < P; p += waves) {
+    const int e = __builtin_amdgcn_readlane(idl, p);
+    float tot[kR];
+#pragma unroll
+    for (int i = 0; i < kR; ++i) tot[i] = 0.f;
+    if (e >= 0) {                                          // uniform; no expert: adds nothing
+      u32x4 cw[kR][kSeg];
+      float am[kR][kSeg], bv[kR];
+      uint32_t sb[kR][kSeg];
+      f32x4 xv[kSeg][8];
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        const int n = min(n0 + g * kR + i, H - 1);
+        const size_t row = (size_t)e * H + n;
+#pragma unroll
+        for (int j = 0; j < kSeg; ++j) {
+          cw[i][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+              codes + row * (size_t)(I / 2) + (size_t)s_cl[j] * 16));
+          if constexpr (kMx) {
+            sb[i][j] = (uint32_t)static_cast<const uint8_t*>(scl)[row * (size_t)(I / 32) + s_cl[j]];
+            am[i][j] = 0.f;
+          } else {
+            am[i][j] = static_cast<const float*>(scl)[row * (size_t)(I / 64) + s_cl[j] / 2];
+            sb[i][j] = 0u;
+          }
+        }
+        bv[i] = bias ? bf16_at(bias, row) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kSeg; ++j) {
+        const f32x4* ap =
+            reinterpret_cast<const f32x4*>(act + (int64_t)p * I + (int64_t)s_cl[j] * 32);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) xv[j][v] = ap[v];
+      }
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        float part = 0.f;
+#pragma unroll
+        for (int j = 0; j < kSeg; ++j)
+          if (active[j]) part += segment_dot_f32<kMx>(lut, cw[i][j], am[i][j], sb[i][j], xv[j]);
+        tot[i] = group_sum_last(part, W) + bv[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kR; ++i)
+      if (s == W - 1) ys[p * Rb + g * kR + i] = tot[i];
+  }
+  lds_barrier();
+  // thread (t, r) sums its token's slots in order
+  for (int idx = tid; idx < rows * Rb; idx += kWave * waves) {
+    const int t = idx / Rb, r = idx - t * Rb;
+    const int n = n0 + r;
+    if (n >= H) continue;
+    float acc = 0.f;
+    for (int sl = 0; sl < topk; ++sl) {
+      const int p = t * topk + sl;
+      acc = __builtin_fmaf(weights[p], ys[p * Rb + r], acc);
+    }
+    y[(int64_t)t * H + n] = f32_to_bf16_bits(acc);
+  }
+}
+
+// ---- host -------------------------------------------------------------------------
+struct MoeSpace {                            // byte offsets into the workspace
+  int64_t logits, ids, weights, act, bytes;
+};
+static MoeSpace moe_space(const gq_moe_layer& l, int rows) {
+  auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  const int64_t P = (int64_t)rows * l.topk;
+  MoeSpace m{};
+  m.ids = up((int64_t)rows * l.num_experts * 4);
+  m.weights = m.ids + up(P * 4);
+  m.act = m.weights + up(P * 4);
+  m.bytes = m.act + up(P * l.inner * 4);
+  return m;
+}
+
+static int layer_checks(const gq_moe_layer* l) {
+  if (!l) return kInvalid;
+  if (l->format != GQ_NF4 && l->format != GQ_MXFP4) return kInvalid;
+  const int blk = l->format == GQ_NF4 ? 64 : 32;
+  if (l->num_experts < 1 || l->topk < 1 || l->topk > l->num_experts) return kInvalid;
+  if (l->hidden < 1 || l->hidden % blk || l->inner < 1 || l->inner % blk) return kInvalid;
+  if (l->format == GQ_MXFP4 &&
+      !(l->limit >= 0.f && l->limit < 3.4e38f && l->alpha > -3.4e38f && l->alpha < 3.4e38f))
+    return kInvalid;
+  if (!l->router_weight || !l->gate_up_codes || !l->gate_up_scales || !l->down_codes ||
+      !l->down_scales)
+    return kInvalid;
+  if (!aligned16(l->router_weight) || !aligned16(l->gate_up_codes) || !aligned16(l->down_codes))
+    return kInvalid;
+  if (l->format == GQ_NF4 && (!aligned4(l->gate_up_scales) || !aligned4(l->down_scales)))
+    return kInvalid;
+  for (const uint16_t* b : {l->router_bias, l->gate_up_bias, l->down_bias})
+    if (reinterpret_cast<uintptr_t>(b) & 1u) return kInvalid;
+  if (l->num_experts > kMoeMaxExperts || l->topk > kMoeMaxPairs || l->hidden > kMoeMaxHidden ||
+      l->inner > kMoeMaxInner)
+    return kNotSupported;
+  return kOk;
+}
+
+template <bool kMx, int kIter, int C>
+static void launch_gate_up(dim3 grid, int NT, bool wave_rows, hipStream_t stream,
+                           const gq_moe_layer& l, const float* logits, const uint16_t* x,
+                           int x_stride, int rows, int32_t* ids, float* w, float* act) {
+  if (wave_rows)
+    hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, true, C>), grid, dim3(NT), 0, stream,
+                       logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden, l.inner,
+                       l.num_experts, x_stride, l.topk, rows, l.gate_up_bias, l.alpha, l.limit,
+                       l.renormalize, ids, w, act);
+  else
+    hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, false, C>), grid, dim3(NT), 0, stream,
+                       logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden, l.inner,
+                       l.num_experts, x_stride, l.topk, rows, l.gate_up_bias, l.alpha, l.limit,
+                       l.renormalize, ids, w, act);
+}
+
+template <bool kMx, int C>
+static void gate_up(hipStream_t stream, const gq_moe_layer& l, const float* logits,
+                    const uint16_t* x, int x_stride, int rows, int32_t* ids, float* w,
+                    float* act) {
+  const int N = 2 * l.inner, P = rows * l.topk;
+  int S, W, G, NT;
+  segment_layout(l.hidden, S, W, G, NT);
+  // rows per thread as in the decode GEMV: the largest count that still
+  // gives about eight workgroups per CU (two where rows are reduced in LDS)
+  const int64_t want = S <= kWave ? 2048 : 512;
+  int iter = 8;
+  while (iter > 2 && (int64_t)((N + G * iter - 1) / (G * iter)) * P < want) iter >>= 1;
+  const dim3 grid((N + G * iter - 1) / (G * iter), (unsigned)P);
+  const bool wr = S <= kWave;
+  if (iter == 8) launch_gate_up<kMx, 8, C>(grid, NT, wr, stream, l, logits, x, x_stride, rows, ids, w, act);
+  else if (iter == 4) launch_gate_up<kMx, 4, C>(grid, NT, wr, stream, l, logits, x, x_stride, rows, ids, w, act);
+  else launch_gate_up<kMx, 2, C>(grid, NT, wr, stream, l, logits, x, x_stride, rows, ids, w, act);
+}
+
+template <bool kMx, int kR, int kSeg>
+static void launch_down(hipStream_t stream, const gq_moe_layer& l, int W, int rows,
+                        const int32_t* ids, const float* w, const float* act, uint16_t* y) {
+  const int P = rows * l.topk, Rb = (kWave / W) * kR;
+  hipLaunchKernelGGL((moe_down_kernel<kMx, kR, kSeg>), dim3((l.hidden + Rb - 1) / Rb),
+                     dim3(kWave * std::min(P, kDownWaves)), (size_t)P * Rb * 4, stream, ids, act,
+                     l.down_codes, l.down_scales, l.inner, l.hidden, l.topk, rows, w, l.down_bias,
+                     y);
+}
+
+template <bool kMx>
+static void moe_decode(hipStream_t stream, const gq_moe_layer& l, const uint16_t* x, int x_stride,
+                       int rows, char* ws, uint16_t* y) {
+  const MoeSpace m = moe_space(l, rows);
+  float* logits = reinterpret_cast<float*>(ws);
+  int32_t* ids = reinterpret_cast<int32_t*>(ws + m.ids);
+  float* w = reinterpret_cast<float*>(ws + m.weights);
+  float* act = reinterpret_cast<float*>(ws + m.act);
+  if (rows == 1)
+    hipLaunchKernelGGL(moe_logits_kernel<1>, dim3(l.num_experts), dim3(kMoeThreads), 0, stream, x,
+                       l.router_weight, l.hidden, x_stride, rows, l.num_experts, l.router_bias,
+                       logits);
+  else
+    hipLaunchKernelGGL(moe_logits_kernel<kMoeMaxRows>, dim3(l.num_experts), dim3(kMoeThreads), 0,
+                       stream, x, l.router_weight, l.hidden, x_stride, rows, l.num_experts,
+                       l.router_bias, logits);
+  if (l.num_experts <= 128) gate_up<kMx, 2>(stream, l, logits, x, x_stride, rows, ids, w, act);
+  else gate_up<kMx, 8>(stream, l, logits, x, x_stride, rows, ids, w, act);
+  int S, W, G, NT;
+  segment_layout(l.inner, S, W, G, NT);
+  if (S > kWave) launch_down<kMx, 4, 2>(stream, l, kWave, rows, ids, w, act, y);
+  else launch_down<kMx, 2, 1>(stream, l, W, rows, ids, w, act, y);
+}
+
+}  // namespace gq
+
+extern "C" int64_t gq_moe_decode_workspace(const gq_moe_layer* layer, int32_t rows) {
+  using namespace gq;
+  if (layer_checks(layer) != kOk || rows < 0 || rows > kMoeMaxRows ||
+      (int64_t)rows * layer->topk > kMoeMaxPairs)
+    return -1;
+  return moe_space(*layer, rows).bytes;
+}
+
+extern "C" int gq_moe_decode(const gq_moe_layer* layer, const uint16_t* x, int32_t rows,
+                             int64_t x_stride, void* workspace, int64_t workspace_bytes,
+                             uint16_t* y, hipStream_t stream) {
+  using namespace gq;
+  const int st = layer_checks(layer);
+  if (st != kOk) return st;
+  if (rows < 0 || x_stride < layer->hidden || x_stride % 8) return kInvalid;
+  if (rows > kMoeMaxRows || (int64_t)rows * layer->topk > kMoeMaxPairs || x_stride > INT32_MAX)
+    return kNotSupported;
+  if (rows == 0) return kOk;
+  if (!x || !y || !workspace || !aligned16(x) || !aligned16(workspace) ||
+      (reinterpret_cast<uintptr_t>(y) & 1u))
+    return kInvalid;
+  if (workspace_bytes < moe_space(*layer, rows).bytes) return kInvalid;
+  char* ws = static_cast<char*>(workspace);
+  if (layer->format == GQ_MXFP4)
+    moe_decode<true>(stream, *layer, x, (int)x_stride, rows, ws, y);
+  else
+    moe_decode<false>(stream, *layer, x, (int)x_stride, rows, ws, y);
+  return launch_status();
+}

@@ -507,6 +507,62 @@ int gq_moe_topk_backward(const float* d_weights, const void* logits, int32_t dty
                          int32_t num_experts, int64_t stride, const int32_t* topk_ids,
                          int32_t topk, int32_t renormalize, void* d_logits, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A whole mixture-of-experts layer for a few tokens: router product,
+ * selection, the experts' gated products and the weighted combine.
+ *
+ *   z = x Wr^T + br;   e_s, w_s as gq_moe_topk(z, topk, renormalize)
+ *   a_s = unit(Wgu[e_s] x + bgu[e_s]);   y = bf16(sum_s w_s (Wd[e_s] a_s + bd[e_s]))
+ *
+ * unit: GQ_NF4 SwiGLU (gate rows [0, I), up rows [I, 2I)), GQ_MXFP4 the
+ * clamped gated unit (gate row 2j, up row 2j + 1; alpha, limit), as in
+ * gq_nf4_grouped_gemv_swiglu and gq_mxfp4_grouped_gemv_swiglu.  float32
+ * throughout between the bf16 input and the bf16 output, the gated products
+ * included.  A NaN of a token reaches that token's output (and no other).
+ */
+enum { GQ_NF4 = 0, GQ_MXFP4 = 1 };
+
+typedef struct gq_moe_layer {
+  int32_t format;                 /* GQ_NF4 or GQ_MXFP4 */
+  int32_t num_experts;            /* E */
+  int32_t topk;
+  int32_t hidden;                 /* H */
+  int32_t inner;                  /* I */
+  int32_t renormalize;            /* weights: softmax over the chosen logits, else over all */
+  float alpha, limit;             /* GQ_MXFP4's unit */
+  const uint16_t* router_weight;  /* bf16 [E, H] */
+  const uint16_t* router_bias;    /* bf16 [E] or NULL */
+  const uint8_t* gate_up_codes;   /* the E experts' [2I, H] as the other entry points take them */
+  const void* gate_up_scales;
+  const uint16_t* gate_up_bias;   /* bf16 [E, 2I] or NULL */
+  const uint8_t* down_codes;      /* [H, I] */
+  const void* down_scales;
+  const uint16_t* down_bias;      /* bf16 [E, H] or NULL */
+} gq_moe_layer;
+
+/*
+ * gq_moe_decode_workspace: bytes of device memory that gq_moe_decode needs
+ * for `rows` tokens (16-byte aligned); -1 if the layer or rows are not ones
+ * that gq_moe_decode takes.  The workspace carries nothing from one call to
+ * the next and needs no clearing; two calls that may run at the same time
+ * need one each.
+ *
+ * gq_moe_decode:
+ *   layer      read during the call only (the arrays it names stay the caller's)
+ *   x          uint16 bf16 [rows, H], row stride x_stride elements
+ *   y          uint16 bf16 [rows, H]
+ * InvalidValue: null layer or array (biases may be NULL), unknown format,
+ *   topk outside [1, E], H or I not a positive multiple of 64 (GQ_NF4) / 32
+ *   (GQ_MXFP4), alpha or limit not finite or limit < 0 (GQ_MXFP4), rows < 0,
+ *   x_stride < H or % 8, workspace too small, misaligned pointers.
+ * NotSupported: rows > 8, rows*topk > 64, E > 512, H > 8192, I > 4096,
+ *   x_stride > 2^31 - 1.
+ * rows == 0 enqueues nothing.
+ */
+int64_t gq_moe_decode_workspace(const gq_moe_layer* layer, int32_t rows);
+int gq_moe_decode(const gq_moe_layer* layer, const uint16_t* x, int32_t rows, int64_t x_stride,
+                  void* workspace, int64_t workspace_bytes, uint16_t* y, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -66,6 +66,54 @@ def test_moe_topk_backward_rejects(lib):
     assert call(rows=0) == 0
 
 
+def _layer(**kw):
+    """A layer struct of fake pointers (topk 4 of 32 MXFP4 experts)."""
+    a = dict(format=1, num_experts=32, topk=4, hidden=2880, inner=2880, renormalize=1, alpha=1.702,
+             limit=7.0, router_weight=0x1000, router_bias=None, gate_up_codes=0x1000,
+             gate_up_scales=0x1000, gate_up_bias=None, down_codes=0x1000, down_scales=0x1000,
+             down_bias=None)
+    a.update(kw)
+    return gq._LayerStruct(**a)
+
+
+def test_moe_decode_rejects(lib):
+    def call(x=F, rows=1, xs=2880, ws=F, nbytes=1 << 30, y=F, **kw):
+        return lib.gq_moe_decode(ctypes.byref(_layer(**kw)), x, rows, xs, ws, nbytes, y, None)
+
+    nan, inf = float("nan"), float("inf")
+    for bad in (dict(x=NULL), dict(y=NULL), dict(ws=NULL), dict(rows=-1), dict(xs=2879),
+                dict(xs=2884), dict(x=F8), dict(ws=F8), dict(y=F1), dict(nbytes=100),
+                dict(format=2), dict(num_experts=0), dict(topk=0), dict(topk=33), dict(hidden=0),
+                dict(hidden=2896, xs=2896), dict(inner=2896), dict(inner=-32), dict(alpha=nan),
+                dict(alpha=inf), dict(limit=-1.0), dict(limit=inf), dict(limit=nan),
+                dict(router_weight=None), dict(gate_up_codes=None), dict(gate_up_scales=None),
+                dict(down_codes=None), dict(down_scales=None), dict(router_weight=0x1008),
+                dict(gate_up_codes=0x1004), dict(down_codes=0x1008), dict(router_bias=0x1001),
+                dict(gate_up_bias=0x1001), dict(down_bias=0x1001)):
+        assert call(**bad) == INVALID, bad
+    assert call(format=0, inner=2912) == INVALID              # NF4: multiples of 64
+    assert call(format=0, gate_up_scales=0x1002) == INVALID
+    for bad in (dict(rows=9), dict(rows=8, topk=9), dict(num_experts=513), dict(inner=4128),
+                dict(hidden=8224, xs=8224), dict(xs=1 << 31)):
+        assert call(**bad) == NOT_SUPPORTED, bad
+    assert call(rows=0, x=NULL, y=NULL, ws=NULL) == 0
+    assert lib.gq_moe_decode(None, F, 1, 2880, F, 1 << 30, F, None) == INVALID
+
+
+def test_moe_decode_workspace_sizes(lib):
+    size = lambda rows, **kw: lib.gq_moe_decode_workspace(ctypes.byref(_layer(**kw)), rows)  # noqa: E731
+    assert size(0) == 0
+    assert size(1) >= 4 * (32 + 2 * 4 + 4 * 2880)
+    assert size(8) > size(1)
+    for bad in (dict(rows=-1), dict(rows=9), dict(rows=8, topk=9), dict(rows=1, hidden=100),
+                dict(rows=1, num_experts=600)):
+        assert size(**bad) == -1, bad
+    assert lib.gq_moe_decode_workspace(None, 1) == -1
+    # a workspace one byte short is refused before anything is enqueued
+    need = size(2)
+    assert lib.gq_moe_decode(ctypes.byref(_layer()), F, 2, 2880, F, need - 1, F, None) == INVALID
+
+
 def test_binding_refuses_host_tensors_and_wrong_types(lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device tensor"):
