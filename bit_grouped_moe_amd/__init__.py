@@ -27,7 +27,9 @@ __all__ = [
     "gq_mxfp4_grouped_gemm_scaled_swiglu_split",
     "gq_mxfp4_grouped_gemv_down_combine", "gq_nf4_grouped_gemv_host", "gq_mxfp4_grouped_gemv_host",
     "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward", "gq_moe_layer",
-    "gq_moe_decode_workspace", "gq_moe_decode",
+    "gq_moe_decode_workspace", "gq_moe_decode", "gq_mxfp4_grouped_gemm_fp4",
+    "gq_mxfp4_grouped_gemm_fp4_swiglu", "gq_mxfp4_grouped_gemv_fp4",
+    "gq_mxfp4_grouped_gemv_fp4_swiglu",
     "OSS_ALPHA", "OSS_LIMIT", "Route",
 ]
 
@@ -46,7 +48,8 @@ EXPORTED_SYMBOLS = (
     "gq_mxfp4_grouped_gemm_scaled_swiglu_split",
     "gq_mxfp4_grouped_gemv_down_combine", "gq_nf4_grouped_gemv_host", "gq_mxfp4_grouped_gemv_host",
     "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward", "gq_moe_decode_workspace",
-    "gq_moe_decode",
+    "gq_moe_decode", "gq_mxfp4_grouped_gemm_fp4", "gq_mxfp4_grouped_gemm_fp4_swiglu",
+    "gq_mxfp4_grouped_gemv_fp4", "gq_mxfp4_grouped_gemv_fp4_swiglu",
 )
 
 _i32, _i64, _p, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -97,6 +100,15 @@ _SIGNATURES = {
     "gq_moe_topk": (ctypes.c_int, [_p, _i32, _i64, _i32, _i64, _i32, _i32, _p, _p, _p]),
     "gq_moe_topk_backward": (ctypes.c_int, [_p, _p, _i32, _i64, _i32, _i64, _p, _i32, _i32, _p,
                                             _p]),
+    "gq_mxfp4_grouped_gemm_fp4": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p, _i32, _i32, _i32, _p,
+                                                 _p, _p, _p, _p, _i32, _i32, _p, _p]),
+    "gq_mxfp4_grouped_gemm_fp4_swiglu": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p, _i32, _i32,
+                                                        _i32, _f32, _f32, _p, _p, _p, _p, _i32,
+                                                        _i32, _p, _p]),
+    "gq_mxfp4_grouped_gemv_fp4": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p, _i32, _i32, _p, _i32,
+                                                 _p, _p, _p]),
+    "gq_mxfp4_grouped_gemv_fp4_swiglu": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p, _i32, _i32,
+                                                        _p, _i32, _f32, _f32, _p, _p]),
     "gq_moe_decode_workspace": (_i64, [_p, _i32]),
     "gq_moe_decode": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _i64, _p, _p]),
 }
@@ -748,6 +760,80 @@ def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
     _on(dev, lib.gq_mxfp4_quantize, "gq_mxfp4_quantize", x.data_ptr(), code, rows, K, stride,
         blocks.data_ptr(), scales.data_ptr(), None if values is None else values.data_ptr())
     return (blocks, scales) if values is None else (blocks, scales, values)
+
+
+# ---- MXFP4 x MXFP4 products --------------------------------------------------------
+def _mx_pair(x, blocks, scales, unit):
+    """Checks of an MXFP4 x MXFP4 product: (x blocks, x scales, rows, E, N, K)."""
+    xb, xs = x[0], x[1]
+    _dev(xb, "x blocks", torch.uint8, 3)
+    _dev(xs, "x scales", torch.uint8, 2)
+    E, N, K = _mx_bank(blocks, scales)
+    rows = xb.shape[0]
+    if tuple(xb.shape) != (rows, K // 32, 16) or tuple(xs.shape) != (rows, K // 32):
+        raise ValueError(f"x must be (blocks [rows, {K // 32}, 16], scales [rows, {K // 32}]) as "
+                         "gq_mxfp4_quantize returns them")
+    if unit and N % 2:
+        raise ValueError("the gate_up width is odd")
+    _beside(xb.device, x_scales=xs, blocks=blocks, scales=scales)
+    return xb, xs, rows, E, N, K
+
+
+def _fp4_gemm(what, x, blocks, scales, route, middle, N_out, pair_scale, out):
+    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, N_out is None)
+    if route.rows != rows or route.num_experts != E:
+        raise ValueError("x, blocks and route disagree")
+    dev = xb.device
+    P = rows * route.topk
+    out = _out(out, P, N // 2 if N_out is None else N, dev)
+    _beside(dev, out=out, pair_scale=pair_scale, route=route.sorted_pairs)
+    args = [xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(), scales.data_ptr(), E, N,
+            route.topk, *middle(P), *_route_ptrs(route), out.data_ptr()]
+    _on(dev, getattr(load_library(), what), what, *args)
+    return out
+
+
+def gq_mxfp4_grouped_gemm_fp4(x, blocks, scales, route, pair_scale=None, out=None):
+    """Prefill grouped GEMM of MXFP4 activations with MXFP4 experts; ``x`` =
+    gq_mxfp4_quantize(activations [rows, K]).  Returns bf16 [rows*topk, N]."""
+    return _fp4_gemm("gq_mxfp4_grouped_gemm_fp4", x, blocks, scales, route,
+                     lambda P: (_ptr(_scale(pair_scale, P)),), True, pair_scale, out)
+
+
+def gq_mxfp4_grouped_gemm_fp4_swiglu(x, blocks, scales, route, alpha=OSS_ALPHA, limit=OSS_LIMIT,
+                                     out=None):
+    """gq_mxfp4_grouped_gemm_fp4 on gate_up experts [E, 2I, K] (gate row 2j,
+    up row 2j + 1) with gpt-oss's gated unit: bf16 [rows*topk, I]."""
+    return _fp4_gemm("gq_mxfp4_grouped_gemm_fp4_swiglu", x, blocks, scales, route,
+                     lambda P: (float(alpha), float(limit)), None, None, out)
+
+
+def _fp4_gemv(what, x, blocks, scales, topk_ids, middle, unit, pair_scale, out):
+    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit)
+    dev = xb.device
+    _dev(topk_ids, "topk_ids", torch.int32, 2)
+    P = _gemv_pairs(topk_ids, rows)
+    out = _out(out, P, N // 2 if unit else N, dev)
+    _beside(dev, out=out, pair_scale=pair_scale, topk_ids=topk_ids)
+    _on(dev, getattr(load_library(), what), what, xb.data_ptr(), xs.data_ptr(), rows, K,
+        blocks.data_ptr(), scales.data_ptr(), E, N, topk_ids.data_ptr(), topk_ids.shape[1],
+        *middle(P), out.data_ptr())
+    return out
+
+
+def gq_mxfp4_grouped_gemv_fp4(x, blocks, scales, topk_ids, pair_scale=None, out=None):
+    """Decode-time product (<= 256 pairs) of MXFP4 activations with MXFP4
+    experts; ``x`` = gq_mxfp4_quantize(activations).  Returns bf16 [rows*topk, N]."""
+    return _fp4_gemv("gq_mxfp4_grouped_gemv_fp4", x, blocks, scales, topk_ids,
+                     lambda P: (_ptr(_scale(pair_scale, P)),), False, pair_scale, out)
+
+
+def gq_mxfp4_grouped_gemv_fp4_swiglu(x, blocks, scales, topk_ids, alpha=OSS_ALPHA,
+                                     limit=OSS_LIMIT, out=None):
+    """gq_mxfp4_grouped_gemv_fp4 on gate_up experts with gpt-oss's gated unit:
+    bf16 [rows*topk, I]."""
+    return _fp4_gemv("gq_mxfp4_grouped_gemv_fp4_swiglu", x, blocks, scales, topk_ids,
+                     lambda P: (float(alpha), float(limit)), True, None, out)
 
 
 # ---- expert routing --------------------------------------------------------------

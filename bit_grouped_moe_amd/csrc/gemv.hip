@@ -57,13 +57,22 @@ constexpr int kGemvMaxK = 8192;     // 256 segments of 32 weights
 // [n0, n0 + R/2) and the gate and up rows of each.  kHostBank: the same code
 // for a bank in pinned host memory (a separate instance, so that profiles
 // keep the host-link launches apart from the HBM ones).
-template <bool kMx, int kIter, bool kWaveRows, int kAct, bool kHostBank = false>
+//
+// kXq (MXFP4 weights): the activations are MXFP4 too, x the blocks (row
+// stride x_stride bytes / 2, i.e. K / 4) and x_scales the scale bytes [rows,
+// K / 32].  A lane's segment is one block: 16 bytes and a scale instead of
+// 64 bytes, turned into the same bf16 pairs (exact), and the two scales are
+// applied to the segment's sum together (the sum of 32 products of e2m1
+// values is exact, so nothing rounds before the segments are added).
+template <bool kMx, int kIter, bool kWaveRows, int kAct, bool kHostBank = false, bool kXq = false>
 __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
     const int32_t* __restrict__ ids, const uint16_t* __restrict__ x,
     const uint8_t* __restrict__ codes, const void* __restrict__ scl, int K, int N, int E,
     int x_stride, int topk, int P, const float* __restrict__ pair_scale,
-    uint16_t* __restrict__ out, float alpha, float limit) {
+    uint16_t* __restrict__ out, float alpha, float limit,
+    const uint8_t* __restrict__ x_scales) {
   constexpr bool kGlu = kAct != 0;
+  static_assert(!kXq || kMx, "MXFP4 activations go with MXFP4 weights");
   __shared__ __attribute__((aligned(4096))) LutT lut[kLutN];
   __shared__ float red[kWaveRows ? 1 : kIter * (kGemvMaxThreads + 32)];
 
@@ -121,7 +130,16 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
     idl[c] = (kWave * c < P && q < P) ? ids[q] : -1;
   }
   u32x4 xr[4];
-  {
+  uint32_t sx = 0u;                                 // kXq: the block's scale byte
+  auto load_xq = [&](int p) {                       // codes in xr[0], expanded by compute_pair
+    const int64_t row = p / topk;
+    const int sg = active ? s : 0;
+    xr[0] = *reinterpret_cast<const u32x4*>(x + row * x_stride + sg * 8);
+    sx = (uint32_t)x_scales[row * (K / 32) + sg];
+  };
+  if constexpr (kXq) {
+    load_xq(p0);
+  } else {
     const u32x4* xp =
         reinterpret_cast<const u32x4*>(x + (int64_t)(p0 / topk) * x_stride + (active ? s : 0) * 32);
 #pragma unroll
@@ -190,7 +208,9 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
   // its segment group; otherwise thread r < R holds row r's total ----
   float vals[kWaveRows ? kIter : 1];
   auto act_pair = [&](float gate, float up) {
-    if constexpr (kAct == 2) {
+    if constexpr (kAct == 2 && kXq) {
+      return clamped_unit(gate, up, alpha, limit);
+    } else if constexpr (kAct == 2) {
       const float gc = fminf(gate, limit);
       const float uc = fminf(fmaxf(up, -limit), limit);
       return gc * sigmoid_f32(alpha * gc) * (uc + 1.0f);
@@ -198,7 +218,23 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
       return silu_f32(gate) * up;
     }
   };
+  auto row_dot = [&](int i, const float (&xf)[32]) {
+    if constexpr (kXq) {
+      const float d = segment_dot<true>(lut, cw[i], 0.f, 127u, xf, xr);
+      const float v = __builtin_amdgcn_ldexpf(d, (int)(sb[i] + sx) - 254);
+      return sb[i] == 255u || sx == 255u ? __uint_as_float(0x7FC00000u) : v;
+    } else {
+      return segment_dot<kMx>(lut, cw[i], am[i], sb[i], xf, xr);
+    }
+  };
   auto compute_pair = [&]() {
+    if constexpr (kXq) {
+      const u32x4 q = xr[0];
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        xr[v] = u32x4{e2m1_pair_bf16_scaled(q[v], 0, 1.0f), e2m1_pair_bf16_scaled(q[v], 1, 1.0f),
+                      e2m1_pair_bf16_scaled(q[v], 2, 1.0f), e2m1_pair_bf16_scaled(q[v], 3, 1.0f)};
+    }
     float xf[32];
 #pragma unroll
     for (int v = 0; v < 4; ++v)
@@ -210,7 +246,7 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
     if constexpr (kWaveRows) {
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
-        const float part = active ? segment_dot<kMx>(lut, cw[i], am[i], sb[i], xf, xr) : 0.f;
+        const float part = active ? row_dot(i, xf) : 0.f;
         vals[i] = group_sum_last(part, W);                     // total on lane s == W-1
       }
       if constexpr (kGlu) {
@@ -221,7 +257,7 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
       constexpr int kStride = kGemvMaxThreads + 32;            // pad: spreads banks
 #pragma unroll
       for (int i = 0; i < kIter; ++i)
-        red[i * kStride + tid] = active ? segment_dot<kMx>(lut, cw[i], am[i], sb[i], xf, xr) : 0.f;
+        red[i * kStride + tid] = active ? row_dot(i, xf) : 0.f;
       lds_barrier();
       vals[0] = 0.f;
       bool unit_done = false;                // the gated unit already applied (uniform)
@@ -321,38 +357,43 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
     while (m) {
       const int p = kWave * c + __builtin_ctzll(m);
       m &= m - 1ull;
-      const u32x4* xp = reinterpret_cast<const u32x4*>(x + (int64_t)(p / topk) * x_stride +
-                                                        (active ? s : 0) * 32);
+      if constexpr (kXq) {
+        load_xq(p);
+      } else {
+        const u32x4* xp = reinterpret_cast<const u32x4*>(x + (int64_t)(p / topk) * x_stride +
+                                                          (active ? s : 0) * 32);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) xr[v] = xp[v];
+        for (int v = 0; v < 4; ++v) xr[v] = xp[v];
+      }
       if (!dropped) compute_pair();          // a dropped pair stores zeros
       store_pair(p);
     }
   }
 }
 
-template <bool kMx, int kIter, int kAct, bool kHostBank>
+template <bool kMx, int kIter, int kAct, bool kHostBank, bool kXq>
 static void launch_gemv_iter(dim3 grid, int NT, bool wave_rows, hipStream_t stream,
                              const uint16_t* x, int x_stride, int K, const uint8_t* codes,
                              const void* scl, int N, int E, const int32_t* ids, int topk, int P,
-                             const float* pair_scale, uint16_t* out, float alpha, float limit) {
+                             const float* pair_scale, uint16_t* out, float alpha, float limit,
+                             const uint8_t* xs) {
   if (wave_rows)
-    hipLaunchKernelGGL((grouped_gemv_kernel<kMx, kIter, true, kAct, kHostBank>), grid, dim3(NT),
-                       0, stream,
-                       ids, x, codes, scl, K, N, E, x_stride, topk, P, pair_scale, out, alpha,
-                       limit);
+    hipLaunchKernelGGL((grouped_gemv_kernel<kMx, kIter, true, kAct, kHostBank, kXq>), grid,
+                       dim3(NT), 0, stream, ids, x, codes, scl, K, N, E, x_stride, topk, P,
+                       pair_scale, out, alpha, limit, xs);
   else
-    hipLaunchKernelGGL((grouped_gemv_kernel<kMx, kIter, false, kAct, kHostBank>), grid, dim3(NT),
-                       0, stream,
-                       ids, x, codes, scl, K, N, E, x_stride, topk, P, pair_scale, out, alpha,
-                       limit);
+    hipLaunchKernelGGL((grouped_gemv_kernel<kMx, kIter, false, kAct, kHostBank, kXq>), grid,
+                       dim3(NT), 0, stream, ids, x, codes, scl, K, N, E, x_stride, topk, P,
+                       pair_scale, out, alpha, limit, xs);
 }
 
-template <bool kMx, int kAct, bool kHostBank = false>
+template <bool kMx, int kAct, bool kHostBank = false, bool kXq = false>
 static int launch_gemv(const uint16_t* x, int32_t rows, int32_t K, int64_t x_stride,
                        const uint8_t* codes, const void* scl, int32_t E, int32_t N,
                        const int32_t* ids, int32_t topk, const float* pair_scale, uint16_t* out,
-                       hipStream_t stream, float alpha = 0.f, float limit = 0.f) {
+                       hipStream_t stream, float alpha = 0.f, float limit = 0.f,
+                       const uint8_t* x_scales = nullptr) {
+  if (kXq && !x_scales) return kInvalid;
   if (!x || !codes || !scl || !ids || !out) return kInvalid;
   if (rows < 1 || topk < 1 || E < 1 || N < 1 || K <= 0) return kInvalid;
   if (K % (kMx ? 32 : 64)) return kInvalid;
@@ -360,7 +401,7 @@ static int launch_gemv(const uint16_t* x, int32_t rows, int32_t K, int64_t x_str
   if (kAct == 2 && !(limit >= 0.f && limit < 3.4e38f && alpha == alpha && alpha > -3.4e38f &&
                      alpha < 3.4e38f))
     return kInvalid;                                       // finite alpha, limit >= 0
-  if (x_stride < K || x_stride % 8) return kInvalid;
+  if (!kXq && (x_stride < K || x_stride % 8)) return kInvalid;
   if (!aligned16(x) || !aligned16(codes) || !aligned4(ids) || !aligned4(out)) return kInvalid;
   if (!kMx && !aligned4(scl)) return kInvalid;
   if (pair_scale && !aligned4(pair_scale)) return kInvalid;
@@ -383,16 +424,19 @@ static int launch_gemv(const uint16_t* x, int32_t rows, int32_t K, int64_t x_str
   const dim3 grid((N + R - 1) / R, (unsigned)P);
   switch (iter) {
     case 8:
-      launch_gemv_iter<kMx, 8, kAct, kHostBank>(grid, NT, S <= kWave, stream, x, (int)x_stride, K, codes, scl,
-                                     N, E, ids, topk, (int)P, pair_scale, out, alpha, limit);
+      launch_gemv_iter<kMx, 8, kAct, kHostBank, kXq>(grid, NT, S <= kWave, stream, x, (int)x_stride, K,
+                                                  codes, scl, N, E, ids, topk, (int)P, pair_scale,
+                                                  out, alpha, limit, x_scales);
       break;
     case 4:
-      launch_gemv_iter<kMx, 4, kAct, kHostBank>(grid, NT, S <= kWave, stream, x, (int)x_stride, K, codes, scl,
-                                     N, E, ids, topk, (int)P, pair_scale, out, alpha, limit);
+      launch_gemv_iter<kMx, 4, kAct, kHostBank, kXq>(grid, NT, S <= kWave, stream, x, (int)x_stride, K,
+                                                  codes, scl, N, E, ids, topk, (int)P, pair_scale,
+                                                  out, alpha, limit, x_scales);
       break;
     default:
-      launch_gemv_iter<kMx, 2, kAct, kHostBank>(grid, NT, S <= kWave, stream, x, (int)x_stride, K, codes, scl,
-                                     N, E, ids, topk, (int)P, pair_scale, out, alpha, limit);
+      launch_gemv_iter<kMx, 2, kAct, kHostBank, kXq>(grid, NT, S <= kWave, stream, x, (int)x_stride, K,
+                                                  codes, scl, N, E, ids, topk, (int)P, pair_scale,
+                                                  out, alpha, limit, x_scales);
       break;
   }
   return launch_status();
@@ -739,4 +783,26 @@ extern "C" int gq_mxfp4_grouped_gemv_swiglu(const uint16_t* x, int32_t rows, int
                                             float limit, uint16_t* act, hipStream_t stream) {
   return gq::launch_gemv<true, 2>(x, rows, K, x_stride, blocks, scales, num_experts, N,
                                   topk_ids, topk, nullptr, act, stream, alpha, limit);
+}
+
+extern "C" int gq_mxfp4_grouped_gemv_fp4(const uint8_t* x_blocks, const uint8_t* x_scales,
+                                         int32_t rows, int32_t K, const uint8_t* blocks,
+                                         const uint8_t* scales, int32_t num_experts, int32_t N,
+                                         const int32_t* topk_ids, int32_t topk,
+                                         const float* pair_scale, uint16_t* out,
+                                         hipStream_t stream) {
+  return gq::launch_gemv<true, 0, false, true>(
+      reinterpret_cast<const uint16_t*>(x_blocks), rows, K, K / 4, blocks, scales, num_experts, N,
+      topk_ids, topk, pair_scale, out, stream, 0.f, 0.f, x_scales);
+}
+
+extern "C" int gq_mxfp4_grouped_gemv_fp4_swiglu(const uint8_t* x_blocks, const uint8_t* x_scales,
+                                                int32_t rows, int32_t K, const uint8_t* blocks,
+                                                const uint8_t* scales, int32_t num_experts,
+                                                int32_t N, const int32_t* topk_ids, int32_t topk,
+                                                float alpha, float limit, uint16_t* act,
+                                                hipStream_t stream) {
+  return gq::launch_gemv<true, 2, false, true>(
+      reinterpret_cast<const uint16_t*>(x_blocks), rows, K, K / 4, blocks, scales, num_experts, N,
+      topk_ids, topk, nullptr, act, stream, alpha, limit, x_scales);
 }

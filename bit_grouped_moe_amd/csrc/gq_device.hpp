@@ -157,6 +157,16 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 // SiLU, z * sigmoid(z), in float32.
 __device__ __forceinline__ float silu_f32(float z) { return z * sigmoid_f32(z); }
 
+// gpt-oss's gated unit of one (gate, up) pair with the gate clamped above at
+// `limit` and the up value clipped to [-limit, limit]; compares and selects
+// keep a NaN, which the minimum and maximum instructions would drop.
+__device__ __forceinline__ float clamped_unit(float gate, float up, float alpha, float limit) {
+  const float gc = gate > limit ? limit : gate;
+  const float hi = up > limit ? limit : up;
+  const float uc = hi < -limit ? -limit : hi;
+  return gc * sigmoid_f32(alpha * gc) * (uc + 1.0f);
+}
+
 // ---- MXFP4 ---------------------------------------------------------------
 // Byte j of a 16-byte block holds element 2j in its low nibble, 2j+1 in its
 // high nibble.  e2m1 -> float32 is exact; the e8m0 factor 2^(s-127) is then

@@ -224,11 +224,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
 
   auto unit = [&](float gate, float up) {
     if constexpr (kMx) {
-      const float gc = fminf(gate, limit);
-      const float uc = fminf(fmaxf(up, -limit), limit);
-      const float a = gc * sigmoid_f32(alpha * gc) * (uc + 1.0f);
-      // the minimum and maximum drop a NaN; the unit does not
-      return gate != gate || up != up ? gate + up : a;
+      return clamped_unit(gate, up, alpha, limit);
     } else {
       return silu_f32(gate) * up;
     }

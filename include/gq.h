@@ -473,6 +473,51 @@ int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, i
                       uint8_t* blocks, uint8_t* scales, uint16_t* values, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * MXFP4 activations times MXFP4 experts, on the e2m1 x e2m1 block-scaled
+ * matrix instruction ([P1] "Which entry point?": native MXFP4 expert math).
+ *
+ *   out[p, n] = bf16( pair_scale[p] * sum_k xq[p/topk, k] * W_{ids[p]}[n, k] )
+ *
+ * x_blocks uint8 [rows, K/32, 16] and x_scales uint8 [rows, K/32] are what
+ * gq_mxfp4_quantize writes; everything else is as for gq_mxfp4_grouped_gemm
+ * (routing from gq_route_sort, dropped pairs' rows zero) and
+ * gq_mxfp4_grouped_gemv (1..8 tokens, topk_ids read directly).  Products of
+ * codes are exact, sums float32, one rounding to bf16.  Scale byte 255 on
+ * either side makes every output that its block enters NaN.
+ * The _swiglu forms apply the clamped gated unit of
+ * gq_mxfp4_grouped_gemv_swiglu (weight rows 2j gate, 2j + 1 up) and write
+ * [rows*topk, N/2]; a NaN passes through the unit.
+ * InvalidValue / NotSupported: as for the named entry points; K % 32, and
+ *   NotSupported: rows*K/2 or N*K/2 >= 2^31 (GEMM), rows*topk > 256 or
+ *   K > 8192 (GEMV).
+ */
+int gq_mxfp4_grouped_gemm_fp4(const uint8_t* x_blocks, const uint8_t* x_scales, int32_t rows,
+                              int32_t K, const uint8_t* blocks, const uint8_t* scales,
+                              int32_t num_experts, int32_t N, int32_t topk,
+                              const float* pair_scale, const int32_t* expert_offsets,
+                              const int32_t* sorted_pairs, const int32_t* tiles,
+                              const int32_t* num_tiles, int32_t max_tiles, int32_t tile_m,
+                              uint16_t* out, hipStream_t stream);
+int gq_mxfp4_grouped_gemm_fp4_swiglu(const uint8_t* x_blocks, const uint8_t* x_scales,
+                                     int32_t rows, int32_t K, const uint8_t* blocks,
+                                     const uint8_t* scales, int32_t num_experts, int32_t N,
+                                     int32_t topk, float alpha, float limit,
+                                     const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                                     const int32_t* tiles, const int32_t* num_tiles,
+                                     int32_t max_tiles, int32_t tile_m, uint16_t* act,
+                                     hipStream_t stream);
+int gq_mxfp4_grouped_gemv_fp4(const uint8_t* x_blocks, const uint8_t* x_scales, int32_t rows,
+                              int32_t K, const uint8_t* blocks, const uint8_t* scales,
+                              int32_t num_experts, int32_t N, const int32_t* topk_ids,
+                              int32_t topk, const float* pair_scale, uint16_t* out,
+                              hipStream_t stream);
+int gq_mxfp4_grouped_gemv_fp4_swiglu(const uint8_t* x_blocks, const uint8_t* x_scales,
+                                     int32_t rows, int32_t K, const uint8_t* blocks,
+                                     const uint8_t* scales, int32_t num_experts, int32_t N,
+                                     const int32_t* topk_ids, int32_t topk, float alpha,
+                                     float limit, uint16_t* act, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Expert routing ([P4] "Functions": the routing tensor [M, top_k] and its
  * weights, which the other entry points take).
  *

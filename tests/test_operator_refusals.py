@@ -66,6 +66,43 @@ def test_moe_topk_backward_rejects(lib):
     assert call(rows=0) == 0
 
 
+def test_fp4_products_reject(lib):
+    nan, inf = float("nan"), float("inf")
+    gemm = dict(x=F, xs=F, rows=2048, K=2880, b=F, s=F, E=32, N=5760, k=4, off=F, sp=F, tl=F, nt=F,
+                mt=32 + 33 + 1, tm=256, out=F)
+    head, tail = "x xs rows K b s E N k".split(), "off sp tl nt mt tm out".split()
+    plain = _caller(lib.gq_mxfp4_grouped_gemm_fp4, head + ["ps"] + tail, dict(gemm, ps=NULL))
+    unit = _caller(lib.gq_mxfp4_grouped_gemm_fp4_swiglu, head + ["al", "li"] + tail,
+                   dict(gemm, al=1.702, li=7.0))
+    for call in (plain, unit):
+        for bad in (dict(x=NULL), dict(xs=NULL), dict(b=NULL), dict(s=NULL), dict(off=NULL),
+                    dict(sp=NULL), dict(tl=NULL), dict(nt=NULL), dict(out=NULL), dict(rows=-1),
+                    dict(K=0), dict(K=2870), dict(N=0), dict(N=5750), dict(E=0), dict(k=0),
+                    dict(mt=64), dict(x=F8), dict(b=F8), dict(out=F8), dict(off=F2), dict(nt=F2)):
+            assert call(**bad) == INVALID, bad
+        assert call(tm=128) == NOT_SUPPORTED
+        assert call(rows=1 << 21, mt=1 << 24) == NOT_SUPPORTED     # 32-bit row offsets
+        assert call(N=1 << 21) == NOT_SUPPORTED                    # 32-bit offsets in an expert
+        assert call(rows=0) == 0
+    for bad in (dict(al=nan), dict(al=inf), dict(li=-1.0), dict(li=nan), dict(li=inf)):
+        assert unit(**bad) == INVALID, bad
+    assert plain(ps=F2) == INVALID
+    gemv = dict(x=F, xs=F, rows=1, K=2880, b=F, s=F, E=32, N=5760, ids=F, k=4, out=F)
+    head = "x xs rows K b s E N ids k".split()
+    plain = _caller(lib.gq_mxfp4_grouped_gemv_fp4, head + ["ps", "out"], dict(gemv, ps=NULL))
+    unit = _caller(lib.gq_mxfp4_grouped_gemv_fp4_swiglu, head + ["al", "li", "out"],
+                   dict(gemv, al=1.702, li=7.0))
+    for call in (plain, unit):
+        for bad in (dict(x=NULL), dict(xs=NULL), dict(b=NULL), dict(s=NULL), dict(ids=NULL),
+                    dict(out=NULL), dict(rows=0), dict(K=0), dict(K=2870), dict(N=0), dict(E=0),
+                    dict(k=0), dict(x=F8), dict(b=F8), dict(ids=F2)):
+            assert call(**bad) == INVALID, bad
+        assert call(rows=65) == NOT_SUPPORTED
+        assert call(K=8224) == NOT_SUPPORTED
+    assert unit(N=5761) == INVALID
+    assert unit(al=nan) == INVALID and unit(li=-1.0) == INVALID
+
+
 def _layer(**kw):
     """A layer struct of fake pointers (topk 4 of 32 MXFP4 experts)."""
     a = dict(format=1, num_experts=32, topk=4, hidden=2880, inner=2880, renormalize=1, alpha=1.702,
