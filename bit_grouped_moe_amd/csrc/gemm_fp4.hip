@@ -93,17 +93,16 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
     if (j < kJA) aoff[j] = (uint32_t)row_s[r] * row_bytes;
     boff[j] = (uint32_t)min(wn0 + r, g.Nw - 1) * row_bytes;
   }
-  auto dma = [&](int ks, uint8_t* A, uint8_t* B) {
-    const uint32_t c = 16u * min((uint32_t)ks * 8 + chunk, (uint32_t)(nb - 1));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r0 = 8 * (4 * j + wave);
-      if (j < kJA)
-        __builtin_amdgcn_global_load_lds((glb_void_t*)(abase + (aoff[j] + c)),
-                                         (lds_void_t*)(A + r0 * kF4RowBytes), 16, 0, 0);
+  auto next_chunk = [&](int ks) { return 16u * min((uint32_t)ks * 8 + chunk, (uint32_t)(nb - 1)); };
+  // load v of a stage: 0 to 7 weight rows, then activation rows
+  auto load_rows = [&](int v, uint32_t c, uint8_t* A, uint8_t* B) {
+    const int j = v & 7, r0 = 8 * (4 * j + wave);
+    if (v < 8)
       __builtin_amdgcn_global_load_lds((glb_void_t*)(bbase + (boff[j] + c)),
                                        (lds_void_t*)(B + r0 * kF4RowBytes), 16, 0, 0);
-    }
+    else
+      __builtin_amdgcn_global_load_lds((glb_void_t*)(abase + (aoff[j] + c)),
+                                       (lds_void_t*)(A + r0 * kF4RowBytes), 16, 0, 0);
   };
   // 8 scale bytes of a row at stage ks.  The first stage of a short row takes
   // them one by one (past its end the last again); a later stage, whose row
@@ -119,9 +118,11 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
     return v;
   };
   auto load_scales = [&](const uint8_t* row, int ks) -> u32x2 {
-    const int at = min(ks * 8, nb - 8);
-    const u32x2 v = *reinterpret_cast<const u32x2_a1*>(row + at);
-    return __builtin_bit_cast(u32x2, __builtin_bit_cast(uint64_t, v) >> (8 * (ks * 8 - at)));
+    return *reinterpret_cast<const u32x2_a1*>(row + min(ks * 8, nb - 8));
+  };
+  auto align_scales = [&](u32x2 v, int ks) -> u32x2 {
+    return __builtin_bit_cast(u32x2, __builtin_bit_cast(uint64_t, v) >>
+                                         (8 * max(ks * 8 - (nb - 8), 0)));
   };
 
   // sub-tile i of this wave / its column block c, as rows of the LDS tiles
@@ -145,39 +146,59 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
 
   SA0[tid] = first_scales(as_row);
   SB0[tid] = first_scales(bs_row);
-  dma(0, A0, B0);
+#pragma unroll
+  for (int v = 0; v < kJA + 8; ++v) load_rows(v, next_chunk(0), A0, B0);
   __builtin_amdgcn_s_waitcnt(0);
   lds_barrier();
 
   auto run_loop = [&](auto rows_c) {
     constexpr int kA = decltype(rows_c)::value;           // active sub-tiles of the wave
-    auto compute = [&](const uint8_t* A, const uint8_t* B, const u32x2* SA, const u32x2* SB) {
+    // One stage, as 4 kA groups of kC matrix instructions that the scheduler
+    // keeps in order: the next depth's fragment reads and, in the first three
+    // depths, the next stage's loads stand between the groups.  (Issued in
+    // one run, the loads hold the wave's instruction stream up for as long as
+    // the address unit takes to accept them.)
+    auto compute = [&](int ks, const uint8_t* A, const uint8_t* B, const u32x2* SA,
+                       const u32x2* SB, uint8_t* An, uint8_t* Bn) {
+      constexpr int kR = kA + kC, kV = kJA + 8, kG = 3 * kA;
+      const uint32_t chunk_off = next_chunk(ks + 1);
       u32x2 sa[kA], sb[kC];
+      u32x4 fa[2][kA], fb[2][kC];
+      auto read = [&](int u, int r) {
+        if (r < kC) fb[u & 1][r] = frag(B, bcol(r), u);
+        else fa[u & 1][r - kC] = frag(A, arow(r - kC), u);
+      };
+#pragma unroll
+      for (int r = 0; r < kR; ++r) read(0, r);
 #pragma unroll
       for (int i = 0; i < kA; ++i) sa[i] = SA[arow(i)] >> (uint32_t)(8 * lh);
 #pragma unroll
       for (int c = 0; c < kC; ++c) sb[c] = SB[bcol(c)] >> (uint32_t)(8 * lh);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        u32x4 fa[kA], fb[kC];
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int c = 0; c < kC; ++c) fb[c] = frag(B, bcol(c), u);
+        for (int i = 0; i < kA; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (u < 3) {
+            const int gi = u * kA + i;
 #pragma unroll
-        for (int i = 0; i < kA; ++i) fa[i] = frag(A, arow(i), u);
+            for (int v = kV * gi / kG; v < kV * (gi + 1) / kG; ++v)
+              load_rows(v, chunk_off, An, Bn);
 #pragma unroll
-        for (int i = 0; i < kA; ++i)
+            for (int r = kR * i / kA; r < kR * (i + 1) / kA; ++r) read(u + 1, r);
+          }
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
             if (u & 1)
               acc[i][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                  wide(fb[c]), wide(fa[i]), acc[i][c], 4, 4, 2, (int)sb[c][u >> 1], 2,
+                  wide(fb[1][c]), wide(fa[1][i]), acc[i][c], 4, 4, 2, (int)sb[c][u >> 1], 2,
                   (int)sa[i][u >> 1]);
             else
               acc[i][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                  wide(fb[c]), wide(fa[i]), acc[i][c], 4, 4, 0, (int)sb[c][u >> 1], 0,
+                  wide(fb[0][c]), wide(fa[0][i]), acc[i][c], 4, 4, 0, (int)sb[c][u >> 1], 0,
                   (int)sa[i][u >> 1]);
           }
-      }
+        }
     };
     // the last stage, one instruction depth at a time: it may hold 1 to 8 K
     // blocks; where K ends inside an instruction (K % 64 == 32) the upper
@@ -212,11 +233,10 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
                      const u32x2* SBc, uint8_t* An, uint8_t* Bn, u32x2* SAn, u32x2* SBn) {
       __builtin_amdgcn_sched_barrier(0);
       const u32x2 na = load_scales(as_row, ks + 1), nbs = load_scales(bs_row, ks + 1);
-      dma(ks + 1, An, Bn);
-      compute(Ac, Bc, SAc, SBc);
+      compute(ks, Ac, Bc, SAc, SBc, An, Bn);
       __builtin_amdgcn_sched_barrier(0);
-      SAn[tid] = na;
-      SBn[tid] = nbs;
+      SAn[tid] = align_scales(na, ks + 1);
+      SBn[tid] = align_scales(nbs, ks + 1);
       // the next stage is in LDS for this wave, then for all; and every wave
       // has read this stage before it is refilled
       __builtin_amdgcn_s_waitcnt(0);
