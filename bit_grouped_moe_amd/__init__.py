@@ -152,14 +152,20 @@ def _check(status, what):
         raise GQError(f"{what}: {lib.gq_status_string(status).decode()} (status {status})", status)
 
 
+# The raw handle of a device's current stream, without the Stream object that
+# torch.cuda.current_stream builds (1.9 us against 0.1 us, of a decode call
+# that takes about 10).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
 
 
 def _dev(t, name, dtype, ndim=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
@@ -171,7 +177,7 @@ def _dev(t, name, dtype, ndim=None):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 Route = namedtuple("Route", "expert_offsets sorted_pairs tiles num_tiles max_tiles tile_m "
@@ -185,7 +191,7 @@ def gq_route_max_tiles(rows, topk, num_experts, tile_m=TILE_M):
 def gq_route_sort(topk_ids, num_experts, tile_m=TILE_M, expert_offsets=None, sorted_pairs=None,
                   tiles=None, num_tiles=None):
     """Group the (token, slot) pairs of ``topk_ids`` int32 [rows, topk] by expert."""
-    lib = load_library()
+    lib = _lib or load_library()
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     rows, topk = topk_ids.shape
     dev = topk_ids.device
@@ -210,7 +216,7 @@ def gq_route_sort(topk_ids, num_experts, tile_m=TILE_M, expert_offsets=None, sor
 
 def gq_nf4_decode(codes, absmax, out_f32=True, out_bf16=True):
     """Decode NF4 codes uint8 [..., K/2] with absmax float32 [..., K/64]."""
-    lib = load_library()
+    lib = _lib or load_library()
     _dev(codes, "codes", torch.uint8)
     _dev(absmax, "absmax", torch.float32)
     K = codes.shape[-1] * 2
@@ -227,7 +233,7 @@ def gq_nf4_decode(codes, absmax, out_f32=True, out_bf16=True):
 
 def gq_mxfp4_decode(blocks, scales, out_f32=True, out_bf16=True):
     """Decode MXFP4 blocks uint8 [..., K/32, 16] with e8m0 scales uint8 [..., K/32]."""
-    lib = load_library()
+    lib = _lib or load_library()
     _dev(blocks, "blocks", torch.uint8)
     _dev(scales, "scales", torch.uint8)
     K = blocks.shape[-2] * 32
@@ -299,7 +305,7 @@ def _gemv_pairs(topk_ids, rows):
 
 def gq_nf4_grouped_gemv(x, codes, absmax, topk_ids, pair_scale=None, out=None):
     """Decode-time grouped GEMV (<= 256 pairs) on NF4 experts; returns bf16 [rows*topk, N]."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     E, N, Kw = _nf4_bank(codes, absmax)
     if Kw != K:
@@ -316,7 +322,7 @@ def gq_nf4_grouped_gemv(x, codes, absmax, topk_ids, pair_scale=None, out=None):
 
 def gq_mxfp4_grouped_gemv(x, blocks, scales, topk_ids, pair_scale=None, out=None):
     """Decode-time grouped GEMV (<= 256 pairs) on MXFP4 experts; returns bf16 [rows*topk, N]."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     E, N, Kw = _mx_bank(blocks, scales)
     if Kw != K:
@@ -337,7 +343,7 @@ def gq_mxfp4_grouped_gemv_swiglu(x, blocks, scales, topk_ids, alpha=OSS_ALPHA, l
     blocks [E, 2I, K] with gate row 2j and up row 2j + 1; returns bf16
     [rows*topk, I] = gc * sigmoid(alpha gc) * (uc + 1) (gc = min(gate, limit),
     uc = up clipped to [-limit, limit])."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     E, N2, Kw = _mx_bank(blocks, scales)
     if Kw != K or N2 % 2:
@@ -367,7 +373,7 @@ def gq_nf4_grouped_gemv_host(x, codes, absmax, topk_ids, pair_scale=None, out=No
     [E, N, K/2] and absmax float32 [E, N, K/64] are pinned CPU tensors; the
     kernel streams the routed experts' bytes over the host link.  x, topk_ids,
     pair_scale and out are device tensors.  Returns bf16 [rows*topk, N]."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     _host_bank(codes, absmax, ("codes", "absmax"))
     if codes.dtype != torch.uint8 or absmax.dtype != torch.float32 or codes.dim() != 3:
@@ -388,7 +394,7 @@ def gq_nf4_grouped_gemv_host(x, codes, absmax, topk_ids, pair_scale=None, out=No
 def gq_mxfp4_grouped_gemv_host(x, blocks, scales, topk_ids, pair_scale=None, out=None):
     """Decode GEMV on MXFP4 experts resident in pinned host memory (blocks
     uint8 [E, N, K/32, 16], scales uint8 [E, N, K/32], pinned CPU tensors)."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     _host_bank(blocks, scales, ("blocks", "scales"))
     if blocks.dtype != torch.uint8 or scales.dtype != torch.uint8 or blocks.dim() != 4:
@@ -413,7 +419,7 @@ def _route_ptrs(route):
 
 def gq_nf4_grouped_gemm(x, codes, absmax, route, pair_scale=None, out=None):
     """Prefill grouped GEMM on NF4 experts using a ``gq_route_sort`` result."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     E, N, Kw = _nf4_bank(codes, absmax)
     if Kw != K or route.rows != rows or route.num_experts != E:
@@ -429,7 +435,7 @@ def gq_nf4_grouped_gemm(x, codes, absmax, route, pair_scale=None, out=None):
 
 def gq_mxfp4_grouped_gemm(x, blocks, scales, route, pair_scale=None, out=None):
     """Prefill grouped GEMM on MXFP4 experts using a ``gq_route_sort`` result."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     E, N, Kw = _mx_bank(blocks, scales)
     if Kw != K or route.rows != rows or route.num_experts != E:
@@ -445,7 +451,7 @@ def gq_mxfp4_grouped_gemm(x, blocks, scales, route, pair_scale=None, out=None):
 
 def gq_nf4_grouped_dgrad(dy, codes, absmax, route, out=None):
     """dX = dY . W per pair through NF4 experts; ``route`` from gq_route_sort(pair ids [P, 1])."""
-    lib = load_library()
+    lib = _lib or load_library()
     P, N, ds = _x_args(dy, "dy")
     E, Nw, K = _nf4_bank(codes, absmax)
     if Nw != N or route.rows * route.topk != P or route.topk != 1 or route.num_experts != E:
@@ -459,7 +465,7 @@ def gq_nf4_grouped_dgrad(dy, codes, absmax, route, out=None):
 
 def gq_mxfp4_grouped_dgrad(dy, blocks, scales, route, out=None):
     """dX = dY . W per pair through MXFP4 experts; ``route`` from gq_route_sort(pair ids [P, 1])."""
-    lib = load_library()
+    lib = _lib or load_library()
     P, N, ds = _x_args(dy, "dy")
     E, Nw, K = _mx_bank(blocks, scales)
     if Nw != N or route.rows * route.topk != P or route.topk != 1 or route.num_experts != E:
@@ -475,7 +481,7 @@ def gq_mxfp4_grouped_dgrad(dy, blocks, scales, route, out=None):
 def gq_nf4_grouped_gemv_swiglu(x, codes, absmax, topk_ids, out=None):
     """Decode gate_up GEMV with SwiGLU fused: codes [E, 2I, K] (gate rows first);
     returns bf16 [rows*topk, I] = silu(gate) * up."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     E, N2, Kw = _nf4_bank(codes, absmax)
     if Kw != K or N2 % 2:
@@ -491,7 +497,7 @@ def gq_nf4_grouped_gemv_swiglu(x, codes, absmax, topk_ids, out=None):
 
 def gq_nf4_grouped_gemm_swiglu(x, codes, absmax, route, out=None):
     """Prefill gate_up GEMM with SwiGLU fused; returns bf16 [rows*topk, I]."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     E, N2, Kw = _nf4_bank(codes, absmax)
     if Kw != K or route.rows != rows or route.num_experts != E or N2 % 2:
@@ -516,7 +522,7 @@ def _weights(topk_weights, rows, topk):
 def gq_nf4_grouped_gemv_down_combine(act, codes, absmax, topk_ids, topk_weights=None, out=None):
     """Decode down GEMV with the router-weighted combine fused: act bf16 [rows*topk, I]
     (row p is pair p's input), codes [E, H, I]; returns bf16 [rows, H]."""
-    lib = load_library()
+    lib = _lib or load_library()
     P, I, a_s = _x_args(act, "act")
     E, H, Iw = _nf4_bank(codes, absmax)
     _dev(topk_ids, "topk_ids", torch.int32, 2)
@@ -537,7 +543,7 @@ def gq_mxfp4_grouped_gemv_down_combine(act, blocks, scales, topk_ids, topk_weigh
     """Decode down GEMV on MXFP4 experts with the router-weighted combine fused:
     act bf16 [rows*topk, I] (row p is pair p's input), blocks [E, H, I];
     returns bf16 [rows, H]."""
-    lib = load_library()
+    lib = _lib or load_library()
     P, I, a_s = _x_args(act, "act")
     E, H, Iw = _mx_bank(blocks, scales)
     _dev(topk_ids, "topk_ids", torch.int32, 2)
@@ -556,7 +562,7 @@ def gq_mxfp4_grouped_gemv_down_combine(act, blocks, scales, topk_ids, topk_weigh
 def gq_moe_combine(y_pairs, topk, topk_weights=None, out=None):
     """y[t] = sum_s w[t, s] * y_pairs[t*topk + s] (plain sum without weights);
     y_pairs bf16 [rows*topk, H]; returns bf16 [rows, H]."""
-    lib = load_library()
+    lib = _lib or load_library()
     P, H, ys = _x_args(y_pairs, "y_pairs")
     if P % topk:
         raise ValueError("y_pairs must hold rows*topk rows")
@@ -579,7 +585,7 @@ def split_sizes(rows, K):
 def gq_act_split_e4m3(x, codes=None, scales=None):
     """Two-term e4m3 split of bf16 activations x [rows, K]; returns the
     (codes, scales) uint8 tensors gq_mxfp4_grouped_gemm_scaled takes."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, K, xs = _x_args(x)
     cshape, sshape = split_sizes(rows, K)
     if codes is None:
@@ -598,7 +604,7 @@ def gq_act_split_e4m3(x, codes=None, scales=None):
 def gq_mxfp4_grouped_gemm_scaled(x_split, blocks, scales, route, pair_scale=None, out=None):
     """Prefill grouped GEMM on MXFP4 experts through the block-scaled fp4
     instruction; ``x_split`` = gq_act_split_e4m3(x) for x [rows, K]."""
-    lib = load_library()
+    lib = _lib or load_library()
     xq, xsc = x_split
     _dev(xq, "x_split codes", torch.uint8, 2)
     _dev(xsc, "x_split scales", torch.uint8, 2)
@@ -624,7 +630,7 @@ def gq_mxfp4_grouped_gemm_scaled_swiglu(x_split, blocks, scales, route, alpha=OS
     """Prefill gate_up GEMM on the block-scaled fp4 instruction with gpt-oss's
     gated unit in the epilogue: blocks [E, 2I, K] (gate row 2j, up row
     2j + 1); returns bf16 [rows*topk, I]."""
-    lib = load_library()
+    lib = _lib or load_library()
     xq, xsc = x_split
     _dev(xq, "x_split codes", torch.uint8, 2)
     _dev(xsc, "x_split scales", torch.uint8, 2)
@@ -653,7 +659,7 @@ def gq_mxfp4_grouped_gemm_scaled_swiglu_split(x_split, blocks, scales, route, al
     written as its two-term e4m3 split (the bytes gq_act_split_e4m3 would
     write for it); returns (codes, scales), the down product's x_split.
     ``out``: an optional (codes, scales) pair of the split_sizes shapes."""
-    lib = load_library()
+    lib = _lib or load_library()
     xq, xsc = x_split
     _dev(xq, "x_split codes", torch.uint8, 2)
     _dev(xsc, "x_split scales", torch.uint8, 2)
@@ -691,7 +697,7 @@ def _typed(t, name):
     """Type code of a device tensor of one of the three float types."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     code = _DTYPES.get(t.dtype)
     if code is None:
@@ -699,20 +705,22 @@ def _typed(t, name):
     return code
 
 
-def _beside(dev, **tensors):
+def _beside(index, *tensors):
     """Every tensor of a call lies on the device that it runs on."""
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, the call runs "
+                             f"on cuda:{index}")
 
 
-def _on(dev, fn, what, *args):
-    """Call the library on ``dev``'s current stream, with ``dev`` current."""
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _on(index, fn, what, *args):
+    """Call the library on the current stream of device ``index``, with that
+    device current."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st != 0:
         _check(st, what)
 
@@ -720,11 +728,14 @@ def _on(dev, fn, what, *args):
 def _rows(t, name):
     """(rows, width, row stride) of a tensor [..., width] whose leading
     dimensions lie at one stride."""
-    if t.dim() < 1 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape = t.shape
+    if len(shape) == 2 and shape[0] > 1 and t.stride(1) == 1:
+        return shape[0], shape[1], t.stride(0)
+    if len(shape) < 1 or (shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    if t.dim() != 2:
+    if len(shape) != 2:
         try:
-            t = t.view(-1, t.shape[-1]) if t.shape[-1] else t.reshape(0, 0)
+            t = t.view(-1, shape[-1]) if shape[-1] else t.reshape(0, 0)
         except RuntimeError:
             raise ValueError(f"the leading dimensions of {name} must lie at one stride") from None
     rows, width = t.shape
@@ -736,12 +747,13 @@ def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
     returns (blocks uint8 [..., K/32, 16], scales uint8 [..., K/32]), the
     layout that the MXFP4 entry points take.  ``values``: True or a bf16
     tensor of x's shape also returns the values that the codes stand for."""
-    lib = load_library()
+    lib = _lib or load_library()
     code = _typed(x, "x")
-    dev = x.device
+    dev, index = x.device, x.get_device()
     rows, K, stride = _rows(x, "x")
-    lead = tuple(x.shape[:-1])
-    bshape, sshape = lead + (K // 32, 16), lead + (K // 32,)
+    nb = K // 32
+    lead = (rows,) if x.dim() == 2 else tuple(x.shape[:-1])
+    bshape, sshape = (*lead, nb, 16), (*lead, nb)
     if blocks is None:
         blocks = torch.empty(bshape, dtype=torch.uint8, device=dev)
     elif tuple(_dev(blocks, "blocks", torch.uint8).shape) != bshape:
@@ -756,8 +768,8 @@ def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
         values = None
     elif values is not None and _dev(values, "values", torch.bfloat16).shape != x.shape:
         raise ValueError("values must have x's shape")
-    _beside(dev, blocks=blocks, scales=scales, values=values)
-    _on(dev, lib.gq_mxfp4_quantize, "gq_mxfp4_quantize", x.data_ptr(), code, rows, K, stride,
+    _beside(index, blocks, scales, values)
+    _on(index, lib.gq_mxfp4_quantize, "gq_mxfp4_quantize", x.data_ptr(), code, rows, K, stride,
         blocks.data_ptr(), scales.data_ptr(), None if values is None else values.data_ptr())
     return (blocks, scales) if values is None else (blocks, scales, values)
 
@@ -775,7 +787,7 @@ def _mx_pair(x, blocks, scales, unit):
                          "gq_mxfp4_quantize returns them")
     if unit and N % 2:
         raise ValueError("the gate_up width is odd")
-    _beside(xb.device, x_scales=xs, blocks=blocks, scales=scales)
+    _beside(xb.get_device(), xs, blocks, scales)
     return xb, xs, rows, E, N, K
 
 
@@ -783,13 +795,13 @@ def _fp4_gemm(what, x, blocks, scales, route, middle, N_out, pair_scale, out):
     xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, N_out is None)
     if route.rows != rows or route.num_experts != E:
         raise ValueError("x, blocks and route disagree")
-    dev = xb.device
+    index = xb.get_device()
     P = rows * route.topk
-    out = _out(out, P, N // 2 if N_out is None else N, dev)
-    _beside(dev, out=out, pair_scale=pair_scale, route=route.sorted_pairs)
+    out = _out(out, P, N // 2 if N_out is None else N, xb.device)
+    _beside(index, out, pair_scale, route.sorted_pairs)
     args = [xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(), scales.data_ptr(), E, N,
             route.topk, *middle(P), *_route_ptrs(route), out.data_ptr()]
-    _on(dev, getattr(load_library(), what), what, *args)
+    _on(index, getattr(_lib or load_library(), what), what, *args)
     return out
 
 
@@ -810,12 +822,12 @@ def gq_mxfp4_grouped_gemm_fp4_swiglu(x, blocks, scales, route, alpha=OSS_ALPHA, 
 
 def _fp4_gemv(what, x, blocks, scales, topk_ids, middle, unit, pair_scale, out):
     xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit)
-    dev = xb.device
+    index = xb.get_device()
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     P = _gemv_pairs(topk_ids, rows)
-    out = _out(out, P, N // 2 if unit else N, dev)
-    _beside(dev, out=out, pair_scale=pair_scale, topk_ids=topk_ids)
-    _on(dev, getattr(load_library(), what), what, xb.data_ptr(), xs.data_ptr(), rows, K,
+    out = _out(out, P, N // 2 if unit else N, xb.device)
+    _beside(index, out, pair_scale, topk_ids)
+    _on(index, getattr(_lib or load_library(), what), what, xb.data_ptr(), xs.data_ptr(), rows, K,
         blocks.data_ptr(), scales.data_ptr(), E, N, topk_ids.data_ptr(), topk_ids.shape[1],
         *middle(P), out.data_ptr())
     return out
@@ -843,12 +855,12 @@ def gq_moe_topk(logits, topk, renormalize=True, topk_ids=None, topk_weights=None
     topk], topk_weights float32 [rows, topk]), the weights a softmax over the
     chosen logits (``renormalize``) or over all.  A logit of -inf is never
     chosen; a slot left without an expert has id -1 and weight 0."""
-    lib = load_library()
+    lib = _lib or load_library()
     code = _typed(logits, "logits")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
     rows, E, stride = _rows(logits, "logits")
-    dev, topk = logits.device, int(topk)
+    dev, index, topk = logits.device, logits.get_device(), int(topk)
     if topk < 1:
         raise ValueError("topk must be at least 1")
     shape = (rows, topk)
@@ -860,8 +872,8 @@ def gq_moe_topk(logits, topk, renormalize=True, topk_ids=None, topk_weights=None
         topk_weights = torch.empty(shape, dtype=torch.float32, device=dev)
     elif tuple(_dev(topk_weights, "topk_weights", torch.float32).shape) != shape:
         raise ValueError(f"topk_weights must be {shape}")
-    _beside(dev, topk_ids=topk_ids, topk_weights=topk_weights)
-    _on(dev, lib.gq_moe_topk, "gq_moe_topk", logits.data_ptr(), code, rows, E, stride, topk,
+    _beside(index, topk_ids, topk_weights)
+    _on(index, lib.gq_moe_topk, "gq_moe_topk", logits.data_ptr(), code, rows, E, stride, topk,
         1 if renormalize else 0, topk_ids.data_ptr(), topk_weights.data_ptr())
     return topk_ids, topk_weights
 
@@ -869,12 +881,12 @@ def gq_moe_topk(logits, topk, renormalize=True, topk_ids=None, topk_weights=None
 def gq_moe_topk_backward(d_weights, logits, topk_ids, renormalize=True, out=None):
     """Gradient of ``gq_moe_topk``'s weights to its logits, the selection held
     fixed: d_weights float32 [rows, topk] -> [rows, E] of the logits' type."""
-    lib = load_library()
+    lib = _lib or load_library()
     code = _typed(logits, "logits")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
     rows, E, stride = _rows(logits, "logits")
-    dev = logits.device
+    dev, index = logits.device, logits.get_device()
     _dev(d_weights, "d_weights", torch.float32, 2)
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     if topk_ids.shape[0] != rows or d_weights.shape != topk_ids.shape:
@@ -883,8 +895,8 @@ def gq_moe_topk_backward(d_weights, logits, topk_ids, renormalize=True, out=None
         out = torch.empty((rows, E), dtype=logits.dtype, device=dev)
     elif tuple(_dev(out, "out", logits.dtype).shape) != (rows, E):
         raise ValueError("out must be [rows, E]")
-    _beside(dev, d_weights=d_weights, topk_ids=topk_ids, out=out)
-    _on(dev, lib.gq_moe_topk_backward, "gq_moe_topk_backward", d_weights.data_ptr(),
+    _beside(index, d_weights, topk_ids, out)
+    _on(index, lib.gq_moe_topk_backward, "gq_moe_topk_backward", d_weights.data_ptr(),
         logits.data_ptr(), code, rows, E, stride, topk_ids.data_ptr(), topk_ids.shape[1],
         1 if renormalize else 0, out.data_ptr())
     return out
@@ -936,8 +948,7 @@ def gq_moe_layer(router_weight, gate_up, down, topk, router_bias=None, gate_up_b
         if b is not None and tuple(_dev(b, name, torch.bfloat16).shape) != shape:
             raise ValueError(f"{name} must be {shape}")
     tensors = (router_weight, router_bias, *gate_up, gate_up_bias, *down, down_bias)
-    for t in tensors:
-        _beside(dev, weight=t)
+    _beside(dev.index, *tensors)
     ptr = [None if t is None else t.data_ptr() for t in tensors]
     struct = _LayerStruct(1 if mx else 0, E, int(topk), H, inner, 1 if renormalize else 0,
                           float(alpha), float(limit), *ptr)
@@ -957,7 +968,7 @@ def gq_moe_decode(layer, x, out=None, workspace=None):
     """The whole layer for x bf16 [rows, H], at most 8 tokens and 64 (token,
     expert) pairs: bf16 [rows, H].  ``workspace``: a uint8 tensor of at least
     gq_moe_decode_workspace bytes (allocated when None)."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, H, stride = _x_args(x)
     dev = x.device
     if H != layer.hidden:
@@ -976,7 +987,8 @@ def gq_moe_decode(layer, x, out=None, workspace=None):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _dev(workspace, "workspace", torch.uint8)
-    _beside(layer.device, x=x, out=out, workspace=workspace)
-    _on(dev, lib.gq_moe_decode, "gq_moe_decode", layer._ref, x.data_ptr(), rows,
+    index = layer.device.index
+    _beside(index, x, out, workspace)
+    _on(index, lib.gq_moe_decode, "gq_moe_decode", layer._ref, x.data_ptr(), rows,
         stride if rows > 1 else H, workspace.data_ptr(), workspace.numel(), out.data_ptr())
     return out
