@@ -1,11 +1,11 @@
 // A whole mixture-of-experts layer for a few tokens (at most 8 tokens and 64
 // routed pairs): router product, selection, the experts' gated products and
-// the weighted combine, in three launches without a host round trip.
+// the weighted combine, without a host round trip.
 //
-//   z = x Wr^T + br                                         (launch 1)
-//   e_s, w_s = the topk largest logits of a token, softmax   (launch 2)
-//   a_s = unit(Wgu[e_s] x + bgu[e_s])                        (launch 2)
-//   y = sum_s w_s (Wd[e_s] a_s + bd[e_s])                    (launch 3)
+//   z = x Wr^T + br                                          moe_logits_kernel
+//   e_s, w_s = the topk largest logits of a token, softmax   moe_select_kernel
+//   a_s = unit(Wgu[e_s] x + bgu[e_s])                        moe_gate_up_kernel
+//   y = sum_s w_s (Wd[e_s] a_s + bd[e_s])                    moe_down_kernel
 //
 // Everything between the bf16 input and the bf16 output is float32 (logits,
 // weights, gated products: the workspace holds them).  Bound by the latency
@@ -15,9 +15,10 @@
 // The launches are the dependencies between workgroups: the logits need
 // every hidden element and are spread over the chip (one workgroup per
 // expert); the gate_up product needs the selection, the down product whole
-// activation rows.  The selection itself is a wave's work on E logits, so
-// each gate_up workgroup makes it again for itself instead of waiting for a
-// launch of its own.
+// activation rows.  The selection is one wave's work on a token's logits:
+// for one token each gate_up workgroup makes it for itself (three launches),
+// for several a launch of its own is faster than every workgroup's making
+// all of them (8 tokens, E = 128: gate_up 39.5 us with the selections inside).
 #include <algorithm>
 #include <type_traits>
 
@@ -83,24 +84,71 @@ __global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
   }
 }
 
-// ---- launch 2: selection, gate_up product and gated unit ---------------------
+// ---- selection of one token by one wave ----------------------------------------
+// The first `slots` slots into id (lane s: slot s); with `write`, all slots'
+// ids and softmax weights to memory.
+template <int C>
+__device__ __forceinline__ int moe_select(const float* __restrict__ logits, int E, int topk,
+                                          int slots, int lane, bool write, int renorm,
+                                          int32_t* __restrict__ ids, float* __restrict__ w) {
+  uint32_t key[C], all[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = 64 * c + lane;
+    const float z = logits[min(e, E - 1)];
+    key[c] = all[c] = e < E ? logit_key(z) : 0u;
+  }
+  int id;
+  float z;
+  wave_topk<C>(key, slots, lane, id, z);
+  if (write) {
+    const float peak = row_peak(z, id);
+    const float part = id >= 0 ? expf(z - peak) : 0.f;
+    float total = part;
+    if (!renorm) {
+      total = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        total += all[c] > kDeadKey ? expf(key_logit(all[c]) - peak) : 0.f;
+    }
+    total = wave_fsum(total);
+    if (lane < topk) {
+      ids[lane] = id;
+      w[lane] = id >= 0 ? part / total : 0.f;
+    }
+  }
+  return id;
+}
+
+// A wave per token.
+template <int C>
+__global__ __launch_bounds__(kWave* kMoeMaxRows) void moe_select_kernel(
+    const float* __restrict__ logits, int E, int topk, int renorm, int32_t* __restrict__ ids,
+    float* __restrict__ w) {
+  const int t = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  moe_select<C>(logits + (int64_t)t * E, E, topk, topk, threadIdx.x & (kWave - 1), true, renorm,
+                ids + t * topk, w + t * topk);
+}
+
+// ---- gate_up product and gated unit ----------------------------------------------
 // Grid (column chunks, pairs), the row layout of the decode GEMV: workgroup
 // (x, p) computes output columns [n0, n0 + R/2) of pair p's expert for every
-// pair that shares it, if p is the first of them; the others end after the
-// selection.  NF4: gate row j, up row I + j, SwiGLU; MXFP4: gate row 2j, up
-// row 2j + 1, the clamped unit.  Workgroup (0, 0) writes the selection for
-// launch 3.
+// pair that shares it, if p is the first of them; the others end at once.
+// NF4: gate row j, up row I + j, SwiGLU; MXFP4: gate row 2j, up row 2j + 1,
+// the clamped unit.  C > 0 (one token, C logits a lane): the workgroup
+// selects for itself, as far as its own slot (a token's experts are
+// distinct), and the last slot's first workgroup writes the selection for
+// the down product; C == 0: ids come from moe_select_kernel.
 template <bool kMx, int kIter, bool kWaveRows, int C>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
     const float* __restrict__ logits, const uint16_t* __restrict__ x,
     const uint8_t* __restrict__ codes, const void* __restrict__ scl, int H, int I, int E,
     int x_stride, int topk, int rows, const uint16_t* __restrict__ bias, float alpha, float limit,
-    int renorm, int32_t* __restrict__ ids_out, float* __restrict__ w_out,
-    float* __restrict__ act) {
+    int renorm, int32_t* __restrict__ ids, float* __restrict__ w, float* __restrict__ act) {
   constexpr int kHalf = kIter / 2;
   __shared__ __attribute__((aligned(4096))) LutT lut[kLutN];
   __shared__ float red[kWaveRows ? 1 : kIter * (kMoeThreads + 32)];
-  __shared__ int ids_s[kMoeMaxPairs];
+  __shared__ int mine_s;
 
   const int N = 2 * I, P = rows * topk;
   const int S = H >> 5;
@@ -134,41 +182,23 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
   load_x(p0);
   if constexpr (!kMx) lut_init(lut, tid, NT);
 
-  // ---- selection: a wave per token ----
-  const bool writer = blockIdx.x == 0 && blockIdx.y == 0;
-  for (int t = wave; t < rows; t += NT / kWave) {
-    uint32_t key[C], all[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = 64 * c + lane;
-      const float z = logits[(int64_t)t * E + min(e, E - 1)];
-      key[c] = all[c] = e < E ? logit_key(z) : 0u;
+  int e;
+  uint64_t same;
+  if constexpr (C > 0) {
+    if (wave == 0) {
+      const bool write = blockIdx.x == 0 && p0 == P - 1;
+      const int id = moe_select<C>(logits, E, topk, p0 + 1, lane, write, renorm, ids, w);
+      if (lane == p0) mine_s = id;
     }
-    int id;
-    float z;
-    wave_topk<C>(key, topk, lane, id, z);
-    if (lane < topk) ids_s[t * topk + lane] = id;
-    if (writer) {
-      const float peak = row_peak(z, id);
-      const float part = id >= 0 ? expf(z - peak) : 0.f;
-      float total = part;
-      if (!renorm) {
-        total = 0.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          total += all[c] > kDeadKey ? expf(key_logit(all[c]) - peak) : 0.f;
-      }
-      total = wave_fsum(total);
-      if (lane < topk) {
-        ids_out[t * topk + lane] = id;
-        w_out[t * topk + lane] = id >= 0 ? part / total : 0.f;
-      }
-    }
+    lds_barrier();
+    e = __builtin_amdgcn_readfirstlane(mine_s);
+    same = 1ull << p0;
+  } else {
+    const int idl = ids[min(lane, P - 1)];
+    if constexpr (!kMx) lds_barrier();                     // the table
+    e = __builtin_amdgcn_readlane(idl, p0);
+    same = __ballot(idl == e && lane < P);
   }
-  lds_barrier();
-  const int e = __builtin_amdgcn_readfirstlane(ids_s[p0]);
-  const int idl = ids_s[min(lane, P - 1)];
-  uint64_t same = __ballot(idl == e && lane < P);
   // no expert, or an earlier pair's workgroup computes this one (uniform)
   if (e < 0 || (same & ((1ull << p0) - 1ull))) return;
 
@@ -282,10 +312,12 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
   }
 }
 
-// ---- launch 3: down product and combine ----------------------------------------
-// Workgroup: output rows [n0, n0 + Rb) for every pair, so a token's products
-// meet in LDS.  Wave w takes pairs w, w + waves, ...; its lane groups (W
-// lanes, one or two 32-weight segments a lane) take kR rows each.
+// ---- down product and combine ------------------------------------------------------
+// Grid (row chunks, tokens): output rows [n0, n0 + Rb) of one token, whose
+// products meet in LDS.  Wave w takes slots w, w + waves, ...; its lane
+// groups (W lanes, one or two 32-weight segments a lane) take kR rows each
+// against the slot's activations, which a lane holds in registers: more rows
+// a lane where several tokens fill the chip.
 template <bool kMx>
 __device__ __forceinline__ float segment_dot_f32(const LutT* lut, u32x4 c, float am, uint32_t sb,
                                                  const f32x4 (&xv)[8]) {
@@ -315,19 +347,19 @@ template <bool kMx, int kR, int kSeg>
 __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ act,
     const uint8_t* __restrict__ codes, const void* __restrict__ scl, int I, int H, int topk,
-    int rows, const float* __restrict__ weights, const uint16_t* __restrict__ bias,
+    const float* __restrict__ weights, const uint16_t* __restrict__ bias,
     uint16_t* __restrict__ y) {
   __shared__ __attribute__((aligned(4096))) LutT lut[kMx ? 1 : kLutN];
-  extern __shared__ float ys[];                            // [P][Rb]
+  extern __shared__ float ys[];                            // [topk][Rb]
 
-  const int P = rows * topk;
   const int S = I >> 5;
   const int W = kSeg == 2 ? kWave : (S > 1 ? 1 << (32 - __builtin_clz(S - 1)) : 1);
-  const int waves = min(P, kDownWaves);
+  const int waves = min(topk, kDownWaves);
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int Rb = (kWave / W) * kR;
   const int n0 = blockIdx.x * Rb;
+  const int p0 = blockIdx.y * topk;                        // the token's first pair
   const int g = lane / W, s = lane - g * W;
   bool active[kSeg];
   int s_cl[kSeg];
@@ -336,21 +368,28 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
     active[j] = s + kWave * j < S;
     s_cl[j] = active[j] ? s + kWave * j : 0;
   }
-  const int idl = lane < P ? ids[lane] : -1;
+  const float w_own = tid < topk ? weights[p0 + tid] : 0.f;    // used by the combine
   if constexpr (!kMx) {
     lut_init(lut, tid, kWave * waves);
     lds_barrier();
   }
-  for (int p = wave; p < P; p += waves) {
-    const int e = __builtin_amdgcn_readlane(idl, p);
+  for (int sl = wave; sl < topk; sl += waves) {
+    const int e = ids[p0 + sl];                            // uniform
     float tot[kR];
 #pragma unroll
     for (int i = 0; i < kR; ++i) tot[i] = 0.f;
-    if (e >= 0) {                                          // uniform; no expert: adds nothing
+    f32x4 xv[kSeg][8];
+#pragma unroll
+    for (int j = 0; j < kSeg; ++j) {
+      const f32x4* ap =
+          reinterpret_cast<const f32x4*>(act + (int64_t)(p0 + sl) * I + (int64_t)s_cl[j] * 32);
+#pragma unroll
+      for (int v = 0; v < 8; ++v) xv[j][v] = ap[v];
+    }
+    if (e >= 0) {                                          // no expert: adds nothing
       u32x4 cw[kR][kSeg];
       float am[kR][kSeg], bv[kR];
       uint32_t sb[kR][kSeg];
-      f32x4 xv[kSeg][8];
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
         const int n = min(n0 + g * kR + i, H - 1);
@@ -370,13 +409,6 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
         bv[i] = bias ? bf16_at(bias, row) : 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < kSeg; ++j) {
-        const f32x4* ap =
-            reinterpret_cast<const f32x4*>(act + (int64_t)p * I + (int64_t)s_cl[j] * 32);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) xv[j][v] = ap[v];
-      }
-#pragma unroll
       for (int i = 0; i < kR; ++i) {
         float part = 0.f;
 #pragma unroll
@@ -387,20 +419,16 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
     }
 #pragma unroll
     for (int i = 0; i < kR; ++i)
-      if (s == W - 1) ys[p * Rb + g * kR + i] = tot[i];
+      if (s == W - 1) ys[sl * Rb + g * kR + i] = tot[i];
   }
+  float* wts = ys + topk * Rb;
+  if (tid < topk) wts[tid] = w_own;
   lds_barrier();
-  // thread (t, r) sums its token's slots in order
-  for (int idx = tid; idx < rows * Rb; idx += kWave * waves) {
-    const int t = idx / Rb, r = idx - t * Rb;
-    const int n = n0 + r;
-    if (n >= H) continue;
+  // thread r sums its row's slots in order
+  for (int r = tid; r < Rb; r += kWave * waves) {
     float acc = 0.f;
-    for (int sl = 0; sl < topk; ++sl) {
-      const int p = t * topk + sl;
-      acc = __builtin_fmaf(weights[p], ys[p * Rb + r], acc);
-    }
-    y[(int64_t)t * H + n] = f32_to_bf16_bits(acc);
+    for (int sl = 0; sl < topk; ++sl) acc = __builtin_fmaf(wts[sl], ys[sl * Rb + r], acc);
+    if (n0 + r < H) y[(int64_t)blockIdx.y * H + n0 + r] = f32_to_bf16_bits(acc);
   }
 }
 
@@ -481,11 +509,11 @@ static void gate_up(hipStream_t stream, const gq_moe_layer& l, const float* logi
 template <bool kMx, int kR, int kSeg>
 static void launch_down(hipStream_t stream, const gq_moe_layer& l, int W, int rows,
                         const int32_t* ids, const float* w, const float* act, uint16_t* y) {
-  const int P = rows * l.topk, Rb = (kWave / W) * kR;
-  hipLaunchKernelGGL((moe_down_kernel<kMx, kR, kSeg>), dim3((l.hidden + Rb - 1) / Rb),
-                     dim3(kWave * std::min(P, kDownWaves)), (size_t)P * Rb * 4, stream, ids, act,
-                     l.down_codes, l.down_scales, l.inner, l.hidden, l.topk, rows, w, l.down_bias,
-                     y);
+  const int Rb = (kWave / W) * kR;
+  hipLaunchKernelGGL((moe_down_kernel<kMx, kR, kSeg>), dim3((l.hidden + Rb - 1) / Rb, rows),
+                     dim3(kWave * std::min(l.topk, kDownWaves)), (size_t)l.topk * (Rb + 1) * 4,
+                     stream, ids, act, l.down_codes, l.down_scales, l.inner, l.hidden, l.topk, w,
+                     l.down_bias, y);
 }
 
 template <bool kMx>
@@ -496,19 +524,30 @@ static void moe_decode(hipStream_t stream, const gq_moe_layer& l, const uint16_t
   int32_t* ids = reinterpret_cast<int32_t*>(ws + m.ids);
   float* w = reinterpret_cast<float*>(ws + m.weights);
   float* act = reinterpret_cast<float*>(ws + m.act);
-  if (rows == 1)
+  const bool narrow = l.num_experts <= 128;                // two logits a lane, else eight
+  if (rows == 1) {
     hipLaunchKernelGGL(moe_logits_kernel<1>, dim3(l.num_experts), dim3(kMoeThreads), 0, stream, x,
                        l.router_weight, l.hidden, x_stride, rows, l.num_experts, l.router_bias,
                        logits);
-  else
+    if (narrow) gate_up<kMx, 2>(stream, l, logits, x, x_stride, rows, ids, w, act);
+    else gate_up<kMx, 8>(stream, l, logits, x, x_stride, rows, ids, w, act);
+  } else {
     hipLaunchKernelGGL(moe_logits_kernel<kMoeMaxRows>, dim3(l.num_experts), dim3(kMoeThreads), 0,
                        stream, x, l.router_weight, l.hidden, x_stride, rows, l.num_experts,
                        l.router_bias, logits);
-  if (l.num_experts <= 128) gate_up<kMx, 2>(stream, l, logits, x, x_stride, rows, ids, w, act);
-  else gate_up<kMx, 8>(stream, l, logits, x, x_stride, rows, ids, w, act);
+    if (narrow)
+      hipLaunchKernelGGL(moe_select_kernel<2>, dim3(1), dim3(kWave * rows), 0, stream, logits,
+                         l.num_experts, l.topk, l.renormalize, ids, w);
+    else
+      hipLaunchKernelGGL(moe_select_kernel<8>, dim3(1), dim3(kWave * rows), 0, stream, logits,
+                         l.num_experts, l.topk, l.renormalize, ids, w);
+    gate_up<kMx, 0>(stream, l, logits, x, x_stride, rows, ids, w, act);
+  }
   int S, W, G, NT;
   segment_layout(l.inner, S, W, G, NT);
+  const bool many = rows > 2;
   if (S > kWave) launch_down<kMx, 4, 2>(stream, l, kWave, rows, ids, w, act, y);
+  else if (many) launch_down<kMx, 8, 1>(stream, l, W, rows, ids, w, act, y);
   else launch_down<kMx, 2, 1>(stream, l, W, rows, ids, w, act, y);
 }
 
