@@ -37,11 +37,7 @@ constexpr int kMoeMaxInner = 128 * 32;       // two segments per lane
 constexpr int kMoeThreads = 256;
 constexpr int kDownWaves = 8;
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p, int64_t i) {
-  return __uint_as_float((uint32_t)p[i] << 16);
-}
-
-// ---- launch 1: logits of one expert for every token -------------------------
+// ---- logits of one expert for every token -------------------------
 // Workgroup e; thread t takes the 16-byte pieces t, t + 256, ... of the
 // expert's row and of each token's.
 template <int kRows>
@@ -51,7 +47,10 @@ __global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
   __shared__ float part[kMoeThreads / kWave][kRows];
   const int e = blockIdx.x, tid = threadIdx.x;
   const int wave = tid / kWave, lane = tid & (kWave - 1);
-  const float b = bias && tid < rows ? bf16_at(bias, e) : 0.f;
+  // biases stay raw until they are added: converted at once, the load would be
+  // waited for here
+  uint32_t braw = 0u;
+  if (bias) braw = bias[e];
   float acc[kRows];
 #pragma unroll
   for (int t = 0; t < kRows; ++t) acc[t] = 0.f;
@@ -80,7 +79,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
     float s = part[0][tid];
 #pragma unroll
     for (int i = 1; i < kMoeThreads / kWave; ++i) s += part[i][tid];
-    logits[(int64_t)tid * E + e] = s + b;
+    logits[(int64_t)tid * E + e] = s + __uint_as_float(braw << 16);
   }
 }
 
@@ -132,8 +131,12 @@ __global__ __launch_bounds__(kWave* kMoeMaxRows) void moe_select_kernel(
 
 // ---- gate_up product and gated unit ----------------------------------------------
 // Grid (column chunks, pairs), the row layout of the decode GEMV: workgroup
-// (x, p) computes output columns [n0, n0 + R/2) of pair p's expert for every
-// pair that shares it, if p is the first of them; the others end at once.
+// (x, p) computes the output column chunks x, x + gridDim.x, ... of pair p.
+// Pairs that share an expert each read its rows: a workgroup that served all
+// of them (as in the decode GEMV) decodes once per pair anyway, and the
+// longest such group then sets the time (8 tokens on E = 128 NF4 experts:
+// 54.4 us a layer, 8 equal tokens 55.4; one pair a workgroup 50.6 and 45.0,
+// the repeated rows coming from the caches).
 // NF4: gate row j, up row I + j, SwiGLU; MXFP4: gate row 2j, up row 2j + 1,
 // the clamped unit.  C > 0 (one token, C logits a lane): the workgroup
 // selects for itself, as far as its own slot (a token's experts are
@@ -143,14 +146,14 @@ template <bool kMx, int kIter, bool kWaveRows, int C>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
     const float* __restrict__ logits, const uint16_t* __restrict__ x,
     const uint8_t* __restrict__ codes, const void* __restrict__ scl, int H, int I, int E,
-    int x_stride, int topk, int rows, const uint16_t* __restrict__ bias, float alpha, float limit,
+    int x_stride, int topk, const uint16_t* __restrict__ bias, float alpha, float limit,
     int renorm, int32_t* __restrict__ ids, float* __restrict__ w, float* __restrict__ act) {
   constexpr int kHalf = kIter / 2;
   __shared__ __attribute__((aligned(4096))) LutT lut[kLutN];
   __shared__ float red[kWaveRows ? 1 : kIter * (kMoeThreads + 32)];
   __shared__ int mine_s;
 
-  const int N = 2 * I, P = rows * topk;
+  const int N = 2 * I;
   const int S = H >> 5;
   int W, G, NT;
   if constexpr (kWaveRows) {
@@ -167,43 +170,37 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int p0 = blockIdx.y;
   const int R = G * kIter, Rout = R / 2;
-  const int n0 = blockIdx.x * Rout;
   const int g = tid / W, s = tid - g * W;
   const bool active = kWaveRows ? s < S : tid < S * G;
 
-  // p0's activations and the table, ahead of the selection
+  // the pair's activations and the table, ahead of the selection
   u32x4 xr[4];
-  auto load_x = [&](int p) {
-    const u32x4* xp = reinterpret_cast<const u32x4*>(x + (int64_t)(p / topk) * x_stride +
+  {
+    const u32x4* xp = reinterpret_cast<const u32x4*>(x + (int64_t)(p0 / topk) * x_stride +
                                                       (active ? s : 0) * 32);
 #pragma unroll
     for (int v = 0; v < 4; ++v) xr[v] = xp[v];
-  };
-  load_x(p0);
+  }
   if constexpr (!kMx) lut_init(lut, tid, NT);
 
   int e;
-  uint64_t same;
   if constexpr (C > 0) {
     if (wave == 0) {
-      const bool write = blockIdx.x == 0 && p0 == P - 1;
+      const bool write = blockIdx.x == 0 && p0 == topk - 1;
       const int id = moe_select<C>(logits, E, topk, p0 + 1, lane, write, renorm, ids, w);
       if (lane == p0) mine_s = id;
     }
     lds_barrier();
     e = __builtin_amdgcn_readfirstlane(mine_s);
-    same = 1ull << p0;
   } else {
-    const int idl = ids[min(lane, P - 1)];
+    e = ids[p0];
     if constexpr (!kMx) lds_barrier();                     // the table
-    e = __builtin_amdgcn_readlane(idl, p0);
-    same = __ballot(idl == e && lane < P);
   }
-  // no expert, or an earlier pair's workgroup computes this one (uniform)
-  if (e < 0 || (same & ((1ull << p0) - 1ull))) return;
+  if (e < 0) return;                                       // no expert (uniform)
 
-  // ---- weight bytes: all of a thread's loads before their first use ----
-  auto wrow = [&](int gg, int i) -> int {
+  // ---- weight rows: the kIter rows of a thread in the chunk that starts at
+  // output column n0; all loads before their first use ----
+  auto wrow = [&](int n0, int gg, int i) -> int {
     if constexpr (!kMx) {
       const int j = min(n0 + gg + G * (i % kHalf), I - 1);
       return i < kHalf ? j : I + j;
@@ -220,74 +217,76 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
   const uint8_t* cbase = codes + (size_t)e * ((size_t)N * row_bytes);
   const uint8_t* sbase =
       static_cast<const uint8_t*>(scl) + (size_t)e * ((size_t)N * spr * kScaleBytes);
-  u32x4 cw[kIter];
-  float am[kIter], bv[kIter];
-  uint32_t sb[kIter];
+  const uint16_t* be = bias ? bias + (size_t)e * N : nullptr;
+  struct Rows {
+    u32x4 c[kIter];
+    float am[kIter];
+    uint32_t sb[kIter];
+    uint32_t braw[kIter];                    // biases, raw until they are added
+  };
+  auto load_rows = [&](int n0, Rows& w) {
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const uint32_t r = (uint32_t)wrow(g, i);
-    cw[i] = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4*>(cbase + (__umul24(r, row_bytes) + s_cl * 16u)));
-    const uint32_t so = (__umul24(r, spr) + (kMx ? s_cl : s_cl / 2)) * kScaleBytes;
-    if constexpr (kMx) {
-      sb[i] = (uint32_t)sbase[so];
-      am[i] = 0.f;
-    } else {
-      am[i] = *reinterpret_cast<const float*>(sbase + so);
-      sb[i] = 0u;
+    for (int i = 0; i < kIter; ++i) {
+      const uint32_t r = (uint32_t)wrow(n0, g, i);
+      w.c[i] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(cbase + (__umul24(r, row_bytes) + s_cl * 16u)));
+      const uint32_t so = (__umul24(r, spr) + (kMx ? s_cl : s_cl / 2)) * kScaleBytes;
+      if constexpr (kMx) {
+        w.sb[i] = (uint32_t)sbase[so];
+        w.am[i] = 0.f;
+      } else {
+        w.am[i] = *reinterpret_cast<const float*>(sbase + so);
+        w.sb[i] = 0u;
+      }
+      w.braw[i] = 0u;
     }
-    bv[i] = 0.f;
-  }
-  // biases: in-wave rows, each row's on its lanes; LDS rows, gate and up of
-  // output column n0 + tid in bv[0], bv[1]
-  if (bias) {
-    const uint16_t* be = bias + (size_t)e * N;
-    if constexpr (kWaveRows) {
+    // in-wave rows: each row's bias on its lanes; LDS rows: gate's and up's of
+    // output column n0 + tid in the first two
+    if (be) {
+      if constexpr (kWaveRows) {
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) bv[i] = bf16_at(be, wrow(g, i));
-    } else {
-      const int n = min(n0 + tid, I - 1);
-      bv[0] = bf16_at(be, kMx ? 2 * n : n);
-      bv[1] = bf16_at(be, kMx ? 2 * n + 1 : I + n);
-    }
-  }
-
-  auto unit = [&](float gate, float up) {
-    if constexpr (kMx) {
-      return clamped_unit(gate, up, alpha, limit);
-    } else {
-      return silu_f32(gate) * up;
+        for (int i = 0; i < kIter; ++i) w.braw[i] = be[wrow(n0, g, i)];
+      } else {
+        const int n = min(n0 + tid, I - 1);
+        w.braw[0] = be[kMx ? 2 * n : n];
+        w.braw[1] = be[kMx ? 2 * n + 1 : I + n];
+      }
     }
   };
-  while (same) {                              // p0 first, then ascending
-    const int p = __builtin_ctzll(same);
-    same &= same - 1ull;
-    if (p != p0) load_x(p);
-    float xf[32];
+  auto unit = [&](float gate, float up) {
+    if constexpr (kMx) return clamped_unit(gate, up, alpha, limit);
+    else return silu_f32(gate) * up;
+  };
+  auto bias_of = [](uint32_t raw) { return __uint_as_float(raw << 16); };
+
+  float xf[32];
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+  for (int v = 0; v < 4; ++v)
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        xf[8 * v + 2 * cc] = bf16lo_to_f32(xr[v][cc]);
-        xf[8 * v + 2 * cc + 1] = bf16hi_to_f32(xr[v][cc]);
-      }
+    for (int cc = 0; cc < 4; ++cc) {
+      xf[8 * v + 2 * cc] = bf16lo_to_f32(xr[v][cc]);
+      xf[8 * v + 2 * cc + 1] = bf16hi_to_f32(xr[v][cc]);
+    }
+  float* arow = act + (int64_t)p0 * I;
+  auto compute = [&](int n0, const Rows& w) {
     if constexpr (kWaveRows) {
       float vals[kIter];
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
-        const float part = active ? segment_dot<kMx>(lut, cw[i], am[i], sb[i], xf, xr) : 0.f;
-        vals[i] = group_sum_last(part, W) + bv[i];             // total on lane s == W - 1
+        const float part = active ? segment_dot<kMx>(lut, w.c[i], w.am[i], w.sb[i], xf, xr) : 0.f;
+        vals[i] = group_sum_last(part, W) + bias_of(w.braw[i]);     // total on lane s == W - 1
       }
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) {
         const int n = n0 + g + G * i;
-        if (s == W - 1 && n < I) act[(int64_t)p * I + n] = unit(vals[i], vals[i + kHalf]);
+        if (s == W - 1 && n < I) arow[n] = unit(vals[i], vals[i + kHalf]);
       }
     } else {
       constexpr int kStride = kMoeThreads + 32;                // pad: spreads banks
 #pragma unroll
       for (int i = 0; i < kIter; ++i)
-        red[i * kStride + tid] = active ? segment_dot<kMx>(lut, cw[i], am[i], sb[i], xf, xr) : 0.f;
+        red[i * kStride + tid] =
+            active ? segment_dot<kMx>(lut, w.c[i], w.am[i], w.sb[i], xf, xr) : 0.f;
       lds_barrier();
       // each row's segments by L threads (8 where the workgroup has them),
       // then an L-lane sum; the totals go through LDS to the output columns
@@ -295,7 +294,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
       const int rr = L == 8 ? tid >> 3 : tid, k = L == 8 ? tid & 7 : 0;
       float v = 0.f;
       if (rr < R) {
-        const int gg = rr % G, ii = rr / G;                    // weight row wrow(gg, ii)
+        const int gg = rr % G, ii = rr / G;                    // weight row wrow(n0, gg, ii)
         const float* src = red + ii * kStride + gg * S;
         for (int j = k; j < S; j += L) v += src[j];
       }
@@ -304,20 +303,36 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
       if (rr < R && k == 0) red[rr] = v;
       lds_barrier();
       if (tid < Rout && n0 + tid < I)
-        act[(int64_t)p * I + n0 + tid] =
-            kMx ? unit(red[2 * tid] + bv[0], red[2 * tid + 1] + bv[1])
-                : unit(red[tid] + bv[0], red[tid + Rout] + bv[1]);
-      lds_barrier();                                           // before the next pair's partials
+        arow[n0 + tid] =
+            kMx ? unit(red[2 * tid] + bias_of(w.braw[0]), red[2 * tid + 1] + bias_of(w.braw[1]))
+                : unit(red[tid] + bias_of(w.braw[0]), red[tid + Rout] + bias_of(w.braw[1]));
+    }
+  };
+  // the next chunk's rows load while this one's are decoded (a single token
+  // has one chunk a workgroup, and so have rows that meet in LDS: their
+  // barriers keep the waves in step, and more workgroups hide them better)
+  const int step = gridDim.x * Rout;
+  int n0 = blockIdx.x * Rout;
+  Rows cur;
+  load_rows(n0, cur);
+  if constexpr (C == 0 && kWaveRows) {
+    for (; n0 + step < I; n0 += step) {
+      Rows next;
+      load_rows(n0 + step, next);
+      compute(n0, cur);
+      cur = next;
     }
   }
+  compute(n0, cur);
 }
 
 // ---- down product and combine ------------------------------------------------------
-// Grid (row chunks, tokens): output rows [n0, n0 + Rb) of one token, whose
+// Grid (row ranges, tokens): `steps` times Rb output rows of one token, whose
 // products meet in LDS.  Wave w takes slots w, w + waves, ...; its lane
 // groups (W lanes, one or two 32-weight segments a lane) take kR rows each
-// against the slot's activations, which a lane holds in registers: more rows
-// a lane where several tokens fill the chip.
+// against the slot's activations, which a lane holds in registers.  kLoop:
+// several steps a workgroup, the next step's rows loading while this one's
+// are decoded (several tokens, where the chip is full anyway).
 template <bool kMx>
 __device__ __forceinline__ float segment_dot_f32(const LutT* lut, u32x4 c, float am, uint32_t sb,
                                                  const f32x4 (&xv)[8]) {
@@ -343,22 +358,23 @@ __device__ __forceinline__ float segment_dot_f32(const LutT* lut, u32x4 c, float
   else return acc * am;
 }
 
-template <bool kMx, int kR, int kSeg>
+template <bool kMx, int kR, int kSeg, bool kLoop>
 __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ act,
     const uint8_t* __restrict__ codes, const void* __restrict__ scl, int I, int H, int topk,
-    const float* __restrict__ weights, const uint16_t* __restrict__ bias,
+    int steps, const float* __restrict__ weights, const uint16_t* __restrict__ bias,
     uint16_t* __restrict__ y) {
   __shared__ __attribute__((aligned(4096))) LutT lut[kMx ? 1 : kLutN];
-  extern __shared__ float ys[];                            // [topk][Rb]
+  extern __shared__ float ys[];                            // [topk][rows], then topk weights
 
   const int S = I >> 5;
   const int W = kSeg == 2 ? kWave : (S > 1 ? 1 << (32 - __builtin_clz(S - 1)) : 1);
   const int waves = min(topk, kDownWaves);
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int Rb = (kWave / W) * kR;
-  const int n0 = blockIdx.x * Rb;
+  const int Rb = (kWave / W) * kR;                         // rows a step
+  const int Rw = kLoop ? Rb * steps : Rb;                  // rows of the workgroup
+  const int n0 = blockIdx.x * Rw;
   const int p0 = blockIdx.y * topk;                        // the token's first pair
   const int g = lane / W, s = lane - g * W;
   bool active[kSeg];
@@ -373,11 +389,14 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
     lut_init(lut, tid, kWave * waves);
     lds_barrier();
   }
+  struct Rows {
+    u32x4 c[kR][kSeg];
+    float am[kR][kSeg];
+    uint32_t sb[kR][kSeg];
+    uint32_t braw[kR];                       // biases, raw until they are added
+  };
   for (int sl = wave; sl < topk; sl += waves) {
     const int e = ids[p0 + sl];                            // uniform
-    float tot[kR];
-#pragma unroll
-    for (int i = 0; i < kR; ++i) tot[i] = 0.f;
     f32x4 xv[kSeg][8];
 #pragma unroll
     for (int j = 0; j < kSeg; ++j) {
@@ -386,48 +405,68 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
 #pragma unroll
       for (int v = 0; v < 8; ++v) xv[j][v] = ap[v];
     }
-    if (e >= 0) {                                          // no expert: adds nothing
-      u32x4 cw[kR][kSeg];
-      float am[kR][kSeg], bv[kR];
-      uint32_t sb[kR][kSeg];
+    if (e < 0) {                                           // no expert: adds nothing
+      for (int r = lane; r < Rw; r += kWave) ys[sl * Rw + r] = 0.f;
+      continue;
+    }
+    auto load_rows = [&](int n, Rows& w) {
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
-        const int n = min(n0 + g * kR + i, H - 1);
-        const size_t row = (size_t)e * H + n;
+        const size_t row = (size_t)e * H + min(n + g * kR + i, H - 1);
 #pragma unroll
         for (int j = 0; j < kSeg; ++j) {
-          cw[i][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+          w.c[i][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
               codes + row * (size_t)(I / 2) + (size_t)s_cl[j] * 16));
           if constexpr (kMx) {
-            sb[i][j] = (uint32_t)static_cast<const uint8_t*>(scl)[row * (size_t)(I / 32) + s_cl[j]];
-            am[i][j] = 0.f;
+            w.sb[i][j] =
+                (uint32_t)static_cast<const uint8_t*>(scl)[row * (size_t)(I / 32) + s_cl[j]];
+            w.am[i][j] = 0.f;
           } else {
-            am[i][j] = static_cast<const float*>(scl)[row * (size_t)(I / 64) + s_cl[j] / 2];
-            sb[i][j] = 0u;
+            w.am[i][j] = static_cast<const float*>(scl)[row * (size_t)(I / 64) + s_cl[j] / 2];
+            w.sb[i][j] = 0u;
           }
         }
-        bv[i] = bias ? bf16_at(bias, row) : 0.f;
+        w.braw[i] = 0u;
       }
+      if (bias) {
+#pragma unroll
+        for (int i = 0; i < kR; ++i)
+          w.braw[i] = bias[(size_t)e * H + min(n + g * kR + i, H - 1)];
+      }
+    };
+    auto compute = [&](int step, const Rows& w) {
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
         float part = 0.f;
 #pragma unroll
         for (int j = 0; j < kSeg; ++j)
-          if (active[j]) part += segment_dot_f32<kMx>(lut, cw[i][j], am[i][j], sb[i][j], xv[j]);
-        tot[i] = group_sum_last(part, W) + bv[i];
+          if (active[j])
+            part += segment_dot_f32<kMx>(lut, w.c[i][j], w.am[i][j], w.sb[i][j], xv[j]);
+        const float tot = group_sum_last(part, W) + __uint_as_float(w.braw[i] << 16);
+        if (s == W - 1) ys[sl * Rw + step * Rb + g * kR + i] = tot;
       }
+    };
+    Rows cur;
+    load_rows(n0, cur);
+    if constexpr (kLoop) {
+      for (int st = 0; st + 1 < steps; ++st) {
+        Rows next;
+        load_rows(n0 + (st + 1) * Rb, next);
+        compute(st, cur);
+        cur = next;
+      }
+      compute(steps - 1, cur);
+    } else {
+      compute(0, cur);
     }
-#pragma unroll
-    for (int i = 0; i < kR; ++i)
-      if (s == W - 1) ys[sl * Rb + g * kR + i] = tot[i];
   }
-  float* wts = ys + topk * Rb;
+  float* wts = ys + topk * Rw;
   if (tid < topk) wts[tid] = w_own;
   lds_barrier();
   // thread r sums its row's slots in order
-  for (int r = tid; r < Rb; r += kWave * waves) {
+  for (int r = tid; r < Rw; r += kWave * waves) {
     float acc = 0.f;
-    for (int sl = 0; sl < topk; ++sl) acc = __builtin_fmaf(wts[sl], ys[sl * Rb + r], acc);
+    for (int sl = 0; sl < topk; ++sl) acc = __builtin_fmaf(wts[sl], ys[sl * Rw + r], acc);
     if (n0 + r < H) y[(int64_t)blockIdx.y * H + n0 + r] = f32_to_bf16_bits(acc);
   }
 }
@@ -471,20 +510,14 @@ static int layer_checks(const gq_moe_layer* l) {
   return kOk;
 }
 
-template <bool kMx, int kIter, int C>
-static void launch_gate_up(dim3 grid, int NT, bool wave_rows, hipStream_t stream,
-                           const gq_moe_layer& l, const float* logits, const uint16_t* x,
-                           int x_stride, int rows, int32_t* ids, float* w, float* act) {
-  if (wave_rows)
-    hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, true, C>), grid, dim3(NT), 0, stream,
-                       logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden, l.inner,
-                       l.num_experts, x_stride, l.topk, rows, l.gate_up_bias, l.alpha, l.limit,
-                       l.renormalize, ids, w, act);
-  else
-    hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, false, C>), grid, dim3(NT), 0, stream,
-                       logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden, l.inner,
-                       l.num_experts, x_stride, l.topk, rows, l.gate_up_bias, l.alpha, l.limit,
-                       l.renormalize, ids, w, act);
+template <bool kMx, int kIter, bool kWaveRows, int C>
+static void launch_gate_up(int chunks, int NT, hipStream_t stream, const gq_moe_layer& l,
+                           const float* logits, const uint16_t* x, int x_stride, int rows,
+                           int32_t* ids, float* w, float* act) {
+  hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, kWaveRows, C>), dim3(chunks, rows * l.topk),
+                     dim3(NT), 0, stream, logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden,
+                     l.inner, l.num_experts, x_stride, l.topk, l.gate_up_bias, l.alpha,
+                     l.limit, l.renormalize, ids, w, act);
 }
 
 template <bool kMx, int C>
@@ -494,26 +527,55 @@ static void gate_up(hipStream_t stream, const gq_moe_layer& l, const float* logi
   const int N = 2 * l.inner, P = rows * l.topk;
   int S, W, G, NT;
   segment_layout(l.hidden, S, W, G, NT);
-  // rows per thread as in the decode GEMV: the largest count that still
-  // gives about eight workgroups per CU (two where rows are reduced in LDS)
+  auto chunks = [&](int iter) { return (N + G * iter - 1) / (G * iter); };
+  auto go = [&](auto iter, auto wave_rows, int n) {
+    launch_gate_up<kMx, decltype(iter)::value, decltype(wave_rows)::value, C>(
+        n, NT, stream, l, logits, x, x_stride, rows, ids, w, act);
+  };
+  using I2 = std::integral_constant<int, 2>;
+  using I4 = std::integral_constant<int, 4>;
+  using I8 = std::integral_constant<int, 8>;
+  if (C == 0 && S <= kWave) {
+    // several tokens: four rows a thread, as many workgroups as the chip
+    // holds at once (four a CU), each running on over its chunks
+    go(I4{}, std::true_type{}, std::min(chunks(4), std::max(1, 1024 / P)));
+    return;
+  }
+  // one chunk a workgroup; rows a thread as in the decode GEMV: the largest
+  // count that still gives about eight workgroups per CU (two where rows are
+  // reduced in LDS)
   const int64_t want = S <= kWave ? 2048 : 512;
-  int iter = 8;
-  while (iter > 2 && (int64_t)((N + G * iter - 1) / (G * iter)) * P < want) iter >>= 1;
-  const dim3 grid((N + G * iter - 1) / (G * iter), (unsigned)P);
-  const bool wr = S <= kWave;
-  if (iter == 8) launch_gate_up<kMx, 8, C>(grid, NT, wr, stream, l, logits, x, x_stride, rows, ids, w, act);
-  else if (iter == 4) launch_gate_up<kMx, 4, C>(grid, NT, wr, stream, l, logits, x, x_stride, rows, ids, w, act);
-  else launch_gate_up<kMx, 2, C>(grid, NT, wr, stream, l, logits, x, x_stride, rows, ids, w, act);
+  const int iter = chunks(8) * (int64_t)P >= want ? 8 : chunks(4) * (int64_t)P >= want ? 4 : 2;
+  auto by_rows = [&](auto wave_rows) {
+    if (iter == 8) go(I8{}, wave_rows, chunks(8));
+    else if (iter == 4) go(I4{}, wave_rows, chunks(4));
+    else go(I2{}, wave_rows, chunks(2));
+  };
+  if (S > kWave) by_rows(std::false_type{});
+  else if constexpr (C > 0) by_rows(std::true_type{});
 }
 
-template <bool kMx, int kR, int kSeg>
+template <bool kMx, int kSeg>
 static void launch_down(hipStream_t stream, const gq_moe_layer& l, int W, int rows,
                         const int32_t* ids, const float* w, const float* act, uint16_t* y) {
+  constexpr int kR = 4;
   const int Rb = (kWave / W) * kR;
-  hipLaunchKernelGGL((moe_down_kernel<kMx, kR, kSeg>), dim3((l.hidden + Rb - 1) / Rb, rows),
-                     dim3(kWave * std::min(l.topk, kDownWaves)), (size_t)l.topk * (Rb + 1) * 4,
-                     stream, ids, act, l.down_codes, l.down_scales, l.inner, l.hidden, l.topk, w,
-                     l.down_bias, y);
+  // steps a workgroup: while two workgroups a CU remain (and the rows of all
+  // slots fit 16 KB of LDS)
+  int64_t groups = (l.hidden + Rb - 1) / Rb;
+  int steps = 1;
+  while (groups / (2 * steps) * rows >= 512 && l.topk * Rb * 2 * steps <= 4096) steps *= 2;
+  groups = (groups + steps - 1) / steps;
+  const dim3 grid((unsigned)groups, rows), block(kWave * std::min(l.topk, kDownWaves));
+  const size_t lds = (size_t)l.topk * (Rb * steps + 1) * 4;
+  if (steps > 1)
+    hipLaunchKernelGGL((moe_down_kernel<kMx, kR, kSeg, true>), grid, block, lds, stream, ids, act,
+                       l.down_codes, l.down_scales, l.inner, l.hidden, l.topk, steps, w,
+                       l.down_bias, y);
+  else
+    hipLaunchKernelGGL((moe_down_kernel<kMx, kR, kSeg, false>), grid, block, lds, stream, ids, act,
+                       l.down_codes, l.down_scales, l.inner, l.hidden, l.topk, steps, w,
+                       l.down_bias, y);
 }
 
 template <bool kMx>
@@ -545,10 +607,8 @@ static void moe_decode(hipStream_t stream, const gq_moe_layer& l, const uint16_t
   }
   int S, W, G, NT;
   segment_layout(l.inner, S, W, G, NT);
-  const bool many = rows > 2;
-  if (S > kWave) launch_down<kMx, 4, 2>(stream, l, kWave, rows, ids, w, act, y);
-  else if (many) launch_down<kMx, 8, 1>(stream, l, W, rows, ids, w, act, y);
-  else launch_down<kMx, 2, 1>(stream, l, W, rows, ids, w, act, y);
+  if (S > kWave) launch_down<kMx, 2>(stream, l, kWave, rows, ids, w, act, y);
+  else launch_down<kMx, 1>(stream, l, W, rows, ids, w, act, y);
 }
 
 }  // namespace gq
