@@ -41,6 +41,7 @@ struct GemmArgs {
   const int32_t* num_tiles;
   int n_col_tiles;             // ceil(Nout / output columns per tile)
   int n_logical;               // max_tiles * n_col_tiles
+  int max_tiles;               // entries of the tile list (gemm_fp4.hip)
   uint16_t* out;               // [P, Nout]
   float act_alpha, act_limit;  // gpt-oss gated unit (kernels with the activation epilogue)
   uint8_t* out_q;              // gated unit written as its two-term e4m3 split instead of

@@ -48,6 +48,51 @@ __device__ __forceinline__ void store_unit(const float (&v)[16], uint16_t* orow,
   *reinterpret_cast<u32x4*>(orow + 8 * lh) = u32x4{a[0], a[1], b[0], b[1]};
 }
 
+// The tile of a workgroup.  Blocks are dealt to the 8 XCDs in turn, each with
+// an L2 of its own; kGroup column tiles of a row tile go to one XCD, which so
+// fetches the tile's activations for all of them, and row tiles, full and
+// short ones, spread evenly (8192 pairs on 32 experts, gate_up / down: all
+// column tiles of a row tile on one XCD 162 / 79 us, one column tile at a
+// time 154 / 92, four 157 / 81).  Tiles past the last expert tile clear the
+// rows of dropped pairs.  A tile entry that cannot come from gq_route_sort is
+// rejected.
+constexpr int kGroup = 4;
+template <int kTNo>
+__device__ __forceinline__ bool fp4_head(const GemmArgs& g, int tid, TileInfo& t, int& pair) {
+  const int bid = blockIdx.x;
+  const int q = bid >> 3, xcd = bid & 7;
+  const int groups = (g.n_col_tiles + kGroup - 1) / kGroup;
+  const int unit = (q / kGroup) * 8 + xcd;
+  const int tile = unit / groups;
+  const int col = (unit % groups) * kGroup + q % kGroup;
+  if (tile >= g.max_tiles || col >= g.n_col_tiles) return false;
+  t.n0 = col * kTNo;
+  // the tile count and the tile's entry in one round trip (entries past the
+  // count hold no expert)
+  const int T = *g.num_tiles;
+  t.e = g.tiles[2 * tile];
+  t.start = g.tiles[2 * tile + 1];
+  if (tile >= T) {
+    const int dstart = g.offsets[g.E] + (tile - T) * kTM;
+    if (dstart >= g.P || dstart < 0) return false;
+    const int dvalid = min(kTM, g.P - dstart);
+    for (int idx = tid; idx < dvalid * (kTNo / 8); idx += kGemmThreads) {
+      const int r = idx / (kTNo / 8), c = t.n0 + idx % (kTNo / 8) * 8;
+      const int p = g.sorted_pairs[dstart + r];
+      if (c < g.Nout && (unsigned)p < (unsigned)g.P)
+        *reinterpret_cast<u32x4*>(g.out + (int64_t)p * g.Nout + c) = u32x4{0u, 0u, 0u, 0u};
+    }
+    return false;
+  }
+  if ((unsigned)t.e >= (unsigned)g.E || (unsigned)t.start >= (unsigned)g.P) return false;
+  // the segment's end and its pairs in the next
+  const int end = g.offsets[t.e + 1];
+  const int p = g.sorted_pairs[min(t.start + tid, g.P - 1)];
+  t.valid = min(kTM, min(end, g.P) - t.start);
+  pair = (unsigned)p < (unsigned)g.P ? p : 0;
+  return t.valid > 0;
+}
+
 // kWide: waves 2 x 2, a wave takes every second 32-row sub-tile (so that the
 // row halves stay balanced when the tile is not full) and 128 columns; else
 // (tiles of at most 128 rows) four waves side by side, 64 columns each.
@@ -55,27 +100,22 @@ template <bool kWide, bool kUnit>
 __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, int tid,
                                          uint8_t* A0, uint8_t* A1, uint8_t* B0, uint8_t* B1,
                                          u32x2* SA0, u32x2* SA1, u32x2* SB0, u32x2* SB1,
-                                         int* pair_s, int* row_s, float* scale_s) {
+                                         int* pair_s, int* row_s, float* scale_s, int pair) {
   constexpr int kC = kWide ? 4 : 2;                       // column blocks of a wave
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 31, lh = lane >> 5;
   const int nb = g.Kw / 32;                               // K blocks
   const int nstages = (nb + 7) / 8;
-  {
-    int p = g.sorted_pairs[t.start + min(tid, t.valid - 1)];
-    p = ((unsigned)p < (unsigned)g.P) ? p : 0;
-    pair_s[tid] = p;
-    row_s[tid] = p / g.topk;
-    scale_s[tid] = g.pair_scale ? g.pair_scale[p] : 1.f;
-  }
+  const int xrow = pair / g.topk;                         // (rows past the tile: some other pair's)
+  pair_s[tid] = pair;
+  row_s[tid] = xrow;
   const int wn0 = kUnit ? 2 * t.n0 : t.n0;                // first weight row of the tile
-  const uint8_t* as_row = g.xs + (size_t)row_s[tid] * g.xs_stride;
+  const uint8_t* as_row = g.xs + (size_t)xrow * g.xs_stride;
   const uint8_t* bs_row = static_cast<const uint8_t*>(g.scl) +
                           ((size_t)t.e * g.Nw + min(wn0 + tid, g.Nw - 1)) * (size_t)nb;
   const char* abase = reinterpret_cast<const char*>(g.x);
   const char* bbase = reinterpret_cast<const char*>(g.codes) +
                       (size_t)t.e * g.Nw * (size_t)(g.Kw / 2);
-  lds_barrier();
 
   // ---- loads: 8 rows of 128 bytes per instruction, rows 8 (4 j + wave) + ..;
   // lane L fills the 16-byte slot L % 8 of row L / 8 with the chunk that the
@@ -88,11 +128,8 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
   constexpr int kJA = kWide ? 8 : 4;                      // 8-row groups of activations a wave loads
   uint32_t aoff[kJA], boff[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = 8 * (4 * j + wave) + (lane >> 3);
-    if (j < kJA) aoff[j] = (uint32_t)row_s[r] * row_bytes;
-    boff[j] = (uint32_t)min(wn0 + r, g.Nw - 1) * row_bytes;
-  }
+  for (int j = 0; j < 8; ++j)
+    boff[j] = (uint32_t)min(wn0 + 8 * (4 * j + wave) + (lane >> 3), g.Nw - 1) * row_bytes;
   auto next_chunk = [&](int ks) { return 16u * min((uint32_t)ks * 8 + chunk, (uint32_t)(nb - 1)); };
   // load v of a stage: 0 to 7 weight rows, then activation rows
   auto load_rows = [&](int v, uint32_t c, uint8_t* A, uint8_t* B) {
@@ -144,11 +181,23 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][c][r] = 0.f;
 
-  SA0[tid] = first_scales(as_row);
-  SB0[tid] = first_scales(bs_row);
+  // first stage: the weight rows need no routing and go first
 #pragma unroll
-  for (int v = 0; v < kJA + 8; ++v) load_rows(v, next_chunk(0), A0, B0);
+  for (int v = 0; v < 8; ++v) load_rows(v, next_chunk(0), A0, B0);
+  const u32x2 sa_first = first_scales(as_row), sb_first = first_scales(bs_row);
+  lds_barrier();                                          // row_s
+#pragma unroll
+  for (int j = 0; j < kJA; ++j)
+    aoff[j] =
+        (uint32_t)row_s[min(8 * (4 * j + wave) + (lane >> 3), t.valid - 1)] * row_bytes;
+#pragma unroll
+  for (int v = 8; v < kJA + 8; ++v) load_rows(v, next_chunk(0), A0, B0);
+  // the pairs' weights arrive with the first stage; added after the loop
+  const float own_scale = !kUnit && g.pair_scale ? g.pair_scale[pair] : 1.f;
+  SA0[tid] = sa_first;
+  SB0[tid] = sb_first;
   __builtin_amdgcn_s_waitcnt(0);
+  scale_s[tid] = own_scale;
   lds_barrier();
 
   auto run_loop = [&](auto rows_c) {
@@ -299,11 +348,14 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_fp4_kernel(GemmA
   __shared__ float scale_s[kTM];
   const int tid = threadIdx.x;
   TileInfo t;
-  if (!tile_head<kUnit ? kXN / 2 : kXN>(g, tid, t)) return;
+  int pair = 0;
+  if (!fp4_head<kUnit ? kXN / 2 : kXN>(g, tid, t, pair)) return;
   if (t.valid <= kF4Small)
-    fp4_tile<false, kUnit>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s, scale_s);
+    fp4_tile<false, kUnit>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s, scale_s,
+                           pair);
   else
-    fp4_tile<true, kUnit>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s, scale_s);
+    fp4_tile<true, kUnit>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s, scale_s,
+                           pair);
 }
 
 template <bool kUnit>
@@ -344,11 +396,10 @@ static int fp4_entry(const uint8_t* x_blocks, const uint8_t* x_scales, int32_t r
   g.num_tiles = num_tiles; g.out = out;
   g.act_alpha = alpha; g.act_limit = limit;
   g.n_col_tiles = (N + kXN - 1) / kXN;                     // 256 weight rows per tile
-  const int64_t n_logical = (int64_t)max_tiles * g.n_col_tiles;
-  const int64_t group = 8LL * g.n_col_tiles;
-  const int64_t grid = ((n_logical + group - 1) / group) * group;
+  const int64_t units = (int64_t)max_tiles * ceil_div64(g.n_col_tiles, kGroup);
+  const int64_t grid = ceil_div64(units, 8) * 8 * kGroup;
   if (grid > INT32_MAX) return kNotSupported;
-  g.n_logical = (int)n_logical;
+  g.max_tiles = max_tiles;
   hipLaunchKernelGGL(grouped_gemm_fp4_kernel<kUnit>, dim3((unsigned)grid), dim3(kGemmThreads), 0,
                      stream, g);
   return launch_status();

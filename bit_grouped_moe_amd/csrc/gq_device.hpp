@@ -157,14 +157,15 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 // SiLU, z * sigmoid(z), in float32.
 __device__ __forceinline__ float silu_f32(float z) { return z * sigmoid_f32(z); }
 
-// gpt-oss's gated unit of one (gate, up) pair with the gate clamped above at
-// `limit` and the up value clipped to [-limit, limit]; compares and selects
-// keep a NaN, which the minimum and maximum instructions would drop.
+// gpt-oss's gated unit of one (gate, up) pair: the gate clamped above at
+// `limit`, the up value clipped to [-limit, limit].  The gfx950 minimum and
+// maximum keep a NaN (fminf and fmaxf would drop it), one instruction each.
 __device__ __forceinline__ float clamped_unit(float gate, float up, float alpha, float limit) {
-  const float gc = gate > limit ? limit : gate;
-  const float hi = up > limit ? limit : up;
-  const float uc = hi < -limit ? -limit : hi;
-  return gc * sigmoid_f32(alpha * gc) * (uc + 1.0f);
+  const float gc = __builtin_elementwise_minimum(gate, limit);
+  const float uc =
+      __builtin_elementwise_minimum(__builtin_elementwise_maximum(up, -limit), limit);
+  const float a = gc * sigmoid_f32(alpha * gc);
+  return __builtin_fmaf(a, uc, a);
 }
 
 // ---- MXFP4 ---------------------------------------------------------------
