@@ -163,6 +163,9 @@ def _stream(t):
 
 
 def _dev(t, name, dtype, ndim=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (ndim is None or t.dim() == ndim)):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -250,11 +253,11 @@ def gq_mxfp4_decode(blocks, scales, out_f32=True, out_bf16=True):
 
 
 def _x_args(x, name="x"):
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda" or x.dtype != torch.bfloat16:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be a bf16 device tensor")
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    return x.shape[0], x.shape[1], x.stride(0)
+    return *x.shape, x.stride(0)
 
 
 def _nf4_bank(codes, absmax):
@@ -271,7 +274,7 @@ def _mx_bank(blocks, scales):
     _dev(blocks, "blocks", torch.uint8, 4)
     _dev(scales, "scales", torch.uint8, 3)
     E, N, nb, sixteen = blocks.shape
-    if sixteen != 16 or tuple(scales.shape) != (E, N, nb):
+    if sixteen != 16 or scales.shape != (E, N, nb):
         raise ValueError("blocks must be [E, N, K/32, 16] and scales [E, N, K/32]")
     return E, N, nb * 32
 
@@ -781,9 +784,9 @@ def _mx_pair(x, blocks, scales, unit):
     _dev(xb, "x blocks", torch.uint8, 3)
     _dev(xs, "x scales", torch.uint8, 2)
     E, N, K = _mx_bank(blocks, scales)
-    rows = xb.shape[0]
-    if tuple(xb.shape) != (rows, K // 32, 16) or tuple(xs.shape) != (rows, K // 32):
-        raise ValueError(f"x must be (blocks [rows, {K // 32}, 16], scales [rows, {K // 32}]) as "
+    rows, nb = xb.shape[0], K // 32
+    if xb.shape != (rows, nb, 16) or xs.shape != (rows, nb):
+        raise ValueError(f"x must be (blocks [rows, {nb}, 16], scales [rows, {nb}]) as "
                          "gq_mxfp4_quantize returns them")
     if unit and N % 2:
         raise ValueError("the gate_up width is odd")
