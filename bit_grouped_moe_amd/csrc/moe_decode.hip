@@ -99,7 +99,7 @@ __device__ __forceinline__ int moe_select(const float* __restrict__ logits, int 
   }
   int id;
   float z;
-  wave_topk<C>(key, slots, lane, id, z);
+  wave_topk<C>(key, slots, id, z);
   if (write) {
     const float peak = row_peak(z, id);
     const float part = id >= 0 ? expf(z - peak) : 0.f;

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_kernel(
   for (int c = 0; c < C; ++c) all[c] = key[c];
   int id;
   float z;
-  wave_topk<C>(key, topk, lane, id, z);
+  wave_topk<C>(key, topk, id, z);
   const float peak = row_peak(z, id);
   const float part = id >= 0 ? expf(z - peak) : 0.f;
   float total = part;

@@ -8,6 +8,11 @@
 
 namespace gq {
 
+// v with lane `lane` (uniform) set to `value` (uniform): v_writelane_b32, which
+// the compiler offers as an intrinsic only.
+__device__ uint32_t wave_writelane(uint32_t value, uint32_t lane, uint32_t v) __asm(
+    "llvm.amdgcn.writelane.i32");
+
 constexpr int kTopkMax = 64;                 // slots: one per lane
 constexpr int kTopkMaxExperts = 1024;        // 16 logits per lane
 
@@ -48,34 +53,35 @@ __device__ __forceinline__ float wave_fsum(float v) {
 
 // The topk largest of the row's logits, largest first, equal ones by lower
 // index.  Lane l holds experts 64 c + l in key[c]; lane s < topk receives
-// slot s (id -1 where only masked experts are left).  One wave maximum and
-// at most C ballots a slot, no memory.
+// slot s (id -1 where only masked experts are left).  A round is a wave
+// maximum and C ballots; the place of the first match is scalar, and the
+// slot's values and the taken key are written with v_writelane: 20 VALU
+// instructions a round for 128 experts, 30 with selects on the lane number
+// (one-token NF4 layer 14.60 -> 14.47 us).  No memory.
 template <int C>
-__device__ __forceinline__ void wave_topk(uint32_t (&key)[C], int topk, int lane, int& id,
-                                          float& logit) {
-  id = -1;
-  logit = -__builtin_inff();
+__device__ __forceinline__ void wave_topk(uint32_t (&key)[C], int topk, int& id, float& logit) {
+  uint32_t ids = 0xFFFFFFFFu, won = kDeadKey;
   for (int s = 0; s < topk; ++s) {
     uint32_t best = key[0];
 #pragma unroll
     for (int c = 1; c < C; ++c) best = max(best, key[c]);
     const uint32_t m = wave_umax(best);
     if (m <= kDeadKey) break;                            // uniform
+    won = wave_writelane(m, s, won);
     bool open = true;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const uint64_t at = __ballot(key[c] == m);
-      if (open && at) {
+      if (open && at) {                                  // uniform
         open = false;
         const int l = __builtin_ctzll(at);
-        if (lane == l) key[c] = 0u;
-        if (lane == s) {
-          id = 64 * c + l;
-          logit = key_logit(m);
-        }
+        key[c] = wave_writelane(0u, l, key[c]);
+        ids = wave_writelane((uint32_t)(64 * c + l), s, ids);
       }
     }
   }
+  id = (int)ids;
+  logit = key_logit(won);
 }
 
 // The row's largest logit (slot 0's); 0 where every expert is masked.
