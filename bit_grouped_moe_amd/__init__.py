@@ -154,8 +154,9 @@ def _check(status, what):
 
 # The raw handle of a device's current stream, without the Stream object that
 # torch.cuda.current_stream builds (1.9 us against 0.1 us, of a decode call
-# that takes about 10).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# that takes about 10); a torch built without it takes the slower way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream(t):
@@ -719,7 +720,7 @@ def _beside(index, *tensors):
 def _on(index, fn, what, *args):
     """Call the library on the current stream of device ``index``, with that
     device current."""
-    if torch._C._cuda_getDevice() == index:
+    if torch.cuda.current_device() == index:
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -749,7 +750,8 @@ def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
     """MXFP4 of x [..., K] (float32, bfloat16 or float16, any row stride):
     returns (blocks uint8 [..., K/32, 16], scales uint8 [..., K/32]), the
     layout that the MXFP4 entry points take.  ``values``: True or a bf16
-    tensor of x's shape also returns the values that the codes stand for."""
+    tensor of x's shape (x itself, if bf16 and contiguous) also returns the
+    values that the codes stand for."""
     lib = _lib or load_library()
     code = _typed(x, "x")
     dev, index = x.device, x.get_device()

@@ -36,6 +36,7 @@ constexpr int kMoeMaxHidden = 8192;          // 256 segments of 32 weights
 constexpr int kMoeMaxInner = 128 * 32;       // two segments per lane
 constexpr int kMoeThreads = 256;
 constexpr int kDownWaves = 8;
+constexpr int kDownLanes = 8;                // of a row at least: bounds the rows a workgroup keeps
 
 // ---- logits of one expert for every token -------------------------
 // Workgroup e; thread t takes the 16-byte pieces t, t + 256, ... of the
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
   extern __shared__ float ys[];                            // [topk][rows], then topk weights
 
   const int S = I >> 5;
-  const int W = kSeg == 2 ? kWave : (S > 1 ? 1 << (32 - __builtin_clz(S - 1)) : 1);
+  const int W = kSeg == 2 ? kWave : max(kDownLanes, S > 1 ? 1 << (32 - __builtin_clz(S - 1)) : 1);
   const int waves = min(topk, kDownWaves);
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -608,7 +609,7 @@ static void moe_decode(hipStream_t stream, const gq_moe_layer& l, const uint16_t
   int S, W, G, NT;
   segment_layout(l.inner, S, W, G, NT);
   if (S > kWave) launch_down<kMx, 2>(stream, l, kWave, rows, ids, w, act, y);
-  else launch_down<kMx, 1>(stream, l, W, rows, ids, w, act, y);
+  else launch_down<kMx, 1>(stream, l, std::max(W, kDownLanes), rows, ids, w, act, y);
 }
 
 }  // namespace gq

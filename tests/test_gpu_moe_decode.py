@@ -111,6 +111,11 @@ def _x(case, rows, std=1.0):
     ("mxfp4", 3, 2080, 96, 2, 3, False, True),
     ("mxfp4", 6, 544, 4096, 6, 8, True, False),
     ("mxfp4", 2, 8192, 96, 2, 1, True, True),
+    ("mxfp4", 70, 32, 32, 64, 1, True, True),          # as many slots as the wave has lanes
+    ("mxfp4", 500, 64, 64, 64, 1, False, False),
+    ("nf4", 66, 64, 64, 32, 2, True, True),
+    ("nf4", 8, 64, 4096, 8, 8, True, True),
+    ("mxfp4", 5, 96, 2080, 1, 8, False, True),
 ])
 def test_layer(fmt, E, H, I, topk, rows, bias, renorm):
     dev = device()

@@ -114,6 +114,18 @@ def test_requantising_decoded_values_reproduces_the_bytes():
     assert torch.equal(f32, values.float())
 
 
+def test_values_in_place():
+    """The values may replace bf16 inputs."""
+    dev = device()
+    x = torch.randn(37, 2880, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(dev)
+    say("quantize in place")
+    ref = gq.gq_mxfp4_quantize(x, values=True)
+    got = gq.gq_mxfp4_quantize(x, values=x)
+    torch.cuda.synchronize()
+    assert got[2] is x
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
 def test_leading_dimensions_given_buffers_and_untouched_neighbours():
     dev = device()
     x = torch.randn(3, 5, 96, generator=torch.Generator().manual_seed(5)).to(dev)
