@@ -11,6 +11,8 @@ Build the library with ``python -m bit_grouped_moe_amd.build``.
 """
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from collections import namedtuple
 
@@ -114,6 +116,7 @@ _SIGNATURES = {
 }
 
 _lib = None
+_calls = None                      # the short calls (csrc/binding/calls.cpp), when built
 
 
 class GQError(RuntimeError):
@@ -143,7 +146,29 @@ def load_library():
         fn.restype = res
         fn.argtypes = args
     _lib = lib
+    _load_calls(lib)
     return lib
+
+
+def _load_calls(lib):
+    """Load the short calls and hand them the library's entry points.  Without
+    them (not built, or built against another torch) every call takes the
+    Python way, with the same checks, kernels and results."""
+    global _calls
+    path = os.path.join(_HERE, "_calls.so")
+    if not os.path.exists(path):
+        return
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+        loader.exec_module(mod)
+    except ImportError:
+        return
+    if mod.torch_version != torch.__version__:
+        return
+    mod.bind({n: ctypes.cast(getattr(lib, n), _p).value for n in EXPORTED_SYMBOLS},
+             torch.cuda.current_device, _raw_stream)
+    _calls = mod
 
 
 def _check(status, what):
@@ -184,6 +209,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _done(result, what):
+    """A short call's outputs; its status, if it is one, as an error."""
+    if type(result) is int:
+        _check(result, what)
+    return result
+
+
 Route = namedtuple("Route", "expert_offsets sorted_pairs tiles num_tiles max_tiles tile_m "
                             "rows topk num_experts")
 
@@ -196,6 +228,11 @@ def gq_route_sort(topk_ids, num_experts, tile_m=TILE_M, expert_offsets=None, sor
                   tiles=None, num_tiles=None):
     """Group the (token, slot) pairs of ``topk_ids`` int32 [rows, topk] by expert."""
     lib = _lib or load_library()
+    if _calls and expert_offsets is sorted_pairs is tiles is num_tiles is None:
+        r = _calls.route_sort(topk_ids, num_experts, tile_m)
+        if r is not None:
+            r = _done(r, "gq_route_sort")
+            return Route(*r, r[2].shape[0], tile_m, *topk_ids.shape, num_experts)
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     rows, topk = topk_ids.shape
     dev = topk_ids.device
@@ -753,6 +790,10 @@ def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
     tensor of x's shape (x itself, if bf16 and contiguous) also returns the
     values that the codes stand for."""
     lib = _lib or load_library()
+    if _calls and blocks is scales is None and (values is None or values is True):
+        r = _calls.quantize(x, values is True)
+        if r is not None:
+            return _done(r, "gq_mxfp4_quantize")
     code = _typed(x, "x")
     dev, index = x.device, x.get_device()
     rows, K, stride = _rows(x, "x")
@@ -796,25 +837,32 @@ def _mx_pair(x, blocks, scales, unit):
     return xb, xs, rows, E, N, K
 
 
-def _fp4_gemm(what, x, blocks, scales, route, middle, N_out, pair_scale, out):
-    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, N_out is None)
+def _fp4_gemm(what, x, blocks, scales, route, unit, pair_scale, out):
+    lib = _lib or load_library()
+    if _calls and out is None:
+        r = _calls.fp4_gemm(x[0], x[1], blocks, scales, route, pair_scale, unit is not None,
+                            *(unit or (0.0, 0.0)))
+        if r is not None:
+            return _done(r, what)
+    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit is not None)
     if route.rows != rows or route.num_experts != E:
         raise ValueError("x, blocks and route disagree")
+    for name in ("expert_offsets", "sorted_pairs", "tiles", "num_tiles"):
+        _dev(getattr(route, name), "route." + name, torch.int32)
     index = xb.get_device()
     P = rows * route.topk
-    out = _out(out, P, N // 2 if N_out is None else N, xb.device)
+    out = _out(out, P, N // 2 if unit else N, xb.device)
     _beside(index, out, pair_scale, route.sorted_pairs)
-    args = [xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(), scales.data_ptr(), E, N,
-            route.topk, *middle(P), *_route_ptrs(route), out.data_ptr()]
-    _on(index, getattr(_lib or load_library(), what), what, *args)
+    middle = unit or (_ptr(_scale(pair_scale, P)),)
+    _on(index, getattr(lib, what), what, xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(),
+        scales.data_ptr(), E, N, route.topk, *middle, *_route_ptrs(route), out.data_ptr())
     return out
 
 
 def gq_mxfp4_grouped_gemm_fp4(x, blocks, scales, route, pair_scale=None, out=None):
     """Prefill grouped GEMM of MXFP4 activations with MXFP4 experts; ``x`` =
     gq_mxfp4_quantize(activations [rows, K]).  Returns bf16 [rows*topk, N]."""
-    return _fp4_gemm("gq_mxfp4_grouped_gemm_fp4", x, blocks, scales, route,
-                     lambda P: (_ptr(_scale(pair_scale, P)),), True, pair_scale, out)
+    return _fp4_gemm("gq_mxfp4_grouped_gemm_fp4", x, blocks, scales, route, None, pair_scale, out)
 
 
 def gq_mxfp4_grouped_gemm_fp4_swiglu(x, blocks, scales, route, alpha=OSS_ALPHA, limit=OSS_LIMIT,
@@ -822,27 +870,33 @@ def gq_mxfp4_grouped_gemm_fp4_swiglu(x, blocks, scales, route, alpha=OSS_ALPHA, 
     """gq_mxfp4_grouped_gemm_fp4 on gate_up experts [E, 2I, K] (gate row 2j,
     up row 2j + 1) with gpt-oss's gated unit: bf16 [rows*topk, I]."""
     return _fp4_gemm("gq_mxfp4_grouped_gemm_fp4_swiglu", x, blocks, scales, route,
-                     lambda P: (float(alpha), float(limit)), None, None, out)
+                     (float(alpha), float(limit)), None, out)
 
 
-def _fp4_gemv(what, x, blocks, scales, topk_ids, middle, unit, pair_scale, out):
-    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit)
+def _fp4_gemv(what, x, blocks, scales, topk_ids, unit, pair_scale, out):
+    lib = _lib or load_library()
+    if _calls and out is None:
+        r = _calls.fp4_gemv(x[0], x[1], blocks, scales, topk_ids, pair_scale, unit is not None,
+                            *(unit or (0.0, 0.0)))
+        if r is not None:
+            return _done(r, what)
+    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit is not None)
     index = xb.get_device()
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     P = _gemv_pairs(topk_ids, rows)
     out = _out(out, P, N // 2 if unit else N, xb.device)
     _beside(index, out, pair_scale, topk_ids)
-    _on(index, getattr(_lib or load_library(), what), what, xb.data_ptr(), xs.data_ptr(), rows, K,
-        blocks.data_ptr(), scales.data_ptr(), E, N, topk_ids.data_ptr(), topk_ids.shape[1],
-        *middle(P), out.data_ptr())
+    middle = unit or (_ptr(_scale(pair_scale, P)),)
+    _on(index, getattr(lib, what), what, xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(),
+        scales.data_ptr(), E, N, topk_ids.data_ptr(), topk_ids.shape[1], *middle, out.data_ptr())
     return out
 
 
 def gq_mxfp4_grouped_gemv_fp4(x, blocks, scales, topk_ids, pair_scale=None, out=None):
     """Decode-time product (<= 256 pairs) of MXFP4 activations with MXFP4
     experts; ``x`` = gq_mxfp4_quantize(activations).  Returns bf16 [rows*topk, N]."""
-    return _fp4_gemv("gq_mxfp4_grouped_gemv_fp4", x, blocks, scales, topk_ids,
-                     lambda P: (_ptr(_scale(pair_scale, P)),), False, pair_scale, out)
+    return _fp4_gemv("gq_mxfp4_grouped_gemv_fp4", x, blocks, scales, topk_ids, None, pair_scale,
+                     out)
 
 
 def gq_mxfp4_grouped_gemv_fp4_swiglu(x, blocks, scales, topk_ids, alpha=OSS_ALPHA,
@@ -850,7 +904,7 @@ def gq_mxfp4_grouped_gemv_fp4_swiglu(x, blocks, scales, topk_ids, alpha=OSS_ALPH
     """gq_mxfp4_grouped_gemv_fp4 on gate_up experts with gpt-oss's gated unit:
     bf16 [rows*topk, I]."""
     return _fp4_gemv("gq_mxfp4_grouped_gemv_fp4_swiglu", x, blocks, scales, topk_ids,
-                     lambda P: (float(alpha), float(limit)), True, None, out)
+                     (float(alpha), float(limit)), None, out)
 
 
 # ---- expert routing --------------------------------------------------------------
@@ -861,6 +915,10 @@ def gq_moe_topk(logits, topk, renormalize=True, topk_ids=None, topk_weights=None
     chosen logits (``renormalize``) or over all.  A logit of -inf is never
     chosen; a slot left without an expert has id -1 and weight 0."""
     lib = _lib or load_library()
+    if _calls and topk_ids is topk_weights is None:
+        r = _calls.moe_topk(logits, topk, bool(renormalize))
+        if r is not None:
+            return _done(r, "gq_moe_topk")
     code = _typed(logits, "logits")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
@@ -887,6 +945,10 @@ def gq_moe_topk_backward(d_weights, logits, topk_ids, renormalize=True, out=None
     """Gradient of ``gq_moe_topk``'s weights to its logits, the selection held
     fixed: d_weights float32 [rows, topk] -> [rows, E] of the logits' type."""
     lib = _lib or load_library()
+    if _calls and out is None:
+        r = _calls.moe_topk_backward(d_weights, logits, topk_ids, bool(renormalize))
+        if r is not None:
+            return _done(r, "gq_moe_topk_backward")
     code = _typed(logits, "logits")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
@@ -974,6 +1036,12 @@ def gq_moe_decode(layer, x, out=None, workspace=None):
     expert) pairs: bf16 [rows, H].  ``workspace``: a uint8 tensor of at least
     gq_moe_decode_workspace bytes (allocated when None)."""
     lib = _lib or load_library()
+    if _calls and out is workspace is None and isinstance(x, torch.Tensor) and x.dim() == 2:
+        need = layer._bytes.get(x.shape[0])
+        if need:
+            r = _calls.moe_decode(layer._ref, layer.device.index, need, x)
+            if r is not None:
+                return _done(r, "gq_moe_decode")
     rows, H, stride = _x_args(x)
     dev = x.device
     if H != layer.hidden:

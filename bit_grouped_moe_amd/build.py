@@ -1,5 +1,6 @@
-"""Build libgq.so (HIP kernels + C ABI) and libgq_probes.so (benchmark
-controls) in-tree for gfx950.
+"""Build libgq.so (HIP kernels + C ABI), libgq_probes.so (benchmark
+controls) and _calls.so (host code: the binding's short calls) in-tree for
+gfx950.
 
     python -m bit_grouped_moe_amd.build        # or __graft_entry__.build()
 
@@ -10,6 +11,7 @@ Each .hip source is compiled to an object with hipcc, then linked into
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgq.so")
 PROBE_LIB = os.path.join(HERE, "libgq_probes.so")
 PROBE_SRC = os.path.join(CSRC, "probes", "probes.hip")
+CALLS_LIB = os.path.join(HERE, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "binding", "calls.cpp")
 ARCH = "gfx950"
 
 CFLAGS = [
@@ -63,10 +67,31 @@ def build(verbose=False, jobs=8):
         return obj
 
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls = ex.submit(build_calls)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     link(hipcc, objs, LIB)
     link(hipcc, [compile_one(PROBE_SRC)], PROBE_LIB)
     return LIB
+
+
+def build_calls():
+    """The binding's short calls, against the installed torch (host code)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    tmp = CALLS_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D__HIP_PLATFORM_AMD__", f'-DGQ_TORCH_VERSION="{torch.__version__}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
+           "-isystem", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {CALLS_SRC}:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, CALLS_LIB)
 
 
 def link(hipcc, objs, lib):

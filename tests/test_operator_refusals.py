@@ -174,3 +174,27 @@ def test_row_layouts():
     for bad in (x[:, :2], x[..., ::2], x.transpose(0, 2)):
         with pytest.raises(ValueError):
             gq._rows(bad, "x")
+
+
+def test_short_calls_leave_what_is_not_ordinary(lib):
+    """The short calls return None, and touch nothing, for what is not a plain
+    device tensor; the Python code then refuses it."""
+    calls = gq._calls
+    assert calls is not None and calls.torch_version == torch.__version__
+    x = torch.zeros(4, 64)
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    assert calls.quantize(x, False) is None
+    assert calls.quantize(None, True) is None
+    assert calls.moe_topk(x, 2, True) is None
+    assert calls.moe_topk("x", 2, True) is None
+    assert calls.moe_topk_backward(torch.zeros(4, 2), x, i, True) is None
+    assert calls.route_sort(i, 4, 256) is None
+    assert calls.fp4_gemv(x, x, x, x, i, None, False, 0.0, 0.0) is None
+    assert calls.fp4_gemm(x, x, x, x, (), None, True, 1.0, 1.0) is None
+    assert calls.moe_decode(0, 0, 16, x) is None
+    for f in (calls.quantize, calls.moe_topk, calls.route_sort, calls.fp4_gemm, calls.bind):
+        with pytest.raises(TypeError):
+            f()
+    with pytest.raises(KeyError):
+        calls.bind({}, None, None)
+    gq._load_calls(lib)                                   # bound again as it was
