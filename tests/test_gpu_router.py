@@ -237,3 +237,78 @@ def test_routing_feeds_the_sort():
     assert live == 42 * 3 + 14
     assert int(route.expert_offsets[-1]) == live
     assert not w.cpu()[::5].any() and (w.cpu()[1::5, 0] == 1).all()
+
+
+def _forward_by_hand(z, topk):
+    """Ids and float64 weights, one row at a time in plain Python."""
+    ids, ws = [], []
+    for row in z.double().tolist():
+        order = sorted((e for e in range(len(row)) if row[e] > -np.inf), key=lambda e: (-row[e], e))
+        mine = order[:topk] + [-1] * (topk - len(order[:topk]))
+        top = max((row[e] for e in mine if e >= 0), default=0.0)
+        ex = [np.exp(row[e] - top) if e >= 0 else 0.0 for e in mine]
+        ids.append(mine)
+        ws.append([v / (sum(ex) or 1.0) for v in ex])
+    return np.array(ids), np.array(ws)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E", [1, 3, 4, 63, 64, 65, 67, 72, 128, 130, 144, 255, 256, 257, 272])
+@pytest.mark.parametrize("topk", [1, 15, 16, 17])
+def test_sizes_where_the_variants_meet(dtype, E, topk):
+    """Row counts that end inside a workgroup, rows at every alignment, few
+    distinct logits, and the gradient of ids with repeats and holes; with many
+    rows a few, the last among them, are compared."""
+    if topk > E:
+        pytest.skip("fewer experts than slots")
+    dev = device()
+    g = torch.Generator().manual_seed(E * 100 + topk)
+    for rows, pad, at in ((1, 0, 0), (17, 5, 2), (4095, 0, 0), (4097, 0, 0), (4101, 1, 1),
+                          (8209, 8, 8), (16421, 3, 2), (64 * E - 1, 0, 0), (64 * E + 4096, 0, 0)):
+        say("router variants", dtype, E, topk, rows, pad, at)
+        z = (torch.randn(rows, E, generator=g) * 2).round() / 2
+        z[torch.rand(rows, E, generator=g) < 0.2] = -float("inf")
+        room = torch.full((rows, E + pad), float("inf"), dtype=dtype, device=dev)
+        zd = room[:, at:at + E]
+        zd.copy_(z)
+        ids, w = gq.gq_moe_topk(zd, topk)
+        torch.cuda.synchronize()
+        at = sorted({0, rows // 2, rows - 2, rows - 1} & set(range(rows)))
+        rid, rw = _forward_by_hand(z[at], topk)
+        assert np.array_equal(ids.cpu().numpy()[at], rid)
+        assert (np.abs(w[at].double().cpu().numpy() - rw) <= 60 * U * rw + 1e-37).all()
+        order = np.argsort(-z.double().numpy(), axis=1, kind="stable")[:, :topk]
+        live = np.isfinite(np.take_along_axis(z.numpy(), order, 1))
+        assert np.array_equal(ids.cpu().numpy(), np.where(live, order, -1))
+        given = torch.randint(-2, E + 2, (rows, topk), generator=g, dtype=torch.int32)
+        dw = torch.randn(rows, topk, generator=g)
+        for renorm in (True, False):
+            dz = gq.gq_moe_topk_backward(dw.to(dev), zd, given.to(dev), renormalize=renorm)
+            torch.cuda.synchronize()
+            ref = np.zeros((len(at), E))
+            z64, d64 = z[at].double().numpy(), dw[at].double().numpy()
+            for r in range(len(at)):
+                slots = [(int(j), d64[r, s]) for s, j in enumerate(given[at][r]) if
+                         0 <= j < E and z64[r, j] > -np.inf]
+                if not slots:
+                    continue
+                over = [j for j, _ in slots] if renorm else range(E)
+                top = max(z64[r, j] for j in over)
+                total = sum(np.exp(z64[r, j] - top) for j in over)
+                p = np.exp(z64[r] - top) / total
+                dot = sum(p[j] * d for j, d in slots)
+                if renorm:
+                    for j, d in slots:
+                        ref[r, j] += p[j] * (d - dot)
+                else:
+                    G = np.zeros(E)
+                    for j, d in slots:
+                        G[j] += d
+                    ref[r] = p * (G - dot)
+            # p <= 1; a slot's gradient, the sum p g and their difference are
+            # each below 4 of the largest |dw| a slot; exp, sums of at most 17
+            # + 272 terms and the quotient; the type's own rounding
+            big = np.abs(d64).max(axis=1, keepdims=True) * topk * 4
+            tol = big * 80 * U + np.abs(ref) * torch.finfo(dtype).eps / 2 * 1.0001 + (
+                2.0 ** -25 if dtype == torch.float16 else 1e-37)
+            assert (np.abs(dz[at].double().cpu().numpy() - ref) <= tol).all()
