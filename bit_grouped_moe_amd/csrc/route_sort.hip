@@ -5,10 +5,15 @@
 // synchronisation); the grouping itself is this library's design.
 //
 // Launch: E + 1 workgroups of 1024 threads.  Workgroup b < E owns expert b,
-// workgroup E owns the dropped pairs.  The ids are taken in chunks of 32768;
-// wave w of a workgroup owns ids [chunk + 2048 w, chunk + 2048 (w + 1)) and
-// lane l holds ids chunk + 2048 w + 64 j + l, j < 32, in registers (each
-// load instruction reads 256 contiguous bytes).  Each workgroup
+// workgroup E owns the dropped pairs.  The ids are taken in chunks of 1024 L,
+// L ids a lane: wave w of a workgroup owns ids [chunk + 64 L w,
+// chunk + 64 L (w + 1)) and lane l holds ids chunk + 64 L w + 64 j + l, j < L,
+// in registers (each load instruction reads 256 contiguous bytes).  L is the
+// smallest of 1, 8 and 32 that takes all pairs in one chunk (32 beyond), so
+// that few pairs are spread over all waves and no wave counts empty places
+// (L = 32 throughout -> this rule: 666 pairs of 6 experts 7.4 -> 3.5 us, 1024
+// of 128 8.5 -> 4.4 us, 8192 of 32 7.3 -> 4.4 us, of 128 8.2 -> 5.2 us).  Each
+// workgroup
 //   1. builds the full expert histogram with integer LDS atomics into
 //      several copies of the histogram, lane l adding to copy l mod C (C = 64
 //      for E <= 128, fewer for larger E; at most 8192 counters): a skewed
@@ -19,13 +24,15 @@
 //      base and the totals itself (lane partial sums and a butterfly sum, no
 //      barrier),
 //   3. compacts its pairs in ascending pair order from the same registers:
-//      the wave's 32 match ballots are taken once to count (for the first
+//      the wave's L match ballots are taken once to count (for the first
 //      chunk during the histogram pass, so the two share a barrier) and once
 //      to place, rows without a match skipped; a pair's place is the
 //      workgroup's cursor + the earlier waves' counts + the wave's running
 //      count + its rank among the matching lanes (ballot bit count), and
 //   4. writes its offsets entry and its tiles.
 // No global atomics, no workspace; the result is the unique stable order.
+#include <type_traits>
+
 #include "gq_device.hpp"
 #include "gq_host.hpp"
 #include "../../include/gq.h"
@@ -34,17 +41,16 @@ namespace gq {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int kChunkIds = 32768;                          // ids per pass
-constexpr int kPerLane = kChunkIds / kSortThreads;        // 32
-constexpr int kWaveIds = kChunkIds / kSortWaves;          // 2048 contiguous ids per wave
 constexpr int kHistCounters = 8192;                       // LDS counters over all copies
 constexpr int kPastEnd = INT32_MIN;                       // slots beyond the last pair
 
-// The lane's 32 ids of chunk c0 (kPastEnd past P), all loads issued first:
-// unconditional where the wave's 2048 ids are all in range, clamped
+// The lane's ids of chunk c0 (kPastEnd past P), all loads issued first:
+// unconditional where the wave's 64 L ids are all in range, clamped
 // addresses then a select on the last partial range, none past P.
+template <int kPerLane>
 __device__ __forceinline__ void load_ids(const int32_t* __restrict__ ids, int32_t P, int64_t c0,
                                          int (&v)[kPerLane]) {
+  constexpr int kWaveIds = kWave * kPerLane;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int64_t wbase = c0 + (int64_t)wave * kWaveIds;
   if (wbase + kWaveIds <= P) {
@@ -79,12 +85,14 @@ __device__ __forceinline__ int wave_total(int v) {
 // One workgroup's whole share of the sort.  kDropped selects the pairs it
 // compacts at compile time (expert b's, or the dropped ones for b = E), so
 // the match test in the loops is one compare with no branch.
-template <bool kDropped>
+template <bool kDropped, int kPerLane>
 __device__ __forceinline__ void sort_workgroup(
     const int32_t* __restrict__ ids, int32_t P, int32_t E, int32_t tile_m,
     int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs,
     int32_t* __restrict__ tiles, int32_t max_tiles, int32_t* __restrict__ num_tiles,
     int* __restrict__ hist_c, int* __restrict__ hist, int* __restrict__ wcount) {
+  constexpr int kWaveIds = kWave * kPerLane;              // contiguous ids per wave
+  constexpr int kChunkIds = kSortWaves * kWaveIds;
   const int b = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const unsigned uE = (unsigned)E;
@@ -202,6 +210,7 @@ __device__ __forceinline__ void sort_workgroup(
   }
 }
 
+template <int kPerLane>
 __global__ __launch_bounds__(kSortThreads) void route_sort_kernel(
     const int32_t* __restrict__ ids, int32_t P, int32_t E, int32_t tile_m,
     int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs,
@@ -211,11 +220,11 @@ __global__ __launch_bounds__(kSortThreads) void route_sort_kernel(
   __shared__ int hist[1024];
   __shared__ int wcount[kSortWaves];
   if ((int)blockIdx.x < E)
-    sort_workgroup<false>(ids, P, E, tile_m, offsets, sorted_pairs, tiles, max_tiles, num_tiles,
-                          hist_c, hist, wcount);
+    sort_workgroup<false, kPerLane>(ids, P, E, tile_m, offsets, sorted_pairs, tiles, max_tiles,
+                                    num_tiles, hist_c, hist, wcount);
   else
-    sort_workgroup<true>(ids, P, E, tile_m, offsets, sorted_pairs, tiles, max_tiles, num_tiles,
-                         hist_c, hist, wcount);
+    sort_workgroup<true, kPerLane>(ids, P, E, tile_m, offsets, sorted_pairs, tiles, max_tiles,
+                                   num_tiles, hist_c, hist, wcount);
 }
 
 }  // namespace gq
@@ -241,8 +250,13 @@ extern "C" int gq_route_sort(const int32_t* topk_ids, int32_t rows, int32_t topk
   if (num_experts > 1024) return kNotSupported;
   int32_t need = gq_route_max_tiles(rows, topk, num_experts, tile_m);
   if (need < 0 || max_tiles < need) return kInvalid;
-  hipLaunchKernelGGL(route_sort_kernel, dim3(num_experts + 1), dim3(kSortThreads), 0, stream,
-                     topk_ids, (int32_t)P, num_experts, tile_m, expert_offsets, sorted_pairs,
-                     tiles, max_tiles, num_tiles);
+  auto go = [&](auto per_lane) {
+    hipLaunchKernelGGL((route_sort_kernel<decltype(per_lane)::value>), dim3(num_experts + 1),
+                       dim3(kSortThreads), 0, stream, topk_ids, (int32_t)P, num_experts, tile_m,
+                       expert_offsets, sorted_pairs, tiles, max_tiles, num_tiles);
+  };
+  if (P <= kSortThreads) go(std::integral_constant<int, 1>{});
+  else if (P <= 8 * kSortThreads) go(std::integral_constant<int, 8>{});
+  else go(std::integral_constant<int, 32>{});
   return launch_status();
 }

@@ -64,3 +64,10 @@ def test_degenerate():
     _check(g.integers(0, 16, (16385, 3)).astype(np.int32), 16)             # two LDS chunks
     _check(g.integers(-2, 64, (9000, 8)).astype(np.int32), 64)             # three chunks, dropped
     _check(np.full((1, 1), -1, dtype=np.int32), 4)                          # only a dropped pair
+
+
+@pytest.mark.parametrize("pairs", [1, 63, 64, 65, 1023, 1024, 1025, 8191, 8192, 8193, 32767, 32769])
+@pytest.mark.parametrize("E", [1, 6, 128, 129, 1024])
+def test_pair_counts_where_the_chunking_changes(pairs, E):
+    g = np.random.default_rng(pairs * 2000 + E)
+    _check(g.integers(-1, E + 1, (pairs, 1)).astype(np.int32), E)

@@ -253,14 +253,13 @@ def _forward_by_hand(z, topk):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("E", [1, 3, 4, 63, 64, 65, 67, 72, 128, 130, 144, 255, 256, 257, 272])
-@pytest.mark.parametrize("topk", [1, 15, 16, 17])
+@pytest.mark.parametrize("E,topk", [
+    (E, k) for k in (1, 15, 16, 17)
+    for E in (1, 3, 4, 63, 64, 65, 67, 72, 128, 130, 144, 255, 256, 257, 272) if k <= E])
 def test_sizes_where_the_variants_meet(dtype, E, topk):
     """Row counts that end inside a workgroup, rows at every alignment, few
     distinct logits, and the gradient of ids with repeats and holes; with many
     rows a few, the last among them, are compared."""
-    if topk > E:
-        pytest.skip("fewer experts than slots")
     dev = device()
     g = torch.Generator().manual_seed(E * 100 + topk)
     for rows, pad, at in ((1, 0, 0), (17, 5, 2), (4095, 0, 0), (4097, 0, 0), (4101, 1, 1),
