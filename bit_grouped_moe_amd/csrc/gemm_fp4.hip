@@ -32,6 +32,7 @@ typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 
 constexpr int kF4K = 256;                     // k per stage
 constexpr int kF4RowBytes = kF4K / 2;
+constexpr int kF4Rsrc = 0x00027000;           // flags of a raw buffer of 32-bit data
 constexpr int kF4Small = 128;                 // tiles up to here: waves side by side
 
 // 16 (gate, up) pairs of a transposed block -> 16 outputs, exchanged and
@@ -113,10 +114,15 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
   const uint8_t* as_row = g.xs + (size_t)xrow * g.xs_stride;
   const uint8_t* bs_row = static_cast<const uint8_t*>(g.scl) +
                           ((size_t)t.e * g.Nw + min(wn0 + tid, g.Nw - 1)) * (size_t)nb;
-  const char* abase = reinterpret_cast<const char*>(g.x);
-  const char* bbase = reinterpret_cast<const char*>(g.codes) +
-                      (size_t)t.e * g.Nw * (size_t)(g.Kw / 2);
-
+  // raw buffers over the activations and the expert's weights.  (Buffer loads
+  // into LDS, not global ones: after a global one the compiler waits for
+  // everything in flight where it needs one earlier load or LDS read.  8192
+  // pairs on 32 experts, gate_up 151 -> 149 us.)
+  const __amdgpu_buffer_rsrc_t arsrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(g.x), 0, g.P / g.topk * (g.Kw / 2), kF4Rsrc);
+  const __amdgpu_buffer_rsrc_t brsrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.codes) + (size_t)t.e * g.Nw * (size_t)(g.Kw / 2), 0,
+      g.Nw * (g.Kw / 2), kF4Rsrc);
   // ---- loads: 8 rows of 128 bytes per instruction, rows 8 (4 j + wave) + ..;
   // lane L fills the 16-byte slot L % 8 of row L / 8 with the chunk that the
   // swizzle puts there ((row >> 1) & 7 = 4 (wave & 1) + (L >> 4)).  Rows past
@@ -135,11 +141,11 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
   auto load_rows = [&](int v, uint32_t c, uint8_t* A, uint8_t* B) {
     const int j = v & 7, r0 = 8 * (4 * j + wave);
     if (v < 8)
-      __builtin_amdgcn_global_load_lds((glb_void_t*)(bbase + (boff[j] + c)),
-                                       (lds_void_t*)(B + r0 * kF4RowBytes), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (lds_void_t*)(B + r0 * kF4RowBytes), 16,
+                                               (int)(boff[j] + c), 0, 0, 0);
     else
-      __builtin_amdgcn_global_load_lds((glb_void_t*)(abase + (aoff[j] + c)),
-                                       (lds_void_t*)(A + r0 * kF4RowBytes), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (lds_void_t*)(A + r0 * kF4RowBytes), 16,
+                                               (int)(aoff[j] + c), 0, 0, 0);
   };
   // 8 scale bytes of a row at stage ks.  The first stage of a short row takes
   // them one by one (past its end the last again); a later stage, whose row
