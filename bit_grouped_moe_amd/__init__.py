@@ -847,12 +847,15 @@ def _fp4_gemm(what, x, blocks, scales, route, unit, pair_scale, out):
     xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit is not None)
     if route.rows != rows or route.num_experts != E:
         raise ValueError("x, blocks and route disagree")
-    for name in ("expert_offsets", "sorted_pairs", "tiles", "num_tiles"):
-        _dev(getattr(route, name), "route." + name, torch.int32)
     index = xb.get_device()
     P = rows * route.topk
+    for name, least in (("expert_offsets", E + 1), ("sorted_pairs", P),
+                        ("tiles", 2 * route.max_tiles), ("num_tiles", 1)):
+        if _dev(getattr(route, name), "route." + name, torch.int32).numel() < least:
+            raise ValueError(f"route.{name} is too short for the route's sizes")
     out = _out(out, P, N // 2 if unit else N, xb.device)
-    _beside(index, out, pair_scale, route.sorted_pairs)
+    _beside(index, out, pair_scale, route.expert_offsets, route.sorted_pairs, route.tiles,
+            route.num_tiles)
     middle = unit or (_ptr(_scale(pair_scale, P)),)
     _on(index, getattr(lib, what), what, xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(),
         scales.data_ptr(), E, N, route.topk, *middle, *_route_ptrs(route), out.data_ptr())

@@ -112,6 +112,10 @@ def test_same_refusals(monkeypatch):
               lambda: gq.gq_mxfp4_grouped_gemm_fp4(q, *o.bank, route._replace(max_tiles=1)),
               lambda: gq.gq_mxfp4_grouped_gemm_fp4(
                   q, *o.bank, route._replace(tiles=route.tiles.long())),
+              lambda: gq.gq_mxfp4_grouped_gemm_fp4(q, *o.bank, route._replace(topk=3)),
+              lambda: gq.gq_mxfp4_grouped_gemm_fp4(q, *o.bank, route._replace(max_tiles=1000)),
+              lambda: gq.gq_mxfp4_grouped_gemm_fp4(
+                  q, *o.bank, route._replace(expert_offsets=route.expert_offsets[:4])),
               lambda: gq.gq_mxfp4_grouped_gemm_fp4_swiglu(q, *o.bank, route, limit=-1.0),
               lambda: gq.gq_moe_decode(layer, cpu), lambda: gq.gq_moe_decode(layer, o.x.float()),
               lambda: gq.gq_moe_decode(layer, o.x[:, :64]), lambda: gq.gq_moe_decode(layer, [1]),

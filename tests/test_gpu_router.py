@@ -311,3 +311,33 @@ def test_sizes_where_the_variants_meet(dtype, E, topk):
             tol = big * 80 * U + np.abs(ref) * torch.finfo(dtype).eps / 2 * 1.0001 + (
                 2.0 ** -25 if dtype == torch.float16 else 1e-37)
             assert (np.abs(dz[at].double().cpu().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("rows,dtype", [(5, torch.float32), (5000, torch.bfloat16)])
+def test_replayed_graph(rows, dtype):
+    """Selection, grouping and gradient captured once and replayed on new
+    logits, with eager calls on other data between the replays."""
+    dev = device()
+    g = torch.Generator().manual_seed(rows)
+    say("router graph", rows, dtype)
+    z = torch.randn(rows, 96, generator=g).to(dtype).to(dev)
+    dw = torch.randn(rows, 6, generator=g).to(dev)
+    other = torch.randn(rows, 96, generator=g).to(dtype).to(dev)
+
+    def step(logits):
+        ids, w = gq.gq_moe_topk(logits, 6)
+        return (ids, w, gq.gq_moe_topk_backward(dw, logits, ids), *gq.gq_route_sort(ids, 96)[:4])
+
+    step(z)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(z)
+    for _ in range(4):
+        z.copy_(torch.randn(rows, 96, generator=g).to(dtype))
+        ref = [t.clone() for t in step(z)]
+        graph.replay()
+        step(other)
+        torch.cuda.synchronize()
+        for a, b in zip(held, ref):
+            assert torch.equal(a, b)
