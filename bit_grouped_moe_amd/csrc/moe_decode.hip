@@ -3,7 +3,7 @@
 // the weighted combine, without a host round trip.
 //
 //   z = x Wr^T + br                                          moe_logits_kernel
-//   e_s, w_s = the topk largest logits of a token, softmax   moe_select_kernel
+//   e_s, w_s = the topk largest logits of a token, softmax   moe_gate_up_kernel
 //   a_s = unit(Wgu[e_s] x + bgu[e_s])                        moe_gate_up_kernel
 //   y = sum_s w_s (Wd[e_s] a_s + bd[e_s])                    moe_down_kernel
 //
@@ -16,9 +16,10 @@
 // every hidden element and are spread over the chip (one workgroup per
 // expert); the gate_up product needs the selection, the down product whole
 // activation rows.  The selection is one wave's work on a token's logits:
-// for one token each gate_up workgroup makes it for itself (three launches),
-// for several a launch of its own is faster than every workgroup's making
-// all of them (8 tokens, E = 128: gate_up 39.5 us with the selections inside).
+// every gate_up workgroup makes it for its own token, as far as its own slot.
+// A launch of its own between the two, which wrote all selections, cost more
+// than that for any number of tokens (8 NF4 tokens, E = 128: 46.2 us a layer,
+// so 44.5; 2 tokens 22.0 and 20.6; 8 MXFP4 tokens of 2880 82.1 and 81.0).
 #include <algorithm>
 #include <type_traits>
 
@@ -41,8 +42,8 @@ constexpr int kDownLanes = 8;                // of a row at least: bounds the ro
 // Place of a pair's activation n in the workspace: the 4-value piece v of
 // segment s is piece v S + s, so that the down product's lanes, a segment
 // each, read 16 consecutive bytes per lane.  (In the order of n a lane's
-// pieces lie 128 bytes apart, 64 lines an instruction: one-token MXFP4 layer 21.1 us, so
-// 18.7; eight NF4 tokens 46.2, so 45.3.)
+// pieces lie 128 bytes apart, 64 lines an instruction: one-token MXFP4 layer
+// 21.1 us, so 18.7; eight NF4 tokens 46.2, so 45.3.)
 __device__ __forceinline__ int act_place(int n, int S) {
   return ((((n >> 2) & 7) * S + (n >> 5)) << 2) + (n & 3);
 }
@@ -129,16 +130,6 @@ __device__ __forceinline__ int moe_select(const float* __restrict__ logits, int 
   return id;
 }
 
-// A wave per token.
-template <int C>
-__global__ __launch_bounds__(kWave* kMoeMaxRows) void moe_select_kernel(
-    const float* __restrict__ logits, int E, int topk, int renorm, int32_t* __restrict__ ids,
-    float* __restrict__ w) {
-  const int t = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  moe_select<C>(logits + (int64_t)t * E, E, topk, topk, threadIdx.x & (kWave - 1), true, renorm,
-                ids + t * topk, w + t * topk);
-}
-
 // ---- gate_up product and gated unit ----------------------------------------------
 // Grid (column chunks, pairs), the row layout of the decode GEMV: workgroup
 // (x, p) computes the output column chunks x, x + gridDim.x, ... of pair p.
@@ -148,11 +139,12 @@ __global__ __launch_bounds__(kWave* kMoeMaxRows) void moe_select_kernel(
 // 54.4 us a layer, 8 equal tokens 55.4; one pair a workgroup 50.6 and 45.0,
 // the repeated rows coming from the caches).
 // NF4: gate row j, up row I + j, SwiGLU; MXFP4: gate row 2j, up row 2j + 1,
-// the clamped unit.  C > 0 (one token, C logits a lane): the workgroup
-// selects for itself, as far as its own slot (a token's experts are
-// distinct), and the last slot's first workgroup writes the selection for
-// the down product; C == 0: ids come from moe_select_kernel.
-template <bool kMx, int kIter, bool kWaveRows, int C>
+// the clamped unit.  The workgroup selects for itself (C logits a lane), as
+// far as its own slot (a token's experts are distinct), and the last slot's
+// first workgroup writes the token's selection for the down product.  kLoop:
+// several chunks a workgroup, the next one's rows loading while this one's
+// are decoded.
+template <bool kMx, int kIter, bool kWaveRows, int C, bool kLoop>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
     const float* __restrict__ logits, const uint16_t* __restrict__ x,
     const uint8_t* __restrict__ codes, const void* __restrict__ scl, int H, int I, int E,
@@ -193,19 +185,15 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
   }
   if constexpr (!kMx) lut_init(lut, tid, NT);
 
-  int e;
-  if constexpr (C > 0) {
-    if (wave == 0) {
-      const bool write = blockIdx.x == 0 && p0 == topk - 1;
-      const int id = moe_select<C>(logits, E, topk, p0 + 1, lane, write, renorm, ids, w);
-      if (lane == p0) mine_s = id;
-    }
-    lds_barrier();
-    e = __builtin_amdgcn_readfirstlane(mine_s);
-  } else {
-    e = ids[p0];
-    if constexpr (!kMx) lds_barrier();                     // the table
+  if (wave == 0) {
+    const int t = p0 / topk, slot = p0 - t * topk;
+    const bool write = blockIdx.x == 0 && slot == topk - 1;
+    const int id = moe_select<C>(logits + (int64_t)t * E, E, topk, slot + 1, lane, write, renorm,
+                                 ids + t * topk, w + t * topk);
+    if (lane == slot) mine_s = id;
   }
+  lds_barrier();
+  const int e = __builtin_amdgcn_readfirstlane(mine_s);
   if (e < 0) return;                                       // no expert (uniform)
 
   // ---- weight rows: the kIter rows of a thread in the chunk that starts at
@@ -318,14 +306,14 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
                 : unit(red[tid] + bias_of(w.braw[0]), red[tid + Rout] + bias_of(w.braw[1]));
     }
   };
-  // the next chunk's rows load while this one's are decoded (a single token
-  // has one chunk a workgroup, and so have rows that meet in LDS: their
-  // barriers keep the waves in step, and more workgroups hide them better)
+  // (a single token has one chunk a workgroup, and so have rows that meet in
+  // LDS: their barriers keep the waves in step, and more workgroups hide them
+  // better)
   const int step = gridDim.x * Rout;
   int n0 = blockIdx.x * Rout;
   Rows cur;
   load_rows(n0, cur);
-  if constexpr (C == 0 && kWaveRows) {
+  if constexpr (kLoop) {
     for (; n0 + step < I; n0 += step) {
       Rows next;
       load_rows(n0 + step, next);
@@ -520,11 +508,11 @@ static int layer_checks(const gq_moe_layer* l) {
   return kOk;
 }
 
-template <bool kMx, int kIter, bool kWaveRows, int C>
+template <bool kMx, int kIter, bool kWaveRows, int C, bool kLoop>
 static void launch_gate_up(int chunks, int NT, hipStream_t stream, const gq_moe_layer& l,
                            const float* logits, const uint16_t* x, int x_stride, int rows,
                            int32_t* ids, float* w, float* act) {
-  hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, kWaveRows, C>), dim3(chunks, rows * l.topk),
+  hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, kWaveRows, C, kLoop>), dim3(chunks, rows * l.topk),
                      dim3(NT), 0, stream, logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden,
                      l.inner, l.num_experts, x_stride, l.topk, l.gate_up_bias, l.alpha,
                      l.limit, l.renormalize, ids, w, act);
@@ -538,17 +526,18 @@ static void gate_up(hipStream_t stream, const gq_moe_layer& l, const float* logi
   int S, W, G, NT;
   segment_layout(l.hidden, S, W, G, NT);
   auto chunks = [&](int iter) { return (N + G * iter - 1) / (G * iter); };
-  auto go = [&](auto iter, auto wave_rows, int n) {
-    launch_gate_up<kMx, decltype(iter)::value, decltype(wave_rows)::value, C>(
-        n, NT, stream, l, logits, x, x_stride, rows, ids, w, act);
+  auto go = [&](auto iter, auto wave_rows, int n, auto loop) {
+    launch_gate_up<kMx, decltype(iter)::value, decltype(wave_rows)::value, C,
+                   decltype(loop)::value>(n, NT, stream, l, logits, x, x_stride, rows, ids, w,
+                                          act);
   };
   using I2 = std::integral_constant<int, 2>;
   using I4 = std::integral_constant<int, 4>;
   using I8 = std::integral_constant<int, 8>;
-  if (C == 0 && S <= kWave) {
+  if (rows > 1 && S <= kWave) {
     // several tokens: four rows a thread, as many workgroups as the chip
     // holds at once (four a CU), each running on over its chunks
-    go(I4{}, std::true_type{}, std::min(chunks(4), std::max(1, 1024 / P)));
+    go(I4{}, std::true_type{}, std::min(chunks(4), std::max(1, 1024 / P)), std::true_type{});
     return;
   }
   // one chunk a workgroup; rows a thread as in the decode GEMV: the largest
@@ -557,12 +546,12 @@ static void gate_up(hipStream_t stream, const gq_moe_layer& l, const float* logi
   const int64_t want = S <= kWave ? 2048 : 512;
   const int iter = chunks(8) * (int64_t)P >= want ? 8 : chunks(4) * (int64_t)P >= want ? 4 : 2;
   auto by_rows = [&](auto wave_rows) {
-    if (iter == 8) go(I8{}, wave_rows, chunks(8));
-    else if (iter == 4) go(I4{}, wave_rows, chunks(4));
-    else go(I2{}, wave_rows, chunks(2));
+    if (iter == 8) go(I8{}, wave_rows, chunks(8), std::false_type{});
+    else if (iter == 4) go(I4{}, wave_rows, chunks(4), std::false_type{});
+    else go(I2{}, wave_rows, chunks(2), std::false_type{});
   };
   if (S > kWave) by_rows(std::false_type{});
-  else if constexpr (C > 0) by_rows(std::true_type{});
+  else by_rows(std::true_type{});
 }
 
 template <bool kMx, int kSeg>
@@ -607,13 +596,8 @@ static void moe_decode(hipStream_t stream, const gq_moe_layer& l, const uint16_t
     hipLaunchKernelGGL(moe_logits_kernel<kMoeMaxRows>, dim3(l.num_experts), dim3(kMoeThreads), 0,
                        stream, x, l.router_weight, l.hidden, x_stride, rows, l.num_experts,
                        l.router_bias, logits);
-    if (narrow)
-      hipLaunchKernelGGL(moe_select_kernel<2>, dim3(1), dim3(kWave * rows), 0, stream, logits,
-                         l.num_experts, l.topk, l.renormalize, ids, w);
-    else
-      hipLaunchKernelGGL(moe_select_kernel<8>, dim3(1), dim3(kWave * rows), 0, stream, logits,
-                         l.num_experts, l.topk, l.renormalize, ids, w);
-    gate_up<kMx, 0>(stream, l, logits, x, x_stride, rows, ids, w, act);
+    if (narrow) gate_up<kMx, 2>(stream, l, logits, x, x_stride, rows, ids, w, act);
+    else gate_up<kMx, 8>(stream, l, logits, x, x_stride, rows, ids, w, act);
   }
   int S, W, G, NT;
   segment_layout(l.inner, S, W, G, NT);
