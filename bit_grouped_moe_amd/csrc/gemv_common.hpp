@@ -32,7 +32,16 @@ constexpr int kLutN = 256;
 __device__ __forceinline__ void lut_init(LutT* lut, int tid, int nt) {
   for (int t = tid; t < kLutN; t += nt) nf4_pairs_init(lut, t);
 }
-template <bool kMx>
+// The table in 2^kLog copies side by side, lane l reading copy l mod 2^kLog.
+template <int kLog>
+__device__ __forceinline__ void lut_init_copies(LutT* lut, int tid, int nt) {
+  for (int t = tid; t < kLutN; t += nt) {
+    const LutT v = nf4_pair(t);
+#pragma unroll
+    for (int c = 0; c < 1 << kLog; ++c) lut[(t << kLog) + ((c + t) & ((1 << kLog) - 1))] = v;
+  }
+}
+template <bool kMx, int kLog = 0>
 __device__ __forceinline__ float segment_dot(const LutT* lut, u32x4 c, float am, uint32_t sb,
                                              const float (&xf)[32], const u32x4 (&xr)[4]) {
   float acc = 0.f;
@@ -54,7 +63,7 @@ __device__ __forceinline__ float segment_dot(const LutT* lut, u32x4 c, float am,
       }
     } else {
       float q[8];
-      nf4_pairs8(lut, d, q);                        // element 2j: high nibble
+      nf4_pairs8<kLog>(lut, d, q);                        // element 2j: high nibble
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc = __builtin_fmaf(q[j], xf[8 * w + j], acc);
     }

@@ -121,24 +121,30 @@ __device__ __forceinline__ void nf4_decode8_bf16(const float* lut, uint32_t d, f
 // holds {value of the high nibble (element 2j), value of the low nibble
 // (element 2j+1)}.  One 8-byte LDS read yields both weights of a byte; with
 // the table at LDS address 0 its byte offset (b << 3) is a single shift.
-__device__ __forceinline__ void nf4_pairs_init(f32x2* tab, int t) {
+__device__ __forceinline__ f32x2 nf4_pair(int t) {
   uint32_t hi = 0u, lo = 0u;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     hi = ((t >> 4) == i) ? kNF4Bits[i] : hi;
     lo = ((t & 15) == i) ? kNF4Bits[i] : lo;
   }
-  if (t < 256) tab[t] = f32x2{__uint_as_float(hi), __uint_as_float(lo)};
+  return f32x2{__uint_as_float(hi), __uint_as_float(lo)};
+}
+__device__ __forceinline__ void nf4_pairs_init(f32x2* tab, int t) {
+  const f32x2 v = nf4_pair(t);
+  if (t < 256) tab[t] = v;
 }
 
 // NF4 codebook values of the 8 weights of one code dword, in element order,
-// from the pair table.
+// from the pair table, or from a table of 2^kLog copies side by side (entry b
+// of copy c at b 2^kLog + c; `tab` then points to the lane's copy).
+template <int kLog = 0>
 __device__ __forceinline__ void nf4_pairs8(const f32x2* tab, uint32_t d, float q[8]) {
   const char* base = reinterpret_cast<const char*>(tab);
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    const f32x2 v =
-        *reinterpret_cast<const f32x2*>(base + (__builtin_amdgcn_ubfe(d, 8 * b, 8) << 3));
+    const f32x2 v = *reinterpret_cast<const f32x2*>(
+        base + (__builtin_amdgcn_ubfe(d, 8 * b, 8) << (3 + kLog)));
     q[2 * b] = v.x;
     q[2 * b + 1] = v.y;
   }

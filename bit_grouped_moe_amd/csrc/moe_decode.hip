@@ -143,7 +143,11 @@ __device__ __forceinline__ int moe_select(const float* __restrict__ logits, int 
 // far as its own slot (a token's experts are distinct), and the last slot's
 // first workgroup writes the token's selection for the down product.  kLoop:
 // several chunks a workgroup, the next one's rows loading while this one's
-// are decoded.
+// are decoded, and the NF4 table in 16 copies, so that 16 lanes never meet in
+// a bank (8 tokens, E = 128: 44.4 us a layer, so 42.9; where a workgroup has
+// one chunk, filling 32 KB costs more than that: one token 14.0, so 16.2; in
+// the down product, of a third of the weights, it gains nothing).
+constexpr int kCopiesLog = 4;
 template <bool kMx, int kIter, bool kWaveRows, int C, bool kLoop>
 __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
     const float* __restrict__ logits, const uint16_t* __restrict__ x,
@@ -151,7 +155,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
     int x_stride, int topk, const uint16_t* __restrict__ bias, float alpha, float limit,
     int renorm, int32_t* __restrict__ ids, float* __restrict__ w, float* __restrict__ act) {
   constexpr int kHalf = kIter / 2;
-  __shared__ __attribute__((aligned(4096))) LutT lut[kLutN];
+  constexpr int kLog = !kMx && kLoop ? kCopiesLog : 0;
+  __shared__ __attribute__((aligned(4096))) LutT lut_s[kMx ? 1 : kLutN << kLog];
   __shared__ float red[kWaveRows ? 1 : kIter * (kMoeThreads + 32)];
   __shared__ int mine_s;
 
@@ -183,7 +188,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
 #pragma unroll
     for (int v = 0; v < 4; ++v) xr[v] = xp[v];
   }
-  if constexpr (!kMx) lut_init(lut, tid, NT);
+  if constexpr (!kMx) lut_init_copies<kLog>(lut_s, tid, NT);
+  const LutT* lut = lut_s + (lane & ((1 << kLog) - 1));
 
   if (wave == 0) {
     const int t = p0 / topk, slot = p0 - t * topk;
@@ -271,7 +277,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
       float vals[kIter];
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
-        const float part = active ? segment_dot<kMx>(lut, w.c[i], w.am[i], w.sb[i], xf, xr) : 0.f;
+        const float part =
+            active ? segment_dot<kMx, kLog>(lut, w.c[i], w.am[i], w.sb[i], xf, xr) : 0.f;
         vals[i] = group_sum_last(part, W) + bias_of(w.braw[i]);     // total on lane s == W - 1
       }
 #pragma unroll
@@ -284,7 +291,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_gate_up_kernel(
 #pragma unroll
       for (int i = 0; i < kIter; ++i)
         red[i * kStride + tid] =
-            active ? segment_dot<kMx>(lut, w.c[i], w.am[i], w.sb[i], xf, xr) : 0.f;
+            active ? segment_dot<kMx, kLog>(lut, w.c[i], w.am[i], w.sb[i], xf, xr) : 0.f;
       lds_barrier();
       // each row's segments by L threads (8 where the workgroup has them),
       // then an L-lane sum; the totals go through LDS to the output columns
@@ -512,8 +519,8 @@ template <bool kMx, int kIter, bool kWaveRows, int C, bool kLoop>
 static void launch_gate_up(int chunks, int NT, hipStream_t stream, const gq_moe_layer& l,
                            const float* logits, const uint16_t* x, int x_stride, int rows,
                            int32_t* ids, float* w, float* act) {
-  hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, kWaveRows, C, kLoop>), dim3(chunks, rows * l.topk),
-                     dim3(NT), 0, stream, logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden,
+  hipLaunchKernelGGL((moe_gate_up_kernel<kMx, kIter, kWaveRows, C, kLoop>),
+                     dim3(chunks, rows * l.topk), dim3(NT), 0, stream, logits, x, l.gate_up_codes, l.gate_up_scales, l.hidden,
                      l.inner, l.num_experts, x_stride, l.topk, l.gate_up_bias, l.alpha,
                      l.limit, l.renormalize, ids, w, act);
 }
