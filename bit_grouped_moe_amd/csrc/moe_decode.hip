@@ -58,20 +58,26 @@ __global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
   __shared__ float part[kMoeThreads / kWave][kRows];
   const int e = blockIdx.x, tid = threadIdx.x;
   const int wave = tid / kWave, lane = tid & (kWave - 1);
-  // biases stay raw until they are added: converted at once, the load would be
-  // waited for here
-  uint32_t braw = 0u;
-  if (bias) braw = bias[e];
+  // raw until it is added, and loaded without a branch (no bias: some weight's
+  // bits, not used): converted at once, the load would be waited for here
+  const uint32_t braw = (bias ? bias : w)[e];
   float acc[kRows];
 #pragma unroll
   for (int t = 0; t < kRows; ++t) acc[t] = 0.f;
   const u32x4* wr = reinterpret_cast<const u32x4*>(w + (int64_t)e * H);
-  for (int c = tid; c < H / 8; c += kMoeThreads) {
+  // (unrolled: ahead of a loop the compiler waits for what is in flight)
+#pragma unroll
+  for (int it = 0; it < kMoeMaxHidden / 8 / kMoeThreads; ++it) {
+    const int c = tid + it * kMoeThreads;
+    if (c >= H / 8) break;
     const u32x4 wv = wr[c];
     u32x4 xv[kRows];
 #pragma unroll
     for (int t = 0; t < kRows; ++t)
       xv[t] = *reinterpret_cast<const u32x4*>(x + (int64_t)min(t, rows - 1) * x_stride + c * 8);
+    // (all loads before the first use: left to itself, the compiler waits for
+    // each token's piece before it asks for the next)
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < kRows; ++t)
 #pragma unroll
@@ -90,7 +96,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
     float s = part[0][tid];
 #pragma unroll
     for (int i = 1; i < kMoeThreads / kWave; ++i) s += part[i][tid];
-    logits[(int64_t)tid * E + e] = s + __uint_as_float(braw << 16);
+    logits[(int64_t)tid * E + e] = s + (bias ? __uint_as_float(braw << 16) : 0.f);
   }
 }
 
@@ -102,12 +108,9 @@ __device__ __forceinline__ int moe_select(const float* __restrict__ logits, int 
                                           int slots, int lane, bool write, int renorm,
                                           int32_t* __restrict__ ids, float* __restrict__ w) {
   uint32_t key[C], all[C];
+  wave_keys<C>(E, lane, [&](int e) { return logits[e]; }, key);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = 64 * c + lane;
-    const float z = logits[min(e, E - 1)];
-    key[c] = all[c] = e < E ? logit_key(z) : 0u;
-  }
+  for (int c = 0; c < C; ++c) all[c] = key[c];
   int id;
   float z;
   wave_topk<C>(key, slots, id, z);

@@ -48,12 +48,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_kernel(
       __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (row >= rows) return;
   uint32_t key[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = 64 * c + lane;
-    const float z = load1<kType>(logits, row * stride + min(e, E - 1));
-    key[c] = e < E ? logit_key(z) : 0u;
-  }
+  wave_keys<C>(E, lane, [&](int e) { return load1<kType>(logits, row * stride + e); }, key);
   uint32_t all[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) all[c] = key[c];
@@ -101,13 +96,9 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
   for (int c = 0; c < C; ++c) key[c] = 0u;
   uint32_t best = id >= 0 ? logit_key(zs) : 0u;
   if (!renorm) {
+    wave_keys<C>(E, lane, [&](int e) { return load1<kType>(logits, row * stride + e); }, key);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = 64 * c + lane;
-      const float z = load1<kType>(logits, row * stride + min(e, E - 1));
-      key[c] = e < E ? logit_key(z) : 0u;
-      best = max(best, key[c]);
-    }
+    for (int c = 0; c < C; ++c) best = max(best, key[c]);
   }
   const uint32_t m = wave_umax(best);
   const float peak = m > kDeadKey ? key_logit(m) : 0.f;

@@ -31,6 +31,21 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
 }
 
+// Keys of a row: lane l takes experts 64 c + l, load(e) a logit.  All loads are
+// in flight before the first is used: left to itself, the compiler puts each
+// behind the test of its expert and waits for one before it asks for the next
+// (one-token NF4 layer 14.1 -> 13.8 us).
+template <int C, typename F>
+__device__ __forceinline__ void wave_keys(int E, int lane, F&& load, uint32_t (&key)[C]) {
+  float z[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) z[c] = load(min(64 * c + lane, E - 1));
+#pragma unroll
+  for (int c = 0; c < C; ++c) asm volatile("" : "+v"(z[c]));
+#pragma unroll
+  for (int c = 0; c < C; ++c) key[c] = 64 * c + lane < E ? logit_key(z[c]) : 0u;
+}
+
 // Maximum over the wave, in every lane's scalar (uniform) result.
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
   auto step = [&](auto ctrl, auto mask) {
