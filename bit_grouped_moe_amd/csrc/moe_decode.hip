@@ -393,7 +393,7 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
     s_cl[j] = active[j] ? s + kWave * j : 0;
   }
   const float w_own = tid < topk ? weights[p0 + tid] : 0.f;    // used by the combine
-  if constexpr (!kMx) {
+  if constexpr (!kMx && kLoop) {
     lut_init(lut, tid, kWave * waves);
     lds_barrier();
   }
@@ -413,6 +413,12 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
 #pragma unroll
       for (int v = 0; v < 8; ++v) xv[j][v] = ap[v * S];
     }
+    // one step: the table while the expert and the activations are on their way
+    if constexpr (!kMx && !kLoop)
+      if (sl == wave) {                                    // (every wave's first slot)
+        lut_init(lut, tid, kWave * waves);
+        lds_barrier();
+      }
     if (e < 0) {                                           // no expert: adds nothing
       for (int r = lane; r < Rw; r += kWave) ys[sl * Rw + r] = 0.f;
       continue;
@@ -443,14 +449,28 @@ __global__ __launch_bounds__(kWave* kDownWaves) void moe_down_kernel(
       }
     };
     auto compute = [&](int step, const Rows& w) {
+      // MXFP4: idle lanes compute too (the row's first segment) and their sum
+      // is dropped: without branches the rows' decodes overlap (8 tokens of
+      // 2880 81.0 us a layer, so 79.4).  NF4: idle lanes stay out of the LDS
+      // reads, which bound it (8 tokens, E = 128: 44.2 us, with them 44.9).
+      float part[kR];
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
-        float part = 0.f;
+        part[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kSeg; ++j)
-          if (active[j])
-            part += segment_dot_f32<kMx>(lut, w.c[i][j], w.am[i][j], w.sb[i][j], xv[j]);
-        const float tot = group_sum_last(part, W) + __uint_as_float(w.braw[i] << 16);
+        for (int j = 0; j < kSeg; ++j) {
+          if constexpr (kMx) {
+            float d = segment_dot_f32<kMx>(lut, w.c[i][j], w.am[i][j], w.sb[i][j], xv[j]);
+            asm volatile("" : "+v"(d));
+            part[i] += active[j] ? d : 0.f;
+          } else if (active[j]) {
+            part[i] += segment_dot_f32<kMx>(lut, w.c[i][j], w.am[i][j], w.sb[i][j], xv[j]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        const float tot = group_sum_last(part[i], W) + __uint_as_float(w.braw[i] << 16);
         if (s == W - 1) ys[sl * Rw + step * Rb + g * kR + i] = tot;
       }
     };
