@@ -108,6 +108,27 @@ PyObject* pack(std::initializer_list<Tensor> ts) {
 template <typename T>
 T* data(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
+// The outputs of a call as parts of one allocation (an allocation takes about
+// 0.9 us of a call of 5 to 7): plain tensors that share a storage and do not
+// overlap, each part on a 256-byte boundary.
+struct Parts {
+  Tensor store;
+  int64_t used = 0;
+  static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+  Parts(const Tensor& like, int64_t bytes)
+      : store(at::empty({bytes}, like.options().requires_grad(false).dtype(at::kByte))) {}
+  Tensor take(at::ScalarType type, at::IntArrayRef sizes) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(store.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+        c10::scalarTypeToTypeMeta(type));
+    const int64_t item = (int64_t)c10::elementSize(type);
+    t.unsafeGetTensorImpl()->set_storage_offset(used / item);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    used += room(t.numel() * item);
+    return t;
+  }
+};
+
 #define GQ_ARGS(count) \
   if (n != (count)) {  \
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments"); \
@@ -139,13 +160,14 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   GQ_STREAM(*x)
   const bool want = a[1] == Py_True;
   auto shape = x->sizes().vec();
-  const auto opt = x->options().requires_grad(false);
   shape.back() = K / 32;
-  Tensor scales = at::empty(shape, opt.dtype(at::kByte));
+  const int64_t count = rows * (K / 32);
+  Parts parts(*x, Parts::room(count) + Parts::room(16 * count));
+  Tensor scales = parts.take(at::kByte, shape);
   shape.push_back(16);
-  Tensor blocks = at::empty(shape, opt.dtype(at::kByte));
+  Tensor blocks = parts.take(at::kByte, shape);
   Tensor values;
-  if (want) values = at::empty(x->sizes(), opt.dtype(at::kBFloat16));
+  if (want) values = at::empty(x->sizes(), x->options().requires_grad(false).dtype(at::kBFloat16));
   const int st = launch([&] {
     return lib.quantize(x->data_ptr(), code, rows, (int32_t)K, stride, data<uint8_t>(blocks),
                         data<uint8_t>(scales), want ? data<uint16_t>(values) : nullptr, stream);
@@ -179,9 +201,9 @@ PyObject* moe_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   GQ_STREAM(*z)
   const int renorm = PyObject_IsTrue(a[2]);
-  const auto opt = z->options().requires_grad(false);
-  Tensor ids = at::empty({rows, k}, opt.dtype(at::kInt));
-  Tensor w = at::empty({rows, k}, opt.dtype(at::kFloat));
+  Parts parts(*z, 2 * Parts::room(rows * k * 4));
+  Tensor ids = parts.take(at::kInt, {rows, k});
+  Tensor w = parts.take(at::kFloat, {rows, k});
   const int st = launch([&] {
     return lib.topk(z->data_ptr(), code, rows, (int32_t)E, stride, (int32_t)k, renorm,
                     data<int32_t>(ids), data<float>(w), stream);
@@ -373,9 +395,10 @@ PyObject* route_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t most = lib.max_tiles((int32_t)rows, (int32_t)k, (int32_t)E, (int32_t)tm);
   if (most < 0) Py_RETURN_NONE;
   GQ_STREAM(*ids)
-  const auto opt = ids->options().requires_grad(false);
-  Tensor off = at::empty({E + 1}, opt), sp = at::empty({rows * k}, opt);
-  Tensor tiles = at::empty({most, 2}, opt), nt = at::empty({1}, opt);
+  Parts parts(*ids, Parts::room(4 * (E + 1)) + Parts::room(4 * rows * k) +
+                        Parts::room(8 * (int64_t)most) + Parts::room(4));
+  Tensor off = parts.take(at::kInt, {E + 1}), sp = parts.take(at::kInt, {rows * k});
+  Tensor tiles = parts.take(at::kInt, {most, 2}), nt = parts.take(at::kInt, {1});
   const int st = launch([&] {
     return lib.route_sort(data<int32_t>(*ids), rows, k, E, tm, data<int32_t>(off),
                           data<int32_t>(sp), data<int32_t>(tiles), most, data<int32_t>(nt), stream);

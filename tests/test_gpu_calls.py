@@ -138,3 +138,38 @@ def test_a_stream_of_its_own(monkeypatch):
         got = gq.gq_mxfp4_quantize(y, values=True)
     s.synchronize()
     assert torch.equal(got[0], ref[0]) and torch.equal(got[2], ref[2] * 2)
+
+
+def test_outputs_are_ordinary_tensors(tmp_path):
+    """The outputs of a call share one allocation: they do not overlap, and
+    each can be written, differentiated, saved, copied and viewed by itself."""
+    import copy
+    o = Operands()
+    say("calls: outputs as tensors")
+    ids, w = gq.gq_moe_topk(o.z, 2)
+    blocks, scales = gq.gq_mxfp4_quantize(o.x)
+    route = gq.gq_route_sort(o.ids, 4)
+    for group in ((ids, w), (blocks, scales), route[:4]):
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in group)
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        assert all(t.is_contiguous() and t.data_ptr() % 16 == 0 for t in group)
+        assert all(not t.requires_grad and t.is_leaf for t in group)
+    keep, was = ids.clone(), w.clone()
+    w.mul_(3)
+    assert torch.equal(ids, keep) and torch.equal(w, was * 3)
+    ids.fill_(7)
+    assert torch.equal(w, was * 3)
+    w.copy_(was)
+    w.requires_grad_()
+    (w.view(-1) * torch.arange(12.0, device=w.device)).sum().backward()
+    assert torch.equal(w.grad.flatten().cpu(), torch.arange(12.0))
+    s = scales.clone()
+    torch.save(scales, tmp_path / "scales.pt")
+    assert torch.equal(torch.load(tmp_path / "scales.pt", weights_only=True), s)
+    assert torch.equal(copy.deepcopy(scales), s)
+    blocks.zero_()
+    assert torch.equal(scales, s)
+    with torch.inference_mode():
+        ids, w = gq.gq_moe_topk(o.z, 2)
+        assert w.is_inference() and torch.equal(w, was)
+    assert torch.equal(torch.stack([s, s])[1], s) and scales.untyped_storage().nbytes() > 0
