@@ -82,8 +82,10 @@ __global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
     for (int t = 0; t < kRows; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[t] = __builtin_fmaf(bf16lo_to_f32(wv[i]), bf16lo_to_f32(xv[t][i]), acc[t]);
-        acc[t] = __builtin_fmaf(bf16hi_to_f32(wv[i]), bf16hi_to_f32(xv[t][i]), acc[t]);
+        // (scalar copies: a bit_cast of a vector element reads element 0)
+        const uint32_t a = wv[i], b = xv[t][i];
+        acc[t] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
+                                                 __builtin_bit_cast(bf16x2, b), acc[t], false);
       }
   }
 #pragma unroll
