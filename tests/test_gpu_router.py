@@ -262,8 +262,8 @@ def test_sizes_where_the_variants_meet(dtype, E, topk):
     rows a few, the last among them, are compared."""
     dev = device()
     g = torch.Generator().manual_seed(E * 100 + topk)
-    for rows, pad, at in ((1, 0, 0), (17, 5, 2), (4095, 0, 0), (4097, 0, 0), (4101, 1, 1),
-                          (8209, 8, 8), (16421, 3, 2), (64 * E - 1, 0, 0), (64 * E + 4096, 0, 0)):
+    for rows, pad, at in ((1, 0, 0), (17, 5, 2), (4095, 0, 0), (4101, 1, 1), (8209, 8, 8),
+                          (64 * E + 4096, 0, 0)):
         say("router variants", dtype, E, topk, rows, pad, at)
         z = (torch.randn(rows, E, generator=g) * 2).round() / 2
         z[torch.rand(rows, E, generator=g) < 0.2] = -float("inf")
