@@ -35,11 +35,12 @@ PyObject* raw_stream = nullptr;
 
 using at::Tensor;
 
-// A plain (not subclassed) device tensor, or null.
+// A plain (not subclassed) device tensor, or null.  (A tensor inside a function
+// transform, torch.func.vmap for one, has the plain type and no storage.)
 const Tensor* device_tensor(PyObject* o) {
   if (!THPVariable_CheckExact(o)) return nullptr;
   const Tensor& t = THPVariable_Unpack(o);
-  return t.is_cuda() && t.layout() == at::kStrided ? &t : nullptr;
+  return t.is_cuda() && t.layout() == at::kStrided && t.has_storage() ? &t : nullptr;
 }
 const Tensor* contiguous(PyObject* o, at::ScalarType type, int64_t dim) {
   const Tensor* t = device_tensor(o);
@@ -79,14 +80,18 @@ bool together(const Tensor& a, const Tensor& b, const Rest&... rest) {
   return a.get_device() == b.get_device() && together(a, rest...);
 }
 
-// Launch with the interpreter free (a full queue may hold the call).
-template <typename F>
-int launch(F&& f) {
-  int st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f();
-  Py_END_ALLOW_THREADS;
-  return st;
+// Launch with the interpreter free (a full queue may hold the call).  The
+// arguments are made before, by the caller: a tensor's accessors may throw (an
+// output made inside torch.func.grad has no storage), and an error is a Python
+// error only while this thread holds the interpreter.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename Fn, typename... Args>
+int launch(Fn* fn, Args... args) {
+  Unlocked free;
+  return fn(args...);
 }
 
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
@@ -168,10 +173,9 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor blocks = parts.take(at::kByte, shape);
   Tensor values;
   if (want) values = at::empty(x->sizes(), x->options().requires_grad(false).dtype(at::kBFloat16));
-  const int st = launch([&] {
-    return lib.quantize(x->data_ptr(), code, rows, (int32_t)K, stride, data<uint8_t>(blocks),
-                        data<uint8_t>(scales), want ? data<uint16_t>(values) : nullptr, stream);
-  });
+  const int st = launch(lib.quantize, x->data_ptr(), code, rows, (int32_t)K, stride,
+                        data<uint8_t>(blocks), data<uint8_t>(scales),
+                        want ? data<uint16_t>(values) : nullptr, stream);
   if (st) return PyLong_FromLong(st);
   return want ? pack({blocks, scales, values}) : pack({blocks, scales});
   END_HANDLE_TH_ERRORS
@@ -204,10 +208,8 @@ PyObject* moe_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Parts parts(*z, 2 * Parts::room(rows * k * 4));
   Tensor ids = parts.take(at::kInt, {rows, k});
   Tensor w = parts.take(at::kFloat, {rows, k});
-  const int st = launch([&] {
-    return lib.topk(z->data_ptr(), code, rows, (int32_t)E, stride, (int32_t)k, renorm,
-                    data<int32_t>(ids), data<float>(w), stream);
-  });
+  const int st = launch(lib.topk, z->data_ptr(), code, rows, (int32_t)E, stride, (int32_t)k,
+                        renorm, data<int32_t>(ids), data<float>(w), stream);
   if (st) return PyLong_FromLong(st);
   return pack({ids, w});
   END_HANDLE_TH_ERRORS
@@ -228,11 +230,9 @@ PyObject* moe_topk_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   GQ_STREAM(*z)
   const int renorm = PyObject_IsTrue(a[3]);
   Tensor dz = at::empty({rows, E}, z->options().requires_grad(false));
-  const int st = launch([&] {
-    return lib.topk_backward(data<float>(*dw), z->data_ptr(), code, rows, (int32_t)E, stride,
-                             data<int32_t>(*ids), (int32_t)ids->size(1), renorm, dz.data_ptr(),
-                             stream);
-  });
+  const int st = launch(lib.topk_backward, data<float>(*dw), z->data_ptr(), code, rows,
+                        (int32_t)E, stride, data<int32_t>(*ids), (int32_t)ids->size(1), renorm,
+                        dz.data_ptr(), stream);
   if (st) return PyLong_FromLong(st);
   return wrap(dz);
   END_HANDLE_TH_ERRORS
@@ -255,11 +255,9 @@ PyObject* moe_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto opt = x->options().requires_grad(false);
   Tensor space = at::empty({need}, opt.dtype(at::kByte));
   Tensor y = at::empty({rows, layer->hidden}, opt);
-  const int st = launch([&] {
-    return lib.decode(layer, data<uint16_t>(*x), (int32_t)rows,
-                      rows > 1 ? x->stride(0) : layer->hidden, space.data_ptr(), need,
-                      data<uint16_t>(y), stream);
-  });
+  const int st = launch(lib.decode, layer, data<uint16_t>(*x), (int32_t)rows,
+                        rows > 1 ? x->stride(0) : layer->hidden, space.data_ptr(), need,
+                        data<uint16_t>(y), stream);
   if (st) return PyLong_FromLong(st);
   return wrap(y);
   END_HANDLE_TH_ERRORS
@@ -317,15 +315,14 @@ PyObject* fp4_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   GQ_STREAM(*p.xb)
   Tensor out = at::empty({P, unit ? p.N / 2 : p.N},
                          p.xb->options().requires_grad(false).dtype(at::kBFloat16));
-  const int st = launch([&] {
-    const auto *xb = data<uint8_t>(*p.xb), *xs = data<uint8_t>(*p.xs);
-    const auto *b = data<uint8_t>(*p.blocks), *s = data<uint8_t>(*p.scales);
-    const int32_t k = (int32_t)ids->size(1);
-    return unit ? lib.gemv_unit(xb, xs, p.rows, p.K, b, s, p.E, p.N, data<int32_t>(*ids), k,
-                                (float)alpha, (float)limit, data<uint16_t>(out), stream)
-                : lib.gemv(xb, xs, p.rows, p.K, b, s, p.E, p.N, data<int32_t>(*ids), k, ps,
-                           data<uint16_t>(out), stream);
-  });
+  const auto *xb = data<uint8_t>(*p.xb), *xs = data<uint8_t>(*p.xs);
+  const auto *b = data<uint8_t>(*p.blocks), *s = data<uint8_t>(*p.scales);
+  const auto* id = data<int32_t>(*ids);
+  const int32_t k = (int32_t)ids->size(1);
+  uint16_t* o = data<uint16_t>(out);
+  const int st = unit ? launch(lib.gemv_unit, xb, xs, p.rows, p.K, b, s, p.E, p.N, id, k,
+                               (float)alpha, (float)limit, o, stream)
+                      : launch(lib.gemv, xb, xs, p.rows, p.K, b, s, p.E, p.N, id, k, ps, o, stream);
   if (st) return PyLong_FromLong(st);
   return wrap(out);
   END_HANDLE_TH_ERRORS
@@ -361,17 +358,15 @@ PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   GQ_STREAM(*p.xb)
   Tensor out = at::empty({P, unit ? p.N / 2 : p.N},
                          p.xb->options().requires_grad(false).dtype(at::kBFloat16));
-  const int st = launch([&] {
-    const auto *xb = data<uint8_t>(*p.xb), *xs = data<uint8_t>(*p.xs);
-    const auto *b = data<uint8_t>(*p.blocks), *s = data<uint8_t>(*p.scales);
-    const auto *off = data<int32_t>(*r[0]), *sp = data<int32_t>(*r[1]), *tl = data<int32_t>(*r[2]),
-               *nt = data<int32_t>(*r[3]);
-    return unit ? lib.gemm_unit(xb, xs, p.rows, p.K, b, s, p.E, p.N, k, (float)alpha,
-                                (float)limit, off, sp, tl, nt, v[0], v[1], data<uint16_t>(out),
-                                stream)
-                : lib.gemm(xb, xs, p.rows, p.K, b, s, p.E, p.N, k, ps, off, sp, tl, nt, v[0], v[1],
-                           data<uint16_t>(out), stream);
-  });
+  const auto *xb = data<uint8_t>(*p.xb), *xs = data<uint8_t>(*p.xs);
+  const auto *b = data<uint8_t>(*p.blocks), *s = data<uint8_t>(*p.scales);
+  const auto *off = data<int32_t>(*r[0]), *sp = data<int32_t>(*r[1]), *tl = data<int32_t>(*r[2]),
+             *nt = data<int32_t>(*r[3]);
+  uint16_t* o = data<uint16_t>(out);
+  const int st = unit ? launch(lib.gemm_unit, xb, xs, p.rows, p.K, b, s, p.E, p.N, k, (float)alpha,
+                               (float)limit, off, sp, tl, nt, v[0], v[1], o, stream)
+                      : launch(lib.gemm, xb, xs, p.rows, p.K, b, s, p.E, p.N, k, ps, off, sp, tl,
+                               nt, v[0], v[1], o, stream);
   if (st) return PyLong_FromLong(st);
   return wrap(out);
   END_HANDLE_TH_ERRORS
@@ -399,10 +394,8 @@ PyObject* route_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         Parts::room(8 * (int64_t)most) + Parts::room(4));
   Tensor off = parts.take(at::kInt, {E + 1}), sp = parts.take(at::kInt, {rows * k});
   Tensor tiles = parts.take(at::kInt, {most, 2}), nt = parts.take(at::kInt, {1});
-  const int st = launch([&] {
-    return lib.route_sort(data<int32_t>(*ids), rows, k, E, tm, data<int32_t>(off),
-                          data<int32_t>(sp), data<int32_t>(tiles), most, data<int32_t>(nt), stream);
-  });
+  const int st = launch(lib.route_sort, data<int32_t>(*ids), rows, k, E, tm, data<int32_t>(off),
+                        data<int32_t>(sp), data<int32_t>(tiles), most, data<int32_t>(nt), stream);
   if (st) return PyLong_FromLong(st);
   return pack({off, sp, tiles, nt});
   END_HANDLE_TH_ERRORS

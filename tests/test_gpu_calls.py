@@ -173,3 +173,34 @@ def test_outputs_are_ordinary_tensors(tmp_path):
         ids, w = gq.gq_moe_topk(o.z, 2)
         assert w.is_inference() and torch.equal(w, was)
     assert torch.equal(torch.stack([s, s])[1], s) and scales.untyped_storage().nbytes() > 0
+
+
+def test_function_transforms_raise_alike(monkeypatch):
+    """Tensors without storage (torch.func.vmap) and outputs without storage
+    (torch.func.grad): the same error from both ways."""
+    o = Operands()
+    say("calls: function transforms")
+    layer = gq.gq_moe_layer(o.router, o.bank, o.down, 2)
+    gq.gq_moe_decode(layer, o.x)
+    xb, xs = gq.gq_mxfp4_quantize(o.x)
+    route = gq.gq_route_sort(o.ids, 4)
+    w = o.w.reshape(6, 2)
+    for f, args in ((lambda x: gq.gq_mxfp4_quantize(x, values=True), (o.x,)),
+                    (lambda z: gq.gq_moe_topk(z, 2), (o.z,)),
+                    (lambda w, z, i: gq.gq_moe_topk_backward(w, z, i), (w, o.z, o.ids)),
+                    (lambda i: gq.gq_route_sort(i, 4), (o.ids,)),
+                    (lambda x: gq.gq_moe_decode(layer, x), (o.x,)),
+                    (lambda b, s, i: gq.gq_mxfp4_grouped_gemv_fp4((b, s), *o.bank, i),
+                     (xb, xs, o.ids)),
+                    (lambda b, s: gq.gq_mxfp4_grouped_gemm_fp4((b, s), *o.bank, route), (xb, xs))):
+        batched = [torch.stack([t, t]) for t in args]
+
+        def in_grad(s):
+            f(*args)
+            return s * 2
+        fast, slow = _both(monkeypatch, lambda: torch.func.vmap(lambda *a: f(*a))(*batched))
+        assert isinstance(fast, tuple) and fast[0] is RuntimeError and fast == slow, (fast, slow)
+        one = torch.ones((), device=o.x.device)
+        for e in _both(monkeypatch, lambda: torch.func.grad(in_grad)(one)):
+            assert isinstance(e, tuple) and issubclass(e[0], RuntimeError), e
+        f(*args)                                          # and plain tensors as before
