@@ -113,26 +113,10 @@ PyObject* pack(std::initializer_list<Tensor> ts) {
 template <typename T>
 T* data(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
-// The outputs of a call as parts of one allocation (an allocation takes about
-// 0.9 us of a call of 5 to 7): plain tensors that share a storage and do not
-// overlap, each part on a 256-byte boundary.
-struct Parts {
-  Tensor store;
-  int64_t used = 0;
-  static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
-  Parts(const Tensor& like, int64_t bytes)
-      : store(at::empty({bytes}, like.options().requires_grad(false).dtype(at::kByte))) {}
-  Tensor take(at::ScalarType type, at::IntArrayRef sizes) {
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(
-        c10::Storage(store.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
-        c10::scalarTypeToTypeMeta(type));
-    const int64_t item = (int64_t)c10::elementSize(type);
-    t.unsafeGetTensorImpl()->set_storage_offset(used / item);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-    used += room(t.numel() * item);
-    return t;
-  }
-};
+// An output on the device of `like`, a tensor of its own.
+Tensor output(const Tensor& like, at::ScalarType type, at::IntArrayRef sizes) {
+  return at::empty(sizes, like.options().requires_grad(false).dtype(type));
+}
 
 #define GQ_ARGS(count) \
   if (n != (count)) {  \
@@ -166,13 +150,11 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool want = a[1] == Py_True;
   auto shape = x->sizes().vec();
   shape.back() = K / 32;
-  const int64_t count = rows * (K / 32);
-  Parts parts(*x, Parts::room(count) + Parts::room(16 * count));
-  Tensor scales = parts.take(at::kByte, shape);
+  Tensor scales = output(*x, at::kByte, shape);
   shape.push_back(16);
-  Tensor blocks = parts.take(at::kByte, shape);
+  Tensor blocks = output(*x, at::kByte, shape);
   Tensor values;
-  if (want) values = at::empty(x->sizes(), x->options().requires_grad(false).dtype(at::kBFloat16));
+  if (want) values = output(*x, at::kBFloat16, x->sizes());
   const int st = launch(lib.quantize, x->data_ptr(), code, rows, (int32_t)K, stride,
                         data<uint8_t>(blocks), data<uint8_t>(scales),
                         want ? data<uint16_t>(values) : nullptr, stream);
@@ -205,9 +187,8 @@ PyObject* moe_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   GQ_STREAM(*z)
   const int renorm = PyObject_IsTrue(a[2]);
-  Parts parts(*z, 2 * Parts::room(rows * k * 4));
-  Tensor ids = parts.take(at::kInt, {rows, k});
-  Tensor w = parts.take(at::kFloat, {rows, k});
+  Tensor ids = output(*z, at::kInt, {rows, k});
+  Tensor w = output(*z, at::kFloat, {rows, k});
   const int st = launch(lib.topk, z->data_ptr(), code, rows, (int32_t)E, stride, (int32_t)k,
                         renorm, data<int32_t>(ids), data<float>(w), stream);
   if (st) return PyLong_FromLong(st);
@@ -229,7 +210,7 @@ PyObject* moe_topk_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   GQ_STREAM(*z)
   const int renorm = PyObject_IsTrue(a[3]);
-  Tensor dz = at::empty({rows, E}, z->options().requires_grad(false));
+  Tensor dz = output(*z, z->scalar_type(), {rows, E});
   const int st = launch(lib.topk_backward, data<float>(*dw), z->data_ptr(), code, rows,
                         (int32_t)E, stride, data<int32_t>(*ids), (int32_t)ids->size(1), renorm,
                         dz.data_ptr(), stream);
@@ -252,9 +233,8 @@ PyObject* moe_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   GQ_STREAM(*x)
   const int64_t rows = x->size(0);
-  const auto opt = x->options().requires_grad(false);
-  Tensor space = at::empty({need}, opt.dtype(at::kByte));
-  Tensor y = at::empty({rows, layer->hidden}, opt);
+  Tensor space = output(*x, at::kByte, {need});
+  Tensor y = output(*x, at::kBFloat16, {rows, layer->hidden});
   const int st = launch(lib.decode, layer, data<uint16_t>(*x), (int32_t)rows,
                         rows > 1 ? x->stride(0) : layer->hidden, space.data_ptr(), need,
                         data<uint16_t>(y), stream);
@@ -313,8 +293,7 @@ PyObject* fp4_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double alpha = PyFloat_AsDouble(a[7]), limit = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred()) return nullptr;
   GQ_STREAM(*p.xb)
-  Tensor out = at::empty({P, unit ? p.N / 2 : p.N},
-                         p.xb->options().requires_grad(false).dtype(at::kBFloat16));
+  Tensor out = output(*p.xb, at::kBFloat16, {P, unit ? p.N / 2 : p.N});
   const auto *xb = data<uint8_t>(*p.xb), *xs = data<uint8_t>(*p.xs);
   const auto *b = data<uint8_t>(*p.blocks), *s = data<uint8_t>(*p.scales);
   const auto* id = data<int32_t>(*ids);
@@ -356,8 +335,7 @@ PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* ps;
   if (!pair_weights(a[5], P, *p.xb, ps)) Py_RETURN_NONE;
   GQ_STREAM(*p.xb)
-  Tensor out = at::empty({P, unit ? p.N / 2 : p.N},
-                         p.xb->options().requires_grad(false).dtype(at::kBFloat16));
+  Tensor out = output(*p.xb, at::kBFloat16, {P, unit ? p.N / 2 : p.N});
   const auto *xb = data<uint8_t>(*p.xb), *xs = data<uint8_t>(*p.xs);
   const auto *b = data<uint8_t>(*p.blocks), *s = data<uint8_t>(*p.scales);
   const auto *off = data<int32_t>(*r[0]), *sp = data<int32_t>(*r[1]), *tl = data<int32_t>(*r[2]),
@@ -390,10 +368,8 @@ PyObject* route_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t most = lib.max_tiles((int32_t)rows, (int32_t)k, (int32_t)E, (int32_t)tm);
   if (most < 0) Py_RETURN_NONE;
   GQ_STREAM(*ids)
-  Parts parts(*ids, Parts::room(4 * (E + 1)) + Parts::room(4 * rows * k) +
-                        Parts::room(8 * (int64_t)most) + Parts::room(4));
-  Tensor off = parts.take(at::kInt, {E + 1}), sp = parts.take(at::kInt, {rows * k});
-  Tensor tiles = parts.take(at::kInt, {most, 2}), nt = parts.take(at::kInt, {1});
+  Tensor off = output(*ids, at::kInt, {E + 1}), sp = output(*ids, at::kInt, {rows * k});
+  Tensor tiles = output(*ids, at::kInt, {most, 2}), nt = output(*ids, at::kInt, {1});
   const int st = launch(lib.route_sort, data<int32_t>(*ids), rows, k, E, tm, data<int32_t>(off),
                         data<int32_t>(sp), data<int32_t>(tiles), most, data<int32_t>(nt), stream);
   if (st) return PyLong_FromLong(st);

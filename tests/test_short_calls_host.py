@@ -52,7 +52,7 @@ def module(tmp_path_factory):
     with open(build.CALLS_SRC) as f:
         text = f.read()
     assert text.count("t.is_cuda()") == 1
-    text = text.replace("t.is_cuda()", "t.is_cpu()").replace("DispatchKey::CUDA", "DispatchKey::CPU")
+    text = text.replace("t.is_cuda()", "t.is_cpu()")
     text = text.replace("../../../include/gq.h", os.path.join(ROOT, "include", "gq.h"))
     src, lib = d / "calls.cpp", d / "_calls.so"
     src.write_text(text)
@@ -126,4 +126,24 @@ def test_outputs_without_storage_raise(module, name):
         torch.func.grad(inside)(torch.tensor(1.0))
         assert len(got) == 1 and got[0] is not None, got
         assert f(*plain) is not None                          # and works on after it
+    """)
+
+
+@pytest.mark.parametrize("name", ["quantize", "moe_topk", "route_sort"])
+def test_outputs_have_their_own_storage(module, name):
+    """An output may grow in place, be saved and be kept without its siblings:
+    it shares no memory with them."""
+    f, args = CALLS[name]
+    _run(module, f"""
+        outs = ({f})(*[t[0] for t in ({args},)])
+        assert len({{t.untyped_storage().data_ptr() for t in outs}}) == len(outs)
+        for t in outs:
+            assert t.untyped_storage().nbytes() == t.numel() * t.element_size()
+        for i, t in enumerate(outs):
+            rest = [o for j, o in enumerate(outs) if j != i]
+            for o in rest:
+                o.fill_(1)
+            t.resize_(4096)
+            t.zero_()
+            assert all((o == 1).all() for o in rest)
     """)
