@@ -152,9 +152,10 @@ def load_library():
 
 def _load_calls(lib):
     """Load the short calls and hand them the library's entry points.  Without
-    them (not built, or built against another torch) every call takes the
-    Python way, with the same checks, kernels and results."""
+    them (not built, or built against another torch or another include/gq.h)
+    every call takes the Python way, with the same checks, kernels and results."""
     global _calls
+    _calls = None
     path = os.path.join(_HERE, "_calls.so")
     if not os.path.exists(path):
         return
@@ -164,11 +165,20 @@ def _load_calls(lib):
         loader.exec_module(mod)
     except ImportError:
         return
-    if mod.torch_version != torch.__version__:
+    if mod.torch_version != torch.__version__ or not _same_header(mod):
         return
     mod.bind({n: ctypes.cast(getattr(lib, n), _p).value for n in EXPORTED_SYMBOLS},
              torch.cuda.current_device, _raw_stream)
     _calls = mod
+
+
+def _same_header(mod):
+    """Whether the module was built with the include/gq.h that is there now."""
+    from . import build
+    try:
+        return getattr(mod, "header_id", None) == build.header_id()
+    except OSError:
+        return False
 
 
 def _check(status, what):

@@ -8,7 +8,9 @@ Each .hip source is compiled to an object with hipcc, then linked into
 ``bit_grouped_moe_amd/libgq.so``.  Always rebuilds.
 """
 
+import hashlib
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -22,6 +24,7 @@ PROBE_LIB = os.path.join(HERE, "libgq_probes.so")
 PROBE_SRC = os.path.join(CSRC, "probes", "probes.hip")
 CALLS_LIB = os.path.join(HERE, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "binding", "calls.cpp")
+HEADER = os.path.join(os.path.dirname(HERE), "include", "gq.h")
 ARCH = "gfx950"
 
 CFLAGS = [
@@ -82,6 +85,14 @@ def build(verbose=False, jobs=8):
     return LIB
 
 
+def header_id():
+    """What include/gq.h declares, without its comments and spacing, as a
+    short text: the short calls hold it and are used with that header only."""
+    with open(HEADER) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    return hashlib.sha256(" ".join(text.split()).encode()).hexdigest()[:16]
+
+
 def build_calls():
     """The binding's short calls, against the installed torch (host code)."""
     import torch
@@ -90,6 +101,7 @@ def build_calls():
     tmp = CALLS_LIB + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D__HIP_PLATFORM_AMD__", f'-DGQ_TORCH_VERSION="{torch.__version__}"',
+           f'-DGQ_HEADER_ID="{header_id()}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),

@@ -423,7 +423,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
 PyMODINIT_FUNC PyInit__calls(void) {
   PyObject* m = PyModule_Create(&module);
   // built against this torch; another one's tensors may be laid out otherwise
-  if (m && PyModule_AddStringConstant(m, "torch_version", GQ_TORCH_VERSION) < 0) {
+  // nor does another header's library take these arguments
+  if (m && (PyModule_AddStringConstant(m, "torch_version", GQ_TORCH_VERSION) < 0 ||
+            PyModule_AddStringConstant(m, "header_id", GQ_HEADER_ID) < 0)) {
     Py_DECREF(m);
     return nullptr;
   }

@@ -7,6 +7,7 @@ import sys
 
 import pytest
 
+import bit_grouped_moe_amd as gq
 import bit_grouped_moe_amd.build as build
 
 
@@ -61,3 +62,29 @@ def test_kernels_that_do_not_compile_end_the_build(fake):
     with pytest.raises(RuntimeError, match="no such header"):
         build.build()
     assert not (d / "libgq.so").exists()
+
+
+def test_short_calls_of_another_header_are_not_used(monkeypatch, tmp_path):
+    """A module that was built with other declarations would hand the library
+    arguments that it does not take; other comments change nothing."""
+    lib = gq.load_library()
+    assert gq._calls is not None
+    with open(build.HEADER) as f:
+        text = f.read()
+    header = tmp_path / "gq.h"
+    monkeypatch.setattr(build, "HEADER", str(header))
+    try:
+        for there, used in ((text, True), ("/* more words */" + text, True), (None, False),
+                            (text.replace("int32_t topk", "int64_t topk"), False),
+                            (text.replace("int32_t renormalize; ", "int32_t renormalize, more; "),
+                             False)):
+            header.unlink(missing_ok=True)
+            if there is not None:
+                header.write_text(there)
+                assert used == (there.endswith(text))
+            gq._load_calls(lib)
+            assert (gq._calls is not None) == used
+    finally:
+        monkeypatch.undo()
+        gq._load_calls(lib)
+    assert gq._calls is not None

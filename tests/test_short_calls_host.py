@@ -60,7 +60,7 @@ def module(tmp_path_factory):
     inc = os.path.join(root, "include")
     subprocess.run(
         [os.environ.get("CXX", "g++"), "-O0", "-std=c++17", "-fPIC", "-shared", "-w",
-         "-D__HIP_PLATFORM_AMD__", '-DGQ_TORCH_VERSION="host"',
+         "-D__HIP_PLATFORM_AMD__", '-DGQ_TORCH_VERSION="host"', '-DGQ_HEADER_ID="host"',
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
          "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
