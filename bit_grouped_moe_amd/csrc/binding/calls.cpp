@@ -378,17 +378,22 @@ PyObject* route_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // bind(addresses by name, current_device, raw_stream): the library's entry
-// points and torch's two callables
+// points and torch's two callables; all of them or, with an error, none
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   GQ_ARGS(3)
+  if (!PyDict_Check(a[0])) {
+    PyErr_SetString(PyExc_TypeError, "addresses by name expected");
+    return nullptr;
+  }
   auto get = [&](const char* name) -> void* {
     PyObject* o = PyDict_GetItemString(a[0], name);        // borrowed
     void* p = o ? PyLong_AsVoidPtr(o) : nullptr;
     if (!p && !PyErr_Occurred()) PyErr_SetString(PyExc_KeyError, name);
     return p;
   };
+  Library l{};
 #define GQ_BIND(field, name)                                                    \
-  if (!(lib.field = reinterpret_cast<decltype(lib.field)>(get(#name)))) return nullptr;
+  if (!(l.field = reinterpret_cast<decltype(l.field)>(get(#name)))) return nullptr;
   GQ_BIND(quantize, gq_mxfp4_quantize)
   GQ_BIND(topk, gq_moe_topk)
   GQ_BIND(topk_backward, gq_moe_topk_backward)
@@ -399,6 +404,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   GQ_BIND(gemm_unit, gq_mxfp4_grouped_gemm_fp4_swiglu)
   GQ_BIND(route_sort, gq_route_sort)
   GQ_BIND(max_tiles, gq_route_max_tiles)
+  lib = l;
   Py_XINCREF(a[1]);
   Py_XINCREF(a[2]);
   Py_XDECREF(current_device);

@@ -147,3 +147,17 @@ def test_outputs_have_their_own_storage(module, name):
             t.zero_()
             assert all((o == 1).all() for o in rest)
     """)
+
+
+def test_bind_takes_all_or_nothing(module):
+    """A binding that lacks an entry point leaves the earlier one as it was."""
+    _run(module, """
+        for bad in ({}, {"gq_mxfp4_quantize": 16}, {"gq_mxfp4_quantize": 0}, None):
+            try:
+                calls.bind(bad, None, None)
+                raise SystemExit("bound")
+            except (KeyError, TypeError):
+                pass
+            count = len(done)
+            assert calls.quantize(x[0], False) is not None and len(done) == count + 1
+    """)
