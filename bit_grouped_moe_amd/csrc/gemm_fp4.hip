@@ -404,7 +404,7 @@ static int fp4_entry(const uint8_t* x_blocks, const uint8_t* x_scales, int32_t r
   g.n_col_tiles = (N + kXN - 1) / kXN;                     // 256 weight rows per tile
   const int64_t units = (int64_t)max_tiles * ceil_div64(g.n_col_tiles, kGroup);
   const int64_t grid = ceil_div64(units, 8) * 8 * kGroup;
-  if (grid > INT32_MAX) return kNotSupported;
+  if (grid > most_groups(kGemmThreads)) return kNotSupported;
   g.max_tiles = max_tiles;
   hipLaunchKernelGGL(grouped_gemm_fp4_kernel<kUnit>, dim3((unsigned)grid), dim3(kGemmThreads), 0,
                      stream, g);

@@ -22,6 +22,10 @@ inline int launch_status() {
   return e == hipSuccess ? kOk : (int)e;
 }
 
+// The most workgroups of `threads` threads along a grid's first dimension: HIP
+// takes launches of fewer than 2^32 threads along each.
+constexpr int64_t most_groups(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace gq

@@ -128,9 +128,9 @@ extern "C" int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, i
   if (!x || !blocks || !scales || (reinterpret_cast<uintptr_t>(x) & (size - 1))) return kInvalid;
   if (!aligned16(blocks) || (values && !aligned16(values))) return kInvalid;
   if (x_stride > INT64_MAX / 8 / rows) return kNotSupported;
-  // rows without gaps are one long row
+  // rows without gaps are one long row, up to the threads that a launch takes
   int64_t chunks = K / 8, n = rows;
-  if (x_stride == K) {
+  if (x_stride == K && chunks * rows <= most_groups(kQuantThreads) * kQuantThreads) {
     chunks *= rows;
     n = 1;
   }
@@ -138,7 +138,7 @@ extern "C" int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, i
   while (lgx < 8 && ((int64_t)1 << lgx) < chunks) ++lgx;
   const int64_t bx = ceil_div64(chunks, (int64_t)1 << lgx);
   const int64_t by = ceil_div64(n, kQuantThreads >> lgx);
-  if (bx > INT32_MAX) return kNotSupported;
+  // (a row has at most 2^28 chunks; beyond 65535 groups of rows the kernel strides)
   const dim3 grid((unsigned)bx, (unsigned)(by < 65535 ? by : 65535));
   auto* c = reinterpret_cast<uint32_t*>(blocks);
   auto* v = reinterpret_cast<u32x4*>(values);

@@ -23,6 +23,7 @@
 namespace gq {
 
 constexpr int kRouterThreads = 256;
+constexpr int kWaveRows = kRouterThreads / kWave;        // rows of a workgroup, a wave each
 
 template <int kType>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -421,17 +422,32 @@ static void by_width(int E, F&& f) {
   else f(std::integral_constant<int, 16>{});
 }
 
+// launch(first row, rows) over pieces of the rows: a launch takes 2^24 - 1
+// workgroups of `group` rows (2^26 - 4 rows a wave each, 2^28 - 16 sixteen lanes).
+template <typename F>
+static void by_rows(int64_t rows, int group, F&& launch) {
+  const int64_t most = most_groups(kRouterThreads) * group;
+  for (int64_t at = 0; at < rows; at += most) launch(at, rows - at < most ? rows - at : most);
+}
+template <int kType>
+static const void* row_at(const void* p, int64_t element) {
+  return static_cast<const char*>(p) + element * (kType == GQ_F32 ? 4 : 2);
+}
+template <int kType>
+static void* row_at(void* p, int64_t element) {
+  return static_cast<char*>(p) + element * (kType == GQ_F32 ? 4 : 2);
+}
+
 static int router_checks(const void* logits, int32_t dtype, int64_t rows, int32_t E,
                          int64_t stride, int32_t topk, const void* a, const void* b,
-                         const void* c, int64_t& blocks) {
+                         const void* c) {
   if (dtype != GQ_F32 && dtype != GQ_BF16 && dtype != GQ_F16) return kInvalid;
   if (rows < 0 || E < 1 || topk < 1 || stride < E) return kInvalid;
   if (E > kTopkMaxExperts || topk > kTopkMax) return kNotSupported;
   if (rows == 0) return kOk;
   const uintptr_t mask = dtype == GQ_F32 ? 3 : 1;
   if (!logits || !a || !b || !c || (reinterpret_cast<uintptr_t>(logits) & mask)) return kInvalid;
-  blocks = ceil_div64(rows, kRouterThreads / kWave);
-  if (blocks > INT32_MAX || stride > INT64_MAX / 4 / rows) return kNotSupported;
+  if (rows > (int64_t)1 << 33 || stride > INT64_MAX / 4 / rows) return kNotSupported;
   return kOk;
 }
 
@@ -441,10 +457,9 @@ extern "C" int gq_moe_topk(const void* logits, int32_t dtype, int64_t rows, int3
                            int64_t stride, int32_t topk, int32_t renormalize, int32_t* topk_ids,
                            float* topk_weights, hipStream_t stream) {
   using namespace gq;
-  int64_t blocks = 0;
   if (topk > num_experts) return kInvalid;
   const int st = router_checks(logits, dtype, rows, num_experts, stride, topk, topk_ids,
-                               topk_weights, logits, blocks);
+                               topk_weights, logits);
   if (st != kOk || rows == 0) return st;
   if (!aligned4(topk_ids) || !aligned4(topk_weights)) return kInvalid;
   auto go = [&](auto type) {
@@ -454,18 +469,23 @@ extern "C" int gq_moe_topk(const void* logits, int32_t dtype, int64_t rows, int3
         (T != GQ_F32 || rows >= 64 * (int64_t)num_experts)) {
       by_group<kMost>(num_experts, [&](auto c) {
         constexpr int C = decltype(c)::value;
-        hipLaunchKernelGGL((moe_topk_group_kernel<T, C>),
-                           dim3((unsigned)ceil_div64(rows, kGroupRows)), dim3(kRouterThreads), 0,
-                           stream, logits, rows, num_experts, stride, topk, renormalize,
-                           (int)group_wide<T, C>(logits, num_experts, stride), topk_ids,
-                           topk_weights);
+        by_rows(rows, kGroupRows, [&](int64_t at, int64_t n) {
+          hipLaunchKernelGGL((moe_topk_group_kernel<T, C>),
+                             dim3((unsigned)ceil_div64(n, kGroupRows)), dim3(kRouterThreads), 0,
+                             stream, row_at<T>(logits, at * stride), n, num_experts, stride, topk,
+                             renormalize, (int)group_wide<T, C>(logits, num_experts, stride),
+                             topk_ids + at * topk, topk_weights + at * topk);
+        });
       });
       return;
     }
     by_width(num_experts, [&](auto c) {
-      hipLaunchKernelGGL((moe_topk_kernel<T, decltype(c)::value>), dim3((unsigned)blocks),
-                         dim3(kRouterThreads), 0, stream, logits, rows, num_experts, stride, topk,
-                         renormalize, topk_ids, topk_weights);
+      by_rows(rows, kWaveRows, [&](int64_t at, int64_t n) {
+        hipLaunchKernelGGL((moe_topk_kernel<T, decltype(c)::value>),
+                           dim3((unsigned)ceil_div64(n, kWaveRows)), dim3(kRouterThreads), 0,
+                           stream, row_at<T>(logits, at * stride), n, num_experts, stride, topk,
+                           renormalize, topk_ids + at * topk, topk_weights + at * topk);
+      });
     });
   };
   if (dtype == GQ_F32) go(std::integral_constant<int, GQ_F32>{});
@@ -479,9 +499,8 @@ extern "C" int gq_moe_topk_backward(const float* d_weights, const void* logits, 
                                     const int32_t* topk_ids, int32_t topk, int32_t renormalize,
                                     void* d_logits, hipStream_t stream) {
   using namespace gq;
-  int64_t blocks = 0;
   const int st = router_checks(logits, dtype, rows, num_experts, stride, topk, d_weights,
-                               topk_ids, d_logits, blocks);
+                               topk_ids, d_logits);
   if (st != kOk || rows == 0) return st;
   const uintptr_t mask = dtype == GQ_F32 ? 3 : 1;
   if (!aligned4(d_weights) || !aligned4(topk_ids) ||
@@ -492,18 +511,26 @@ extern "C" int gq_moe_topk_backward(const float* d_weights, const void* logits, 
     if (num_experts <= kGroupMaxExperts && topk <= kGroup && rows >= kGroupFrom) {
       by_group<kGroupMaxExperts>(num_experts, [&](auto c) {
         constexpr int C = decltype(c)::value;
-        hipLaunchKernelGGL((moe_topk_backward_group_kernel<T, C>),
-                           dim3((unsigned)ceil_div64(rows, kGroupRows)), dim3(kRouterThreads), 0,
-                           stream, d_weights, logits, rows, num_experts, stride, topk_ids, topk,
-                           renormalize, (int)group_wide<T, C>(logits, num_experts, stride),
-                           (int)group_wide<T, C>(d_logits, num_experts, num_experts), d_logits);
+        by_rows(rows, kGroupRows, [&](int64_t at, int64_t n) {
+          hipLaunchKernelGGL((moe_topk_backward_group_kernel<T, C>),
+                             dim3((unsigned)ceil_div64(n, kGroupRows)), dim3(kRouterThreads), 0,
+                             stream, d_weights + at * topk, row_at<T>(logits, at * stride), n,
+                             num_experts, stride, topk_ids + at * topk, topk, renormalize,
+                             (int)group_wide<T, C>(logits, num_experts, stride),
+                             (int)group_wide<T, C>(d_logits, num_experts, num_experts),
+                             row_at<T>(d_logits, at * num_experts));
+        });
       });
       return;
     }
     by_width(num_experts, [&](auto c) {
-      hipLaunchKernelGGL((moe_topk_backward_kernel<T, decltype(c)::value>),
-                         dim3((unsigned)blocks), dim3(kRouterThreads), 0, stream, d_weights,
-                         logits, rows, num_experts, stride, topk_ids, topk, renormalize, d_logits);
+      by_rows(rows, kWaveRows, [&](int64_t at, int64_t n) {
+        hipLaunchKernelGGL((moe_topk_backward_kernel<T, decltype(c)::value>),
+                           dim3((unsigned)ceil_div64(n, kWaveRows)), dim3(kRouterThreads), 0,
+                           stream, d_weights + at * topk, row_at<T>(logits, at * stride), n,
+                           num_experts, stride, topk_ids + at * topk, topk, renormalize,
+                           row_at<T>(d_logits, at * num_experts));
+      });
     });
   };
   if (dtype == GQ_F32) go(std::integral_constant<int, GQ_F32>{});

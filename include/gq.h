@@ -467,7 +467,7 @@ enum { GQ_F32 = 0, GQ_BF16 = 1, GQ_F16 = 2 };
  * InvalidValue: null pointer (values may be NULL), unknown x_dtype, rows < 0,
  *   K not a positive multiple of 32, x_stride < K, x not aligned to its
  *   element, blocks or values not 16-byte aligned.
- * NotSupported: more than 2^31 workgroups.  rows == 0 enqueues nothing.
+ * NotSupported: rows*x_stride >= 2^60.  rows == 0 enqueues nothing.
  */
 int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int64_t x_stride,
                       uint8_t* blocks, uint8_t* scales, uint16_t* values, hipStream_t stream);
@@ -488,8 +488,9 @@ int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, i
  * gq_mxfp4_grouped_gemv_swiglu (weight rows 2j gate, 2j + 1 up) and write
  * [rows*topk, N/2]; a NaN passes through the unit.
  * InvalidValue / NotSupported: as for the named entry points; K % 32, and
- *   NotSupported: rows*K/2 or N*K/2 >= 2^31 (GEMM), rows*topk > 256 or
- *   K > 8192 (GEMV).
+ *   NotSupported: rows*K/2 or N*K/2 >= 2^31, or 2^24 workgroups or more
+ *   (max_tiles * 4 * ceil(N / 1024), rounded up to 32) (GEMM), rows*topk > 256
+ *   or K > 8192 (GEMV).
  */
 int gq_mxfp4_grouped_gemm_fp4(const uint8_t* x_blocks, const uint8_t* x_scales, int32_t rows,
                               int32_t K, const uint8_t* blocks, const uint8_t* scales,
@@ -543,7 +544,8 @@ int gq_mxfp4_grouped_gemv_fp4_swiglu(const uint8_t* x_blocks, const uint8_t* x_s
  *   d_logits     dtype [rows, E], contiguous                           out
  * InvalidValue: null pointer, unknown dtype, rows < 0, E < 1, topk < 1,
  *   forward: topk > E, stride < E, misaligned pointers.
- * NotSupported: E > 1024, topk > 64, rows > 2^33.  rows == 0 enqueues nothing.
+ * NotSupported: E > 1024, topk > 64, rows > 2^33, rows*stride >= 2^61.
+ * rows == 0 enqueues nothing.
  */
 int gq_moe_topk(const void* logits, int32_t dtype, int64_t rows, int32_t num_experts,
                 int64_t stride, int32_t topk, int32_t renormalize, int32_t* topk_ids,

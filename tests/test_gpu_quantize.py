@@ -163,3 +163,53 @@ def test_offsets_past_32_bits():
     torch.cuda.synchronize()
     _check(tail, (blocks[-2:], scales[-2:], values[-2:]))
     assert int(scales[0, 0]) == 0 and not blocks[0].any()
+
+
+def test_more_rows_than_a_launch_takes():
+    """2^35 contiguous values, whose groups of eight pass the threads of a
+    launch: the same bytes as the last rows and some in the middle have by
+    themselves, and every block written.  Inputs and codes pass 2^32 bytes."""
+    dev = device()
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of device memory")
+    rows = (1 << 30) + 5
+    say("quantize many launches", rows)
+    x = torch.zeros(rows, 32, dtype=torch.bfloat16, device=dev)
+    at = [slice(0, 100), slice((1 << 29) - 50, (1 << 29) + 50), slice(rows - 100, rows)]
+    g = torch.Generator().manual_seed(10)
+    for s in at:
+        x[s] = torch.randn(100, 32, generator=g).to(torch.bfloat16).to(dev)
+    blocks = torch.empty(rows, 1, 16, dtype=torch.uint8, device=dev)
+    blocks[rows // 3].fill_(0xA5)
+    scales = torch.full((rows, 1), 0xA5, dtype=torch.uint8, device=dev)
+    gq.gq_mxfp4_quantize(x, blocks=blocks, scales=scales)
+    torch.cuda.synchronize()
+    assert int(scales.max()) < 0xA5 and not blocks[rows // 3].any()
+    for s in at:
+        one = x[s].clone()
+        b, c, v = gq.gq_mxfp4_quantize(one, values=True)
+        torch.cuda.synchronize()
+        assert torch.equal(b, blocks[s]) and torch.equal(c, scales[s])
+        _check(one, (b, c, v))
+
+
+def test_strided_rows_past_32_bits():
+    """Rows of a wider buffer, so that a row's own offset counts: values, codes
+    and bf16 values past 2^32 bytes."""
+    dev = device()
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    rows, K, pad = (1 << 18) + 3, 1 << 15, 40
+    say("quantize strided past 32 bits", rows, K)
+    room = torch.zeros(rows, K + pad, dtype=torch.bfloat16, device=dev)
+    x = room[:, 8:8 + K]
+    at = [slice(0, 2), slice((1 << 17) - 1, (1 << 17) + 1), slice(rows - 2, rows)]
+    g = torch.Generator().manual_seed(11)
+    for s in at:
+        x[s] = torch.randn(2, K, generator=g).to(torch.bfloat16).to(dev)
+    blocks, scales, values = gq.gq_mxfp4_quantize(x, values=True)
+    torch.cuda.synchronize()
+    for s in at:
+        _check(x[s].contiguous(), (blocks[s], scales[s], values[s]))
+    for r in (2, (1 << 17) + 1, rows - 3):
+        assert not blocks[r].any() and not scales[r].any() and not values[r].any()

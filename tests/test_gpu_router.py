@@ -341,3 +341,42 @@ def test_replayed_graph(rows, dtype):
         torch.cuda.synchronize()
         for a, b in zip(held, ref):
             assert torch.equal(a, b)
+
+
+def _slices(rows, piece):
+    """Row ranges at the start, around the end of each piece and at the end."""
+    at = {0, rows - 8192}
+    at |= {b - 4096 for b in range(piece, rows, piece) if b + 4096 < rows}
+    return [slice(a, a + 8192) for a in sorted(at)]
+
+
+@pytest.mark.parametrize("E,topk,piece", [(2, 2, (1 << 28) - 16), (17, 17, (1 << 26) - 4)])
+def test_more_rows_than_a_launch_takes(E, topk, piece):
+    """Sixteen lanes a row and a wave a row, past the workgroups of a launch:
+    rows around the joint and the last ones, and no row left out.  (8192 rows
+    by themselves take the same variant.)"""
+    dev = device()
+    rows = piece + 4099
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    say("router many launches", E, topk, rows)
+    g = torch.Generator(device=dev).manual_seed(E)
+    z = torch.empty(rows, E, dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    z[::7] = -float("inf")
+    ids = torch.full((rows, topk), -7, dtype=torch.int32, device=dev)
+    w = torch.full((rows, topk), -7.0, device=dev)
+    gq.gq_moe_topk(z, topk, topk_ids=ids, topk_weights=w)
+    dw = torch.empty(rows, topk, device=dev).normal_(generator=g)
+    dz = torch.full((rows, E), float("inf"), dtype=torch.bfloat16, device=dev)
+    gq.gq_moe_topk_backward(dw, z, ids, renormalize=False, out=dz)
+    torch.cuda.synchronize()
+    assert int(ids.min()) == -1 and int(ids.max()) == E - 1
+    assert float(w.min()) == 0 and float(w.max()) <= 1
+    assert float(dz.abs().max()) < 1e3
+    for s in _slices(rows, piece):
+        say("rows", s)
+        i, v = gq.gq_moe_topk(z[s], topk)
+        d = gq.gq_moe_topk_backward(dw[s], z[s], i, renormalize=False)
+        torch.cuda.synchronize()
+        assert torch.equal(i, ids[s]) and torch.equal(v, w[s]) and torch.equal(d, dz[s])
+        _check_forward(z[s].cpu(), i, v, topk, True)

@@ -198,3 +198,25 @@ def test_short_calls_leave_what_is_not_ordinary(lib):
     with pytest.raises(KeyError):
         calls.bind({}, None, None)
     gq._load_calls(lib)                                   # bound again as it was
+
+
+def test_launches_that_the_runtime_does_not_take(lib):
+    """A launch takes fewer than 2^32 threads along a dimension: the product
+    refuses tile lists of 2^24 workgroups or more."""
+    head, tail = "x xs rows K b s E N k".split(), "off sp tl nt mt tm out".split()
+    base = dict(x=F, xs=F, rows=1 << 26, K=32, b=F, s=F, E=32, N=32, k=16, off=F, sp=F, tl=F, nt=F,
+                mt=(1 << 22) + 64, tm=256, out=F)          # 2^30 pairs, four workgroups a tile
+    plain = _caller(lib.gq_mxfp4_grouped_gemm_fp4, head + ["ps"] + tail, dict(base, ps=NULL))
+    unit = _caller(lib.gq_mxfp4_grouped_gemm_fp4_swiglu, head + ["al", "li"] + tail,
+                   dict(base, al=1.702, li=7.0))
+    for call in (plain, unit):
+        assert call() == NOT_SUPPORTED
+        assert call(rows=2048, k=4, mt=1 << 22) == NOT_SUPPORTED
+        assert call(rows=2048, k=4, N=1025, mt=1 << 21) == INVALID       # N % 32
+        assert call(rows=2048, k=4, N=1056, mt=1 << 21) == NOT_SUPPORTED
+    for rows, E in (((1 << 33) + 1, 1), ((1 << 33) + 1, 300)):
+        f = _caller(lib.gq_moe_topk, "z dt rows E zs k renorm ids w".split(),
+                    dict(z=F, dt=0, rows=rows, E=E, zs=E, k=1, renorm=1, ids=F, w=F))
+        b = _caller(lib.gq_moe_topk_backward, "dw z dt rows E zs ids k renorm dz".split(),
+                    dict(dw=F, z=F, dt=1, rows=rows, E=E, zs=E, ids=F, k=1, renorm=0, dz=F))
+        assert f() == NOT_SUPPORTED and b() == NOT_SUPPORTED
