@@ -215,6 +215,14 @@ def _dev(t, name, dtype, ndim=None):
     return t
 
 
+def _ints(what, *sizes):
+    """Sizes that the library takes in 32 bits: ctypes would pass the low half
+    of a larger one."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise GQError(f"{what}: a size of {n} is not supported", 801)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -231,6 +239,7 @@ Route = namedtuple("Route", "expert_offsets sorted_pairs tiles num_tiles max_til
 
 
 def gq_route_max_tiles(rows, topk, num_experts, tile_m=TILE_M):
+    _ints("gq_route_max_tiles", rows, topk, num_experts, tile_m)
     return int(load_library().gq_route_max_tiles(rows, topk, num_experts, tile_m))
 
 
@@ -825,6 +834,10 @@ def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
     elif values is not None and _dev(values, "values", torch.bfloat16).shape != x.shape:
         raise ValueError("values must have x's shape")
     _beside(index, blocks, scales, values)
+    if K >= 1 << 31 and stride == K and K % 32 == 0:
+        # one long run of blocks, as any number of rows of one block
+        rows, K, stride = rows * nb, 32, 32
+    _ints("gq_mxfp4_quantize", K)
     _on(index, lib.gq_mxfp4_quantize, "gq_mxfp4_quantize", x.data_ptr(), code, rows, K, stride,
         blocks.data_ptr(), scales.data_ptr(), None if values is None else values.data_ptr())
     return (blocks, scales) if values is None else (blocks, scales, values)
@@ -867,6 +880,7 @@ def _fp4_gemm(what, x, blocks, scales, route, unit, pair_scale, out):
     _beside(index, out, pair_scale, route.expert_offsets, route.sorted_pairs, route.tiles,
             route.num_tiles)
     middle = unit or (_ptr(_scale(pair_scale, P)),)
+    _ints(what, rows, K, E, N, route.topk, route.max_tiles, route.tile_m)
     _on(index, getattr(lib, what), what, xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(),
         scales.data_ptr(), E, N, route.topk, *middle, *_route_ptrs(route), out.data_ptr())
     return out
@@ -900,6 +914,7 @@ def _fp4_gemv(what, x, blocks, scales, topk_ids, unit, pair_scale, out):
     out = _out(out, P, N // 2 if unit else N, xb.device)
     _beside(index, out, pair_scale, topk_ids)
     middle = unit or (_ptr(_scale(pair_scale, P)),)
+    _ints(what, rows, K, E, N, topk_ids.shape[1])
     _on(index, getattr(lib, what), what, xb.data_ptr(), xs.data_ptr(), rows, K, blocks.data_ptr(),
         scales.data_ptr(), E, N, topk_ids.data_ptr(), topk_ids.shape[1], *middle, out.data_ptr())
     return out
@@ -939,6 +954,7 @@ def gq_moe_topk(logits, topk, renormalize=True, topk_ids=None, topk_weights=None
     dev, index, topk = logits.device, logits.get_device(), int(topk)
     if topk < 1:
         raise ValueError("topk must be at least 1")
+    _ints("gq_moe_topk", E, topk)
     shape = (rows, topk)
     if topk_ids is None:
         topk_ids = torch.empty(shape, dtype=torch.int32, device=dev)
@@ -971,6 +987,7 @@ def gq_moe_topk_backward(d_weights, logits, topk_ids, renormalize=True, out=None
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     if topk_ids.shape[0] != rows or d_weights.shape != topk_ids.shape:
         raise ValueError("d_weights and topk_ids must both be [rows, topk]")
+    _ints("gq_moe_topk_backward", E, topk_ids.shape[1])
     if out is None:
         out = torch.empty((rows, E), dtype=logits.dtype, device=dev)
     elif tuple(_dev(out, "out", logits.dtype).shape) != (rows, E):
@@ -1029,6 +1046,7 @@ def gq_moe_layer(router_weight, gate_up, down, topk, router_bias=None, gate_up_b
             raise ValueError(f"{name} must be {shape}")
     tensors = (router_weight, router_bias, *gate_up, gate_up_bias, *down, down_bias)
     _beside(dev.index, *tensors)
+    _ints("gq_moe_layer", E, int(topk), H, inner)
     ptr = [None if t is None else t.data_ptr() for t in tensors]
     struct = _LayerStruct(1 if mx else 0, E, int(topk), H, inner, 1 if renormalize else 0,
                           float(alpha), float(limit), *ptr)
@@ -1041,6 +1059,8 @@ def gq_moe_layer(router_weight, gate_up, down, topk, router_bias=None, gate_up_b
 
 def gq_moe_decode_workspace(layer, rows):
     """Bytes of workspace for ``rows`` tokens; -1 where gq_moe_decode does not take them."""
+    if rows >= 1 << 31:
+        return -1
     return int(load_library().gq_moe_decode_workspace(layer._ref, rows))
 
 

@@ -335,3 +335,11 @@ def test_layer_refuses_what_does_not_belong_together():
     for topk in (0, 7):
         with pytest.raises(gq.GQError):
             gq.gq_moe_layer(router, gu, dn, topk)
+
+
+def test_a_topk_past_32_bits_is_refused():
+    dev = device()
+    c = Case("nf4", 6, 128, 64, 2)
+    gu, dn = [tuple(to_dev(t, dev) for t in b) for b in (c.gu, c.dn)]
+    with pytest.raises(gq.GQError):
+        gq.gq_moe_layer(to_dev_bf16(c.router, dev), gu, dn, (1 << 32) + 2)

@@ -213,3 +213,26 @@ def test_strided_rows_past_32_bits():
         _check(x[s].contiguous(), (blocks[s], scales[s], values[s]))
     for r in (2, (1 << 17) + 1, rows - 3):
         assert not blocks[r].any() and not scales[r].any() and not values[r].any()
+
+
+def test_one_row_of_more_than_32_bits():
+    """A flat tensor whose length does not fit 32 bits: the bytes of its parts."""
+    dev = device()
+    n = (1 << 32) + 96                                   # the low half would be three blocks
+    say("quantize one long row", n)
+    x = torch.zeros(n, dtype=torch.bfloat16, device=dev)
+    at = [slice(0, 128), slice((1 << 31) - 64, (1 << 31) + 64), slice(n - 128, n)]
+    g = torch.Generator().manual_seed(12)
+    for s in at:
+        x[s] = torch.randn(128, generator=g).to(torch.bfloat16).to(dev)
+    blocks, scales = gq.gq_mxfp4_quantize(x)
+    assert blocks.shape == (n // 32, 16) and scales.shape == (n // 32,)
+    for s in at:
+        b = slice(s.start // 32, s.stop // 32)
+        one = x[s].clone()
+        _, _, v = gq.gq_mxfp4_quantize(one, values=True)
+        torch.cuda.synchronize()
+        _check(one, (blocks[b], scales[b], v))
+    for bad in (x[:n - 1], torch.as_strided(x, (2, 1 << 31), ((1 << 31) + 32, 1))):
+        with pytest.raises(gq.GQError):                  # not whole blocks; rows with a gap
+            gq.gq_mxfp4_quantize(bad)

@@ -380,3 +380,17 @@ def test_more_rows_than_a_launch_takes(E, topk, piece):
         torch.cuda.synchronize()
         assert torch.equal(i, ids[s]) and torch.equal(v, w[s]) and torch.equal(d, dz[s])
         _check_forward(z[s].cpu(), i, v, topk, True)
+
+
+def test_sizes_past_32_bits_are_refused():
+    dev = device()
+    say("router sizes past 32 bits")
+    wide = torch.zeros(1, (1 << 32) + 8, dtype=torch.bfloat16, device=dev)
+    z = torch.zeros(1, 8, device=dev)
+    ids, w = gq.gq_moe_topk(z, 2)
+    with pytest.raises(gq.GQError):
+        gq.gq_moe_topk(wide, 2)
+    with pytest.raises(gq.GQError):
+        gq.gq_moe_topk(z, (1 << 32) + 2)
+    with pytest.raises(gq.GQError):
+        gq.gq_moe_topk_backward(w, wide, ids)

@@ -220,3 +220,21 @@ def test_launches_that_the_runtime_does_not_take(lib):
         b = _caller(lib.gq_moe_topk_backward, "dw z dt rows E zs ids k renorm dz".split(),
                     dict(dw=F, z=F, dt=1, rows=rows, E=E, zs=E, ids=F, k=1, renorm=0, dz=F))
         assert f() == NOT_SUPPORTED and b() == NOT_SUPPORTED
+
+
+def test_sizes_past_32_bits_are_not_cut_short(lib):
+    """The library takes sizes in 32 bits; a larger one is refused, not passed
+    on as its low half."""
+    layer = gq.MoeLayer(_layer(), (), torch.device("cuda", 0))
+    assert gq.gq_moe_decode_workspace(layer, 1) > 0
+    for rows in ((1 << 32) + 1, 1 << 31, 1 << 40):
+        assert gq.gq_moe_decode_workspace(layer, rows) == -1
+    for bad in (((1 << 32) + 4, 2, 8), (4, (1 << 32) + 2, 8), (4, 2, (1 << 32) + 8),
+                (4, 2, 8, (1 << 32) + 256)):
+        with pytest.raises(gq.GQError):
+            gq.gq_route_max_tiles(*bad)
+    assert gq.gq_route_max_tiles(-1, 2, 8) == -1
+    gq._ints("sizes", 0, -1, (1 << 31) - 1, -(1 << 31))
+    for n in (1 << 31, -(1 << 31) - 1, (1 << 32) + 1):
+        with pytest.raises(gq.GQError, match="not supported"):
+            gq._ints("sizes", 1, n)
