@@ -1014,7 +1014,11 @@ class MoeLayer:
     """A layer's checked weights, made by ``gq_moe_layer``; keeps its tensors."""
 
     def __init__(self, struct, tensors, device):
-        self._struct, self._tensors, self.device = struct, tensors, device
+        self._struct, self.device = struct, device
+        # tensors of its own over the same memory: the struct holds addresses, and
+        # a caller's tensor that is given other memory (`.data = `, Module.to)
+        # would free what they name
+        self._tensors = tuple(None if t is None else t.detach() for t in tensors)
         self._ref = ctypes.addressof(struct)
         self.hidden, self.topk = struct.hidden, struct.topk
         self._bytes = {}                         # workspace bytes by token count
@@ -1028,7 +1032,9 @@ def gq_moe_layer(router_weight, gate_up, down, topk, router_bias=None, gate_up_b
     of NF4 experts [E, 2I, H] and [E, H, I] (SwiGLU, gate rows first) or
     (blocks, scales) of MXFP4 experts (the clamped unit, gate and up rows
     interleaved); the optional biases are bf16 [E], [E, 2I] and [E, H].  The
-    layer refers to these tensors: what is written into them later counts."""
+    layer refers to the memory that these tensors have now and keeps it: what is
+    written into it later counts, memory that a tensor is given later (``.data =``,
+    ``Module.to``) needs a new layer.  The memory itself must not be resized."""
     load_library()
     _dev(router_weight, "router_weight", torch.bfloat16, 2)
     E, H = router_weight.shape

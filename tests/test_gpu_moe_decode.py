@@ -343,3 +343,21 @@ def test_a_topk_past_32_bits_is_refused():
     gu, dn = [tuple(to_dev(t, dev) for t in b) for b in (c.gu, c.dn)]
     with pytest.raises(gq.GQError):
         gq.gq_moe_layer(to_dev_bf16(c.router, dev), gu, dn, (1 << 32) + 2)
+
+
+def test_tensors_given_other_memory_leave_the_layer_as_it_was():
+    dev = device()
+    c = Case("nf4", 6, 128, 64, 2, bias=True)
+    x = to_dev_bf16(_x(c, 3), dev)
+    say("moe decode tensors given other memory")
+    tensors = [to_dev_bf16(c.router, dev)] + [to_dev(t, dev) for t in (*c.gu, *c.dn)] + [
+        to_dev_bf16(b, dev) for b in c.bias]
+    layer = gq.gq_moe_layer(tensors[0], tensors[1:3], tensors[3:5], 2, router_bias=tensors[5],
+                            gate_up_bias=tensors[6], down_bias=tensors[7])
+    ref = gq.gq_moe_decode(layer, x)
+    for t in tensors:
+        t.data = torch.zeros_like(t)
+    fill = [torch.full_like(t, 1) for t in tensors for _ in range(4)]    # takes what was freed
+    y = gq.gq_moe_decode(layer, x)
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref) and len(fill) == 32

@@ -238,3 +238,15 @@ def test_sizes_past_32_bits_are_not_cut_short(lib):
     for n in (1 << 31, -(1 << 31) - 1, (1 << 32) + 1):
         with pytest.raises(gq.GQError, match="not supported"):
             gq._ints("sizes", 1, n)
+
+
+def test_a_layer_keeps_the_memory_that_it_names():
+    """A tensor given other memory leaves the layer's addresses valid."""
+    weight = torch.nn.Parameter(torch.arange(8.0))
+    was = weight.data_ptr()
+    layer = gq.MoeLayer(_layer(router_weight=was), (weight, None), torch.device("cpu"))
+    weight.data = torch.zeros(8)
+    assert weight.data_ptr() != was
+    assert [t.data_ptr() for t in layer._tensors if t is not None] == [was]
+    assert torch.equal(layer._tensors[0], torch.arange(8.0))
+    assert not layer._tensors[0].requires_grad
