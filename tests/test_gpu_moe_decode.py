@@ -361,3 +361,67 @@ def test_tensors_given_other_memory_leave_the_layer_as_it_was():
     y = gq.gq_moe_decode(layer, x)
     torch.cuda.synchronize()
     assert torch.equal(y, ref) and len(fill) == 32
+
+
+class RandomCase(Case):
+    """A layer of random bytes (made faster than packed weights)."""
+
+    def __init__(self, fmt, E, H, I, topk, rows):
+        g = np.random.default_rng([1, E, H, I, topk])
+        self.fmt, self.E, self.H, self.I, self.topk, self.renorm = fmt, E, H, I, topk, rows % 2 == 0
+        self.alpha, self.limit = 1.702, 7.0
+        self.gu, self.dn = [self.bank(g, N, K) for N, K in ((2 * I, H), (H, I))]
+        self.router = wl.draw_bf16(g, (E, H), std=0.1)
+        self.bias = [wl.draw_bf16(g, s, std=0.5) for s in ((E,), (E, 2 * I), (E, H))]
+        self.g = g
+
+    def bank(self, g, N, K):
+        codes = g.integers(0, 256, (self.E, N, K // 2), dtype=np.uint8)
+        if self.fmt == "nf4":
+            return codes, (0.02 + 0.04 * g.random((self.E, N, K // 64), dtype=np.float32))
+        return (codes.reshape(self.E, N, K // 32, 16),
+                g.integers(119, 122, (self.E, N, K // 32), dtype=np.uint8))
+
+
+@pytest.mark.parametrize("fmt,E,H,I,topk,rows", [
+    # one token, rows inside a wave, 8 and 4 rows a thread (64 slots: few columns suffice),
+    # two and eight logits a lane
+    ("nf4", 64, 1088, 512, 64, 1),
+    ("nf4", 130, 1088, 512, 64, 1),
+    ("nf4", 64, 1088, 256, 64, 1),
+    ("nf4", 130, 1088, 256, 64, 1),
+    ("nf4", 200, 128, 64, 5, 1),
+    ("mxfp4", 64, 1056, 512, 64, 1),
+    ("mxfp4", 130, 1056, 512, 64, 1),
+    ("mxfp4", 64, 1056, 256, 64, 1),
+    ("mxfp4", 130, 1056, 256, 64, 1),
+    # rows that meet in LDS, 8, 4 and 2 a thread, three and one rows' segments a workgroup
+    ("nf4", 9, 2112, 128, 8, 8),
+    ("nf4", 130, 2112, 128, 8, 8),
+    ("nf4", 9, 2112, 64, 8, 8),
+    ("nf4", 130, 2112, 64, 8, 8),
+    ("nf4", 130, 2112, 64, 2, 2),
+    ("nf4", 3, 4160, 64, 2, 8),
+    ("mxfp4", 130, 2080, 96, 8, 8),
+    ("mxfp4", 9, 2080, 64, 8, 8),
+    ("mxfp4", 130, 2080, 64, 8, 8),
+    ("mxfp4", 130, 2080, 32, 2, 2),
+    ("mxfp4", 3, 4128, 64, 2, 8),            # down: 2 steps, the last workgroup has one
+    # down products of 4, 8 and 16 steps a workgroup, of 16 with a last one of 8
+    ("nf4", 12, 2048, 768, 8, 8),
+    ("nf4", 3, 2880, 1536, 2, 8),
+    ("mxfp4", 3, 2880, 1536, 2, 8),
+    ("mxfp4", 2, 4128, 1536, 1, 8),
+    # two segments a lane in the down product, 8 and 16 steps
+    ("nf4", 2, 2048, 2112, 2, 8),
+    ("mxfp4", 2, 4128, 2080, 2, 8),
+    ("mxfp4", 3, 2880, 2880, 2, 7),
+])
+def test_every_kernel_that_the_sizes_choose(fmt, E, H, I, topk, rows):
+    dev = device()
+    c = RandomCase(fmt, E, H, I, topk, rows)
+    x = _x(c, rows)
+    say("moe decode kernels", fmt, E, H, I, topk, rows)
+    y = gq.gq_moe_decode(c.layer(dev), to_dev_bf16(x, dev))
+    torch.cuda.synchronize()
+    c.check(y, x)
