@@ -282,3 +282,54 @@ def test_binding_refuses_what_disagrees():
         gq.gq_mxfp4_grouped_gemm_fp4(x, *bank, route, pair_scale=torch.ones(4, device=dev))
     empty = gq.gq_mxfp4_grouped_gemm_fp4((x[0][:0], x[1][:0]), *bank, gq.gq_route_sort(ids[:0], 3))
     assert empty.shape == (0, 64)
+
+
+@pytest.mark.parametrize("unit", [False, True])
+@pytest.mark.parametrize("rows,topk,E,N,K", [
+    (64, 4, 4, 250, 1056), (64, 4, 4, 130, 1056),         # rows inside a wave, 8 and 4 a thread
+    (64, 4, 4, 42, 2080), (64, 4, 4, 20, 2080),           # rows that meet in LDS, 8 and 4
+    (16, 4, 5, 64, 8192), (16, 4, 5, 32, 8192),           # the same, one row's segments a workgroup
+])
+def test_single_token_form_at_every_row_count(rows, topk, E, N, K, unit):
+    dev = device()
+    g = np.random.default_rng(rows + 3 * N + K)
+    bank = packed_mx_bank(g, E, N, K)
+    ids = wl.route_uniform(g, rows, E, topk)
+    ids[2, 1] = -1
+    x, xv = _x(g, rows, K)
+    say("fp4 gemv row counts", rows, topk, E, N, K, unit)
+    args = (_both(x, dev), *_both(bank, dev), to_dev(ids, dev))
+    ref = _ref(xv, LazyDecoded("mx", *bank), ids, E, N)
+    if unit:
+        out = gq.gq_mxfp4_grouped_gemv_fp4_swiglu(*args, alpha=1.3, limit=2.0)
+        ref = oracle.swiglu_oss(ref, 1.3, 2.0) * (ids >= 0).reshape(-1, 1)
+    else:
+        out = gq.gq_mxfp4_grouped_gemv_fp4(*args)
+    torch.cuda.synchronize()
+    _check(out, ref)
+
+
+@pytest.mark.parametrize("unit", [False, True])
+@pytest.mark.parametrize("N,K,M", [(1056, 96, 900), (2336, 64, 300), (3328, 288, 40)])
+def test_more_columns_than_a_group_of_tiles(N, K, M, unit):
+    """Widths of several groups of column tiles, the last one partly filled,
+    with row tiles of every kind and dropped pairs."""
+    dev = device()
+    g = np.random.default_rng(N + K + M)
+    E, topk = 5, 2
+    bank = packed_mx_bank(g, E, N, K)
+    ids = wl.route_zipf(g, M, E, topk, s=2.0)
+    ids[g.random(ids.shape) < 0.05] = -1
+    x, xv = _x(g, M, K)
+    say("fp4 column groups", N, K, M, unit)
+    args = (_both(x, dev), *_both(bank, dev), gq.gq_route_sort(to_dev(ids, dev), E))
+    ref = _ref(xv, LazyDecoded("mx", *bank), ids, E, N)
+    shape = (M * topk, N // 2 if unit else N)
+    out = torch.full(shape, float("nan"), dtype=torch.bfloat16, device=dev)
+    if unit:
+        gq.gq_mxfp4_grouped_gemm_fp4_swiglu(*args, out=out)
+        ref = oracle.swiglu_oss(ref) * (ids >= 0).reshape(-1, 1)
+    else:
+        gq.gq_mxfp4_grouped_gemm_fp4(*args, out=out)
+    torch.cuda.synchronize()
+    _check(out, ref)

@@ -394,3 +394,21 @@ def test_sizes_past_32_bits_are_refused():
         gq.gq_moe_topk(z, (1 << 32) + 2)
     with pytest.raises(gq.GQError):
         gq.gq_moe_topk_backward(w, wide, ids)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E", [1, 33, 64, 100, 128, 200, 256])
+def test_softmax_over_all_experts_in_both_variants(dtype, E):
+    """Not renormalised, few rows and many, masked experts among them."""
+    dev = device()
+    g = torch.Generator().manual_seed(E)
+    for rows in (70, 64 * E + 4099):
+        z = torch.randn(rows, E, generator=g) * 3
+        z[torch.rand(rows, E, generator=g) < 0.3] = -float("inf")
+        z[5] = -float("inf")
+        z = z.to(dtype)
+        say("router softmax over all", dtype, E, rows)
+        ids, w = gq.gq_moe_topk(z.to(dev), min(E, 9), renormalize=False)
+        torch.cuda.synchronize()
+        at = torch.cat([torch.arange(70), torch.arange(rows - 300, rows)]) if rows > 370 else slice(0, rows)
+        _check_forward(z[at], ids[at], w[at], min(E, 9), False)
