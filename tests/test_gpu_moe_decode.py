@@ -425,3 +425,71 @@ def test_every_kernel_that_the_sizes_choose(fmt, E, H, I, topk, rows):
     y = gq.gq_moe_decode(c.layer(dev), to_dev_bf16(x, dev))
     torch.cuda.synchronize()
     c.check(y, x)
+
+
+def _choice_layer(dev, router, topk=1):
+    """An MXFP4 layer whose output names the chosen expert: weights of zero
+    and a down bias of e for expert e."""
+    E, H = router.shape
+    zeros = lambda *s: torch.zeros(s, dtype=torch.uint8, device=dev)          # noqa: E731
+    bias = torch.arange(E, device=dev, dtype=torch.bfloat16).reshape(E, 1).expand(E, H).contiguous()
+    return gq.gq_moe_layer(to_dev_bf16(router, dev), (zeros(E, 64, H // 32, 16), zeros(E, 64, H // 32)),
+                           (zeros(E, H, 1, 16), zeros(E, H, 1)), topk, down_bias=bias)
+
+
+@pytest.mark.parametrize("H,rows", [(64, 1), (64, 8), (544, 1), (2048, 8), (8192, 1), (8192, 8)])
+def test_close_experts(H, rows):
+    """Two experts whose logits differ by little more than the error that
+    their sums may have: the larger one is chosen, and of equal ones the first.
+
+    A lane adds at most H / 2048 pieces (rounded up) of four dot products; one
+    is off by at most 3 2^-24 of the magnitudes that it adds (two roundings and
+    the alignment of three terms); then 9 additions across lanes and waves and
+    the bias's, half a step each.  So a logit is off by at most u = (12 pieces +
+    10) 2^-24 of the sum of |x w|, and 2 u apart decides."""
+    dev = device()
+    for trial, x, pair, want in _close_pairs(H, rows):
+        say("moe decode close experts", H, rows, trial, want)
+        y = gq.gq_moe_decode(_choice_layer(dev, np.concatenate(pair)), to_dev_bf16(x, dev))
+        torch.cuda.synchronize()
+        assert (y.float().cpu() == want).all(), (trial, want)
+
+
+def _close_pairs(H, rows):
+    g = np.random.default_rng([H, rows])
+    f = lambda b: oracle.bf16_to_f32(b).astype(np.float64)   # noqa: E731
+    u = (12 * -(-H // 2048) + 10) * 2.0 ** -24
+    for trial in range(12):
+        x = wl.draw_bf16(g, (rows, H))
+        w = wl.draw_bf16(g, (1, H), std=0.1)
+        least = 2 * u * (np.abs(f(x)) @ np.abs(f(w[0]))).max()
+        # one weight of the second expert one or a few steps larger in magnitude,
+        # where every token has the same activation
+        steps = np.arange(1, 129, dtype=np.uint16)[:, None]
+        by = np.abs(f(x[0])) * np.abs(f(w + steps) - f(w))
+        fits = np.argwhere((by > 1.3 * least) & (by < 2.6 * least))
+        s, j = fits[g.integers(len(fits))]
+        x[:, j] = x[0, j]
+        up = w.copy()
+        up[0, j] += s + 1
+        gap = f(x[0])[j] * (f(up[0])[j] - f(w[0])[j])
+        assert 2 * u * (np.abs(f(x)) @ np.abs(f(up[0]))).max() < abs(gap)
+        yield trial, x, (w, up), int(gap > 0)
+        yield trial, x, (up, w), int(gap < 0)
+        yield trial, x, (w, w), 0
+
+
+def test_subnormal_activations_and_weights_count():
+    """bf16 subnormals of the token or of the router's weights: 2^-130 2^120 is
+    a logit like any other."""
+    dev = device()
+    tiny, big = 0x0008, 0x7B80                               # 2^-130, 2^120
+    say("moe decode subnormals")
+    for x0, w0, w1 in ((tiny, big, big + 0x80), (big, tiny, 2 * tiny)):
+        router = np.zeros((2, 64), dtype=np.uint16)
+        router[:, 5] = w0, w1
+        x = np.zeros((1, 64), dtype=np.uint16)
+        x[0, 5] = x0
+        y = gq.gq_moe_decode(_choice_layer(dev, router), to_dev_bf16(x, dev))
+        torch.cuda.synchronize()
+        assert (y.float().cpu() == 1).all()
