@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -113,9 +114,20 @@ PyObject* pack(std::initializer_list<Tensor> ts) {
 template <typename T>
 T* data(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
-// An output on the device of `like`, a tensor of its own.
+// An output on the device of `like`, which is the current one: a tensor of its
+// own, as at::empty makes it.  Where no mode or transform of this thread asks to
+// see the allocation (dispatch keys beyond the two that are always there), it
+// comes from the same allocator without a way through the dispatcher (an output
+// 0.5 to 0.7 us of a call of 5: quantise 5.76 -> 4.85 us, route sort 7.9 -> 6.3).
 Tensor output(const Tensor& like, at::ScalarType type, at::IntArrayRef sizes) {
-  return at::empty(sizes, like.options().requires_grad(false).dtype(type));
+  const auto options = like.options().requires_grad(false).dtype(type);
+  const c10::DispatchKeySet always(
+      {c10::DispatchKey::BackendSelect, c10::DispatchKey::ADInplaceOrView});
+  if (!(c10::impl::tls_local_dispatch_key_set().included_ - always).empty())
+    return at::empty(sizes, options);
+  static c10::Allocator* const from = at::empty({1}, options).storage().allocator();
+  return Tensor(at::detail::empty_generic(
+      sizes, from, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, c10::nullopt));
 }
 
 #define GQ_ARGS(count) \

@@ -204,3 +204,39 @@ def test_function_transforms_raise_alike(monkeypatch):
         for e in _both(monkeypatch, lambda: torch.func.grad(in_grad)(one)):
             assert isinstance(e, tuple) and issubclass(e[0], RuntimeError), e
         f(*args)                                          # and plain tensors as before
+
+
+def test_outputs_are_what_torch_makes():
+    """Each output has a storage of its own from torch's allocator: it grows in
+    place without its siblings, knows its streams, and its memory is counted."""
+    o = Operands()
+    say("calls: outputs like torch's")
+    layer = gq.gq_moe_layer(o.router, o.bank, o.down, 2)
+    gq.gq_moe_decode(layer, o.x)
+    q = gq.gq_mxfp4_quantize(o.x)
+    route = gq.gq_route_sort(o.ids, 4)
+    ids, w = gq.gq_moe_topk(o.z, 2)
+    for f in (lambda: gq.gq_mxfp4_quantize(o.x, values=True), lambda: gq.gq_moe_topk(o.z, 2),
+              lambda: gq.gq_route_sort(o.ids, 4)[:4],
+              lambda: (gq.gq_moe_topk_backward(w, o.z, ids),),
+              lambda: (gq.gq_moe_decode(layer, o.x),),
+              lambda: (gq.gq_mxfp4_grouped_gemv_fp4(q, *o.bank, o.ids),),
+              lambda: (gq.gq_mxfp4_grouped_gemm_fp4(q, *o.bank, route),)):
+        before = torch.cuda.memory_allocated()
+        outs = f()
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() > before
+        for t in outs:
+            like = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            assert torch._C._dispatch_keys(t) == torch._C._dispatch_keys(like)
+            assert t.device == like.device and t.stride() == like.stride() and t._version == 0
+            assert t.untyped_storage().nbytes() == t.numel() * t.element_size()
+            t.record_stream(torch.cuda.Stream())
+        kept = [t.clone() for t in outs]
+        for i, t in enumerate(outs):
+            t.resize_(1 << 16).zero_()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in list(zip(outs, kept))[i + 1:])
+        del outs, t, like, kept
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() == before

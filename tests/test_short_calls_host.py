@@ -52,7 +52,7 @@ def module(tmp_path_factory):
     with open(build.CALLS_SRC) as f:
         text = f.read()
     assert text.count("t.is_cuda()") == 1
-    text = text.replace("t.is_cuda()", "t.is_cpu()")
+    text = text.replace("t.is_cuda()", "t.is_cpu()").replace("DispatchKey::CUDA", "DispatchKey::CPU")
     text = text.replace("../../../include/gq.h", os.path.join(ROOT, "include", "gq.h"))
     src, lib = d / "calls.cpp", d / "_calls.so"
     src.write_text(text)
@@ -160,4 +160,36 @@ def test_bind_takes_all_or_nothing(module):
                 pass
             count = len(done)
             assert calls.quantize(x[0], False) is not None and len(done) == count + 1
+    """)
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_modes_see_the_allocations(module, name):
+    """A dispatch mode is told of the outputs, as of torch's own; without one
+    they are what torch.empty makes, in and out of inference mode."""
+    f, args = CALLS[name]
+    _run(module, f"""
+        from torch.utils._python_dispatch import TorchDispatchMode
+        f = {f}
+        plain = [t[0] for t in ({args},)]
+        seen = []
+        class Mode(TorchDispatchMode):
+            def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+                seen.append(str(func))
+                return func(*args, **(kwargs or {{}}))
+        flat = lambda r: r if isinstance(r, tuple) else (r,)
+        first = flat(f(*plain))
+        with Mode():
+            under = flat(f(*plain))
+        assert sum("empty" in s for s in seen) >= len(first), seen
+        with torch.inference_mode():
+            inference = flat(f(*plain))
+        for a, b, c in zip(first, under, inference):
+            like = torch.empty(a.shape, dtype=a.dtype)
+            for t in (a, b):
+                assert (t.dtype, t.shape, t.stride(), t.device, t.requires_grad, t.is_inference()) == (
+                    like.dtype, like.shape, like.stride(), like.device, False, False)
+                assert torch._C._dispatch_keys(t) == torch._C._dispatch_keys(like)
+                assert t._version == 0 and t.untyped_storage().resizable()
+            assert c.is_inference() and not c.requires_grad
     """)
