@@ -33,7 +33,13 @@ typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 constexpr int kF4K = 256;                     // k per stage
 constexpr int kF4RowBytes = kF4K / 2;
 constexpr int kF4Rsrc = 0x00027000;           // flags of a raw buffer of 32-bit data
-constexpr int kF4Small = 128;                 // tiles up to here: waves side by side
+// Tiles of up to this many rows: waves side by side, each over all of the rows
+// (the most that it can be: a wave holds four sub-tiles).  Inputs in turn, never
+// / up to 64 / up to 128 rows, us: 2048 tokens x 4 of 32, [5760, 2880] 154.3 /
+// 149.5 / 150.0; 512 tokens x 4 (64 rows an expert) 91.5 / 90.0 / 84.3; 64 x 4 of
+// 16, [2400, 2880] 20.7 / 18.6 / 18.8; 20 x 2 of 4, [1024, 2880] 18.3 / 16.1 /
+// 16.3; balanced routing, whose tiles are full, 116 each.
+constexpr int kF4Small = 128;
 
 // 16 (gate, up) pairs of a transposed block -> 16 outputs, exchanged and
 // written as store_block_act does.
@@ -116,8 +122,11 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
                           ((size_t)t.e * g.Nw + min(wn0 + tid, g.Nw - 1)) * (size_t)nb;
   // raw buffers over the activations and the expert's weights.  (Buffer loads
   // into LDS, not global ones: after a global one the compiler waits for
-  // everything in flight where it needs one earlier load or LDS read.  8192
-  // pairs on 32 experts, gate_up 151 -> 149 us.)
+  // everything in flight where it needs one earlier load or LDS read.  Global ->
+  // buffer, inputs in turn, least and most of nine: 8192 random pairs on 32
+  // experts, gate_up 152.6-153.4 -> 149.9-152.2 us, down 93.6-94.0 -> 92.8-93.1;
+  // 512 tokens x 4, gate_up 85.5-86.5 -> 84.2-84.9; one set of inputs 149.4-149.8
+  // -> 146.7-147.3.)
   const __amdgpu_buffer_rsrc_t arsrc = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint16_t*>(g.x), 0, g.P / g.topk * (g.Kw / 2), kF4Rsrc);
   const __amdgpu_buffer_rsrc_t brsrc = __builtin_amdgcn_make_buffer_rsrc(

@@ -486,7 +486,10 @@ int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, i
  * either side makes every output that its block enters NaN.
  * The _swiglu forms apply the clamped gated unit of
  * gq_mxfp4_grouped_gemv_swiglu (weight rows 2j gate, 2j + 1 up) and write
- * [rows*topk, N/2]; a NaN passes through the unit.
+ * [rows*topk, N/2]; a NaN passes through the unit.  No form takes expert
+ * biases, as none of the other products does: a model whose gate_up has one,
+ * which enters before the unit, takes the plain form and applies both itself,
+ * or gq_moe_decode.
  * InvalidValue / NotSupported: as for the named entry points; K % 32, and
  *   NotSupported: rows*K/2 or N*K/2 >= 2^31, or 2^24 workgroups or more
  *   (max_tiles * 4 * ceil(N / 1024), rounded up to 32) (GEMM), rows*topk > 256
