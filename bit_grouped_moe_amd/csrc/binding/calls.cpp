@@ -125,7 +125,8 @@ Tensor output(const Tensor& like, at::ScalarType type, at::IntArrayRef sizes) {
       {c10::DispatchKey::BackendSelect, c10::DispatchKey::ADInplaceOrView});
   if (!(c10::impl::tls_local_dispatch_key_set().included_ - always).empty())
     return at::empty(sizes, options);
-  static c10::Allocator* const from = at::empty({1}, options).storage().allocator();
+  static c10::Allocator* from = nullptr;               // (under the interpreter's lock)
+  if (!from) from = at::empty({1}, options).storage().allocator();
   return Tensor(at::detail::empty_generic(
       sizes, from, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, c10::nullopt));
 }
