@@ -1065,7 +1065,7 @@ def gq_moe_layer(router_weight, gate_up, down, topk, router_bias=None, gate_up_b
 
 def gq_moe_decode_workspace(layer, rows):
     """Bytes of workspace for ``rows`` tokens; -1 where gq_moe_decode does not take them."""
-    if rows >= 1 << 31:
+    if not 0 <= rows < 1 << 31:
         return -1
     return int(load_library().gq_moe_decode_workspace(layer._ref, rows))
 

@@ -342,7 +342,7 @@ PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) return nullptr;
   const int64_t k = v[3], P = p.rows * k;
   if (v[2] != p.rows || v[4] != p.E || k < 1 || k > INT32_MAX || v[0] < 0 || v[0] > INT32_MAX ||
-      v[1] > INT32_MAX || r[0]->numel() <= p.E || r[1]->numel() < P || r[2]->numel() < 2 * v[0] ||
+      v[1] < 0 || v[1] > INT32_MAX || r[0]->numel() <= p.E || r[1]->numel() < P || r[2]->numel() < 2 * v[0] ||
       r[3]->numel() < 1)
     Py_RETURN_NONE;
   const float* ps;

@@ -227,7 +227,7 @@ def test_sizes_past_32_bits_are_not_cut_short(lib):
     on as its low half."""
     layer = gq.MoeLayer(_layer(), (), torch.device("cuda", 0))
     assert gq.gq_moe_decode_workspace(layer, 1) > 0
-    for rows in ((1 << 32) + 1, 1 << 31, 1 << 40):
+    for rows in ((1 << 32) + 1, 1 << 31, 1 << 40, 1 - (1 << 32)):
         assert gq.gq_moe_decode_workspace(layer, rows) == -1
     for bad in (((1 << 32) + 4, 2, 8), (4, (1 << 32) + 2, 8), (4, 2, (1 << 32) + 8),
                 (4, 2, 8, (1 << 32) + 256)):

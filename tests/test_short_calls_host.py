@@ -193,3 +193,17 @@ def test_modes_see_the_allocations(module, name):
                 assert t._version == 0 and t.untyped_storage().resizable()
             assert c.is_inference() and not c.requires_grad
     """)
+
+
+def test_route_sizes_past_32_bits_are_left_to_the_python_code(module):
+    """A tile height or count whose low half would pass is not passed on."""
+    _run(module, """
+        call = lambda r: calls.fp4_gemm(xb[0], xs[0], *bank, r, None, False, 0.0, 0.0)
+        assert call(route) is not None
+        count = len(done)
+        for bad in (route._replace(tile_m=256 - (1 << 32)), route._replace(tile_m=256 + (1 << 32)),
+                    route._replace(max_tiles=3 + (1 << 32)), route._replace(max_tiles=3 - (1 << 32)),
+                    route._replace(topk=2 + (1 << 32)), route._replace(topk=2 - (1 << 32))):
+            assert call(bad) is None
+        assert len(done) == count
+    """)
