@@ -32,7 +32,8 @@ __all__ = [
     "gq_moe_decode_workspace", "gq_moe_decode", "gq_mxfp4_grouped_gemm_fp4",
     "gq_mxfp4_grouped_gemm_fp4_swiglu", "gq_mxfp4_grouped_gemv_fp4",
     "gq_mxfp4_grouped_gemv_fp4_swiglu",
-    "OSS_ALPHA", "OSS_LIMIT", "Route",
+    "gq_mxfp8_quantize", "gq_rms_norm", "gq_rms_norm_backward", "gq_rms_norm_backward_workspace",
+    "OSS_ALPHA", "OSS_LIMIT", "Route", "RmsNorm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -52,6 +53,7 @@ EXPORTED_SYMBOLS = (
     "gq_mxfp4_quantize", "gq_moe_topk", "gq_moe_topk_backward", "gq_moe_decode_workspace",
     "gq_moe_decode", "gq_mxfp4_grouped_gemm_fp4", "gq_mxfp4_grouped_gemm_fp4_swiglu",
     "gq_mxfp4_grouped_gemv_fp4", "gq_mxfp4_grouped_gemv_fp4_swiglu",
+    "gq_mxfp8_quantize", "gq_rms_norm", "gq_rms_norm_backward", "gq_rms_norm_backward_workspace",
 )
 
 _i32, _i64, _p, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -111,6 +113,12 @@ _SIGNATURES = {
                                                  _p, _p, _p]),
     "gq_mxfp4_grouped_gemv_fp4_swiglu": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p, _i32, _i32,
                                                         _p, _i32, _f32, _f32, _p, _p]),
+    "gq_mxfp8_quantize": (ctypes.c_int, [_p, _i32, _i64, _i32, _i64, _p, _p, _p, _p]),
+    "gq_rms_norm": (ctypes.c_int, [_p, _i64, _p, _i64, _i32, _i64, _i32, _p, _i32, _f32, _p, _p,
+                                   _p, _p, _p, _p]),
+    "gq_rms_norm_backward_workspace": (_i64, [_i64, _i32]),
+    "gq_rms_norm_backward": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _i32, _i64, _i32, _p,
+                                            _i32, _f32, _p, _p, _p, _i64, _p]),
     "gq_moe_decode_workspace": (_i64, [_p, _i32]),
     "gq_moe_decode": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _i64, _p, _p]),
 }
@@ -841,6 +849,149 @@ def gq_mxfp4_quantize(x, values=None, blocks=None, scales=None):
     _on(index, lib.gq_mxfp4_quantize, "gq_mxfp4_quantize", x.data_ptr(), code, rows, K, stride,
         blocks.data_ptr(), scales.data_ptr(), None if values is None else values.data_ptr())
     return (blocks, scales) if values is None else (blocks, scales, values)
+
+
+def _like(t, name, dtype, shape, dev):
+    """An output: a new tensor where ``t`` is None or True, else ``t`` checked."""
+    if t is None or t is True:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if _dev(t, name, dtype).shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    return t
+
+
+def gq_mxfp8_quantize(x, values=None, codes=None, scales=None):
+    """MXFP8 of x [..., K] (float32, bfloat16 or float16, any row stride):
+    returns (codes uint8 [..., K], OCP e4m3 in element order, scales uint8
+    [..., K/32]), the layout that the _fp8 entry points take.  ``values``: True
+    or a bf16 tensor of x's shape (x itself, if bf16 and contiguous) also
+    returns the values that the codes stand for."""
+    lib = _lib or load_library()
+    code = _typed(x, "x")
+    dev, index = x.device, x.get_device()
+    rows, K, stride = _rows(x, "x")
+    codes = _like(codes, "codes", torch.uint8, x.shape, dev)
+    scales = _like(scales, "scales", torch.uint8, torch.Size((*x.shape[:-1], K // 32)), dev)
+    values = None if values is False or values is None else _like(values, "values", torch.bfloat16,
+                                                                  x.shape, dev)
+    _beside(index, codes, scales, values)
+    if K >= 1 << 31 and stride == K and K % 32 == 0:
+        # one long run of blocks, as any number of rows of one block
+        rows, K, stride = rows * (K // 32), 32, 32
+    _ints("gq_mxfp8_quantize", K)
+    _on(index, lib.gq_mxfp8_quantize, "gq_mxfp8_quantize", x.data_ptr(), code, rows, K, stride,
+        codes.data_ptr(), scales.data_ptr(), None if values is None else values.data_ptr())
+    return (codes, scales) if values is None else (codes, scales, values)
+
+
+# ---- root-mean-square norm ---------------------------------------------------------
+RmsNorm = namedtuple("RmsNorm", "y residual mxfp8 values")
+
+
+def _gain(weight, x, H):
+    """Type code of a norm's weight."""
+    code = _typed(weight, "weight")
+    if weight.shape != (H,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be [{H}] and contiguous (got shape {tuple(weight.shape)})")
+    if weight.dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"weight must be {x.dtype} or float32 (got {weight.dtype})")
+    return code
+
+
+def _same_rows(t, like, name):
+    """Row stride of a tensor that has the shape and type of another."""
+    _typed(t, name)
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)} "
+                         f"(got {t.dtype} {tuple(t.shape)})")
+    return _rows(t, name)[2]
+
+
+def gq_rms_norm(x, weight, eps=1e-6, residual=None, y=True, sum=None, mxfp8=False, values=False):
+    """h = x + ``residual`` (rounded to x's type; h = x without one) and its
+    root-mean-square norm y = h / sqrt(mean(h^2) + eps) * weight, over the last
+    dimension of x [..., H] (float32, bfloat16 or float16; x and residual at any
+    row stride).  ``weight`` [H] is of x's type or float32.
+
+    Returns RmsNorm(y, residual, mxfp8, values): y of x's type (None with
+    ``y=False``); h, the new residual stream (None where no residual was given);
+    with ``mxfp8=True`` the pair (codes uint8 [..., H], scales uint8 [..., H/32])
+    of the unrounded y, as gq_mxfp8_quantize lays it out, and with
+    ``values=True`` also the bf16 values that the codes stand for.  ``y`` and
+    ``sum`` (for h) may be tensors to write to, x or residual among them;
+    ``mxfp8`` a pair of tensors and ``values`` a tensor likewise."""
+    lib = _lib or load_library()
+    code = _typed(x, "x")
+    dev, index = x.device, x.get_device()
+    rows, H, stride = _rows(x, "x")
+    wcode = _gain(weight, x, H)
+    rstride = 0
+    if residual is not None:
+        rstride = _same_rows(residual, x, "residual")
+        sum = _like(sum, "sum", x.dtype, x.shape, dev)
+    elif sum is not None:
+        raise ValueError("sum goes with a residual")
+    y = None if y is False or y is None else _like(y, "y", x.dtype, x.shape, dev)
+    codes = scales = None
+    if mxfp8 is not False and mxfp8 is not None:
+        if H % 32:
+            raise ValueError(f"mxfp8 takes rows of whole blocks of 32 (got {H})")
+        codes, scales = (None, None) if mxfp8 is True else mxfp8
+        codes = _like(codes, "mxfp8 codes", torch.uint8, x.shape, dev)
+        scales = _like(scales, "mxfp8 scales", torch.uint8, torch.Size((*x.shape[:-1], H // 32)),
+                       dev)
+    values = None if values is False or values is None else _like(values, "values", torch.bfloat16,
+                                                                  x.shape, dev)
+    if values is not None and codes is None:
+        raise ValueError("values goes with mxfp8")
+    _beside(index, weight, residual, sum, y, codes, scales, values)
+    _ints("gq_rms_norm", H)
+    _on(index, lib.gq_rms_norm, "gq_rms_norm", x.data_ptr(), stride, _ptr(residual), rstride, code,
+        rows, H, weight.data_ptr(), wcode, float(eps), _ptr(sum), _ptr(y), _ptr(codes),
+        _ptr(scales), _ptr(values))
+    return RmsNorm(y, sum, None if codes is None else (codes, scales), values)
+
+
+def gq_rms_norm_backward_workspace(rows, H):
+    """Bytes of workspace for gq_rms_norm_backward; -1 where it does not take the sizes."""
+    if not 0 <= rows < 1 << 63 or not 0 <= H < 1 << 31:
+        return -1
+    return int(load_library().gq_rms_norm_backward_workspace(rows, H))
+
+
+def gq_rms_norm_backward(d_y, h, weight, eps=1e-6, d_residual=None, d_x=None, d_weight=True,
+                         workspace=None):
+    """Gradients of gq_rms_norm: (d_x, d_weight) from d_y and h [..., H], the
+    forward's residual sum (its x, where there was no residual), of one type.
+    ``d_residual``: the gradient that reaches h by another way; d_x, the gradient
+    of x and of residual alike, includes it.  d_weight [H] is of weight's type;
+    ``d_weight=False`` leaves it out (None).  ``d_x`` and ``d_weight`` may be
+    tensors to write to (d_x: d_y, h or d_residual among them); ``workspace``: a
+    uint8 tensor of at least gq_rms_norm_backward_workspace bytes."""
+    lib = _lib or load_library()
+    code = _typed(h, "h")
+    dev, index = h.device, h.get_device()
+    rows, H, stride = _rows(h, "h")
+    wcode = _gain(weight, h, H)
+    dstride = _same_rows(d_y, h, "d_y")
+    rstride = 0 if d_residual is None else _same_rows(d_residual, h, "d_residual")
+    d_x = _like(d_x, "d_x", h.dtype, h.shape, dev)
+    d_weight = None if d_weight is False or d_weight is None else _like(
+        d_weight, "d_weight", weight.dtype, weight.shape, dev)
+    if d_weight is None:
+        workspace = None
+    elif workspace is None:
+        need = gq_rms_norm_backward_workspace(rows, H)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    _beside(index, weight, d_y, d_residual, d_x, d_weight, workspace)
+    _ints("gq_rms_norm_backward", H)
+    _on(index, lib.gq_rms_norm_backward, "gq_rms_norm_backward", d_y.data_ptr(), dstride,
+        h.data_ptr(), stride, _ptr(d_residual), rstride, code, rows, H, weight.data_ptr(), wcode,
+        float(eps), d_x.data_ptr(), _ptr(d_weight), _ptr(workspace),
+        0 if workspace is None else workspace.numel())
+    return d_x, d_weight
 
 
 # ---- MXFP4 x MXFP4 products --------------------------------------------------------

@@ -473,6 +473,79 @@ int gq_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, i
                       uint8_t* blocks, uint8_t* scales, uint16_t* values, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * MXFP8 quantisation on the device: what gq_mxfp4_quantize is to MXFP4, for
+ * the entry points that take 8-bit activations.
+ *   codes   uint8 [rows, K]: OCP e4m3 (NaN at 0x7F and 0xFF), in element order;
+ *           scales uint8 [rows, K/32] e8m0, 255 = NaN                  out
+ *   values  uint16 bf16 [rows, K] or NULL: the values that the codes stand for
+ *           (exact; magnitudes below 2^-133 rounded to bf16's steps, and
+ *           float32 values that round up to 2^128 infinite)           out
+ * A decoded block, quantised again, decodes to the same values.
+ * Per block of 32: X = the smallest integer in [-127, 127] with
+ * amax 2^-X <= 448, the largest e4m3 magnitude (so that no code saturates;
+ * the rule of the first term of gq_act_split_e4m3), -127 for a zero block;
+ * code = e4m3 of v 2^-X, ties to even, sign kept; scale byte X + 127.  A block
+ * with an infinity or NaN stores scale 255 and codes 0: it decodes to NaN.
+ * Arguments and errors as gq_mxfp4_quantize.
+ */
+int gq_mxfp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int64_t x_stride,
+                      uint8_t* codes, uint8_t* scales, uint16_t* values, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of rows before the experts: the residual's addition,
+ * the norm, and its result in 8 bits, in one pass.
+ *
+ *   h = x + residual, rounded to the rows' type (h = x without a residual)
+ *   y_i = h_i weight_i / sqrt(mean(h^2) + eps)
+ *
+ *   x         dtype [rows, H], row stride x_stride elements (any >= H, any
+ *             alignment of one element); residual the same, or NULL
+ *   weight    weight_dtype [H]: the rows' type or GQ_F32
+ *   sum       dtype [rows, H] or NULL: h (only with a residual)        out
+ *   y         dtype [rows, H] or NULL                                  out
+ *   codes, scales, values  or NULL: y in MXFP8, as gq_mxfp8_quantize would
+ *             write it for a float32 y (H a multiple of 32)            out
+ * float32 throughout; h and y are rounded once each, the codes are made of
+ * the unrounded y.  The norm is the norm of the rounded h.
+ * sum and y may each be x or residual where that is contiguous (they must not
+ * both be the same one); no other output may overlap an input.
+ * InvalidValue: null x or weight, no output, sum without a residual, codes
+ *   without scales or the reverse, values without codes, codes with H % 32,
+ *   unknown dtype, a weight_dtype that is neither, rows < 0, H < 1, a stride
+ *   < H, eps < 0 or not finite, a pointer not aligned to its element, codes or
+ *   values not 16-byte aligned.
+ * NotSupported: H > 32768, rows*stride >= 2^60.  rows == 0 enqueues nothing.
+ *
+ * gq_rms_norm_backward: gradients of y to x (and residual, the same) and to
+ * the weight.  With rstd = 1 / sqrt(mean(h^2) + eps), n = h rstd, g = d_y weight:
+ *   d_x_i = rstd (g_i - n_i mean(g n)) + d_h_i,  d_weight_i = sum_rows d_y_i n_i
+ *   h         dtype [rows, H]: forward's sum (x, where there was no residual)
+ *   d_h       dtype [rows, H] or NULL: the gradient of forward's sum
+ *   d_x       dtype [rows, H]                                          out
+ *   d_weight  weight_dtype [H] or NULL: not wanted                     out
+ *   workspace 16-byte aligned device memory of at least
+ *             gq_rms_norm_backward_workspace(rows, H) bytes (with d_weight);
+ *             carries nothing from one call to the next; two calls that may
+ *             run at the same time need one each
+ * float32 sums in a fixed order; rows == 0 writes d_weight = 0.  The gradient
+ * of codes is taken as y's (straight through).  d_x may be d_y, h or d_h where
+ * that is contiguous.
+ * Errors as gq_rms_norm; InvalidValue also for a workspace that is too small.
+ * gq_rms_norm_backward_workspace returns -1 for rows < 0 or an H outside
+ * [1, 32768].
+ */
+int gq_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                int32_t dtype, int64_t rows, int32_t H, const void* weight, int32_t weight_dtype,
+                float eps, void* sum, void* y, uint8_t* codes, uint8_t* scales, uint16_t* values,
+                hipStream_t stream);
+int64_t gq_rms_norm_backward_workspace(int64_t rows, int32_t H);
+int gq_rms_norm_backward(const void* d_y, int64_t d_y_stride, const void* h, int64_t h_stride,
+                         const void* d_h, int64_t d_h_stride, int32_t dtype, int64_t rows,
+                         int32_t H, const void* weight, int32_t weight_dtype, float eps, void* d_x,
+                         void* d_weight, void* workspace, int64_t workspace_bytes,
+                         hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * MXFP4 activations times MXFP4 experts, on the e2m1 x e2m1 block-scaled
  * matrix instruction ([P1] "Which entry point?": native MXFP4 expert math).
  *

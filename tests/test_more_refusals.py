@@ -1,0 +1,94 @@
+"""What the norm, the 8-bit quantiser, the routing with groups and the 8-bit
+products refuse, on the host: malformed arguments to the C ABI (nothing is
+enqueued, no GPU is needed) and to the Python binding."""
+
+import ctypes
+
+import pytest
+import torch
+
+import bit_grouped_moe_amd as gq
+
+INVALID, NOT_SUPPORTED = 1, 801
+F = ctypes.c_void_p(0x1000)          # a fake, aligned, never-dereferenced pointer
+F1 = ctypes.c_void_p(0x1001)
+F2 = ctypes.c_void_p(0x1002)
+F8 = ctypes.c_void_p(0x1008)
+NULL = None
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return gq.load_library()
+
+
+def _caller(fn, names, ok):
+    def call(**kw):
+        assert set(kw) <= set(names)
+        return fn(*[{**ok, **kw}[n] for n in names], None)
+    return call
+
+
+def test_quantize_rejects(lib):
+    call = _caller(lib.gq_mxfp8_quantize, "x dt rows K xs c s v".split(),
+                   dict(x=F, dt=1, rows=4, K=64, xs=64, c=F, s=F, v=NULL))
+    for bad in (dict(x=NULL), dict(c=NULL), dict(s=NULL), dict(dt=3), dict(dt=-1), dict(rows=-1),
+                dict(K=0), dict(K=-32), dict(K=48), dict(xs=63), dict(xs=0), dict(xs=-64),
+                dict(x=F1), dict(x=F2, dt=0), dict(c=F8), dict(v=F8)):
+        assert call(**bad) == INVALID, bad
+    assert call(xs=1 << 62) == NOT_SUPPORTED
+    assert call(rows=0, x=NULL, c=NULL, s=NULL) == 0
+
+
+def test_norm_rejects(lib):
+    call = _caller(lib.gq_rms_norm, "x xs r rs dt rows H w wdt eps sum y c s v".split(),
+                   dict(x=F, xs=64, r=F, rs=64, dt=1, rows=4, H=64, w=F, wdt=1, eps=1e-6, sum=F,
+                        y=F, c=F, s=F, v=F))
+    nan, inf = float("nan"), float("inf")
+    for bad in (dict(x=NULL), dict(w=NULL), dict(dt=3), dict(wdt=2), dict(wdt=3), dict(dt=0, x=F),
+                dict(rows=-1), dict(H=0), dict(H=-64), dict(xs=63), dict(rs=63), dict(rs=0),
+                dict(eps=-1.0), dict(eps=nan), dict(eps=inf), dict(r=NULL), dict(c=NULL),
+                dict(s=NULL), dict(c=NULL, s=NULL), dict(H=63), dict(x=F1), dict(r=F1), dict(w=F1),
+                dict(sum=F1), dict(y=F1), dict(c=F8), dict(v=F8),
+                dict(w=F2, wdt=0), dict(sum=NULL, y=NULL, c=NULL, s=NULL, v=NULL)):
+        assert call(**bad) == INVALID, bad
+    assert call(H=32800, xs=32800, rs=32800) == NOT_SUPPORTED
+    assert call(xs=1 << 62) == NOT_SUPPORTED
+    assert call(rs=1 << 62) == NOT_SUPPORTED
+    assert call(rows=1 << 50, H=32768, xs=32768, rs=32768) == NOT_SUPPORTED
+    assert call(rows=0, x=NULL, w=NULL, y=NULL) == 0
+
+
+def test_norm_backward_rejects(lib):
+    call = _caller(lib.gq_rms_norm_backward,
+                   "dy dys h hs dh dhs dt rows H w wdt eps dx dw ws wn".split(),
+                   dict(dy=F, dys=64, h=F, hs=64, dh=F, dhs=64, dt=2, rows=4, H=64, w=F, wdt=2,
+                        eps=1e-6, dx=F, dw=F, ws=F, wn=1 << 30))
+    for bad in (dict(dy=NULL), dict(h=NULL), dict(w=NULL), dict(dx=NULL), dict(ws=NULL),
+                dict(wn=64 * 4 - 1), dict(ws=F8), dict(dt=3), dict(wdt=1), dict(rows=-1),
+                dict(H=0), dict(dys=63), dict(hs=63), dict(dhs=63), dict(eps=-1e-6), dict(dy=F1),
+                dict(h=F1), dict(dh=F1), dict(w=F1), dict(dx=F1), dict(dw=F1),
+                dict(dw=F2, wdt=0)):
+        assert call(**bad) == INVALID, bad
+    assert call(H=32769, dys=32769, hs=32769, dhs=32769) == NOT_SUPPORTED
+    assert call(hs=1 << 62) == NOT_SUPPORTED
+    assert call(dhs=1 << 62) == NOT_SUPPORTED
+    assert call(rows=0, dw=NULL) == 0
+    assert lib.gq_rms_norm_backward_workspace(-1, 64) == -1
+    assert lib.gq_rms_norm_backward_workspace(4, 0) == -1
+    assert lib.gq_rms_norm_backward_workspace(4, 32769) == -1
+    assert lib.gq_rms_norm_backward_workspace(0, 64) == 0
+    assert gq.gq_rms_norm_backward_workspace(1 << 70, 64) == -1
+    assert gq.gq_rms_norm_backward_workspace(4, 1 << 40) == -1
+
+
+def test_binding_takes_device_tensors_only():
+    x, w = torch.zeros(2, 64), torch.ones(64)
+    for call in (lambda: gq.gq_mxfp8_quantize(x), lambda: gq.gq_rms_norm(x, w),
+                 lambda: gq.gq_rms_norm_backward(x, x, w)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: gq.gq_mxfp8_quantize(None), lambda: gq.gq_rms_norm([1.0], w),
+                 lambda: gq.gq_rms_norm_backward(x, None, w)):
+        with pytest.raises(TypeError):
+            call()
