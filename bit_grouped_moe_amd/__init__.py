@@ -33,6 +33,8 @@ __all__ = [
     "gq_mxfp4_grouped_gemm_fp4_swiglu", "gq_mxfp4_grouped_gemv_fp4",
     "gq_mxfp4_grouped_gemv_fp4_swiglu",
     "gq_mxfp8_quantize", "gq_rms_norm", "gq_rms_norm_backward", "gq_rms_norm_backward_workspace",
+    "gq_mxfp4_grouped_gemm_fp8", "gq_mxfp4_grouped_gemm_fp8_swiglu",
+    "gq_mxfp4_grouped_gemv_fp8", "gq_mxfp4_grouped_gemv_fp8_swiglu",
     "OSS_ALPHA", "OSS_LIMIT", "Route", "RmsNorm",
 ]
 
@@ -54,6 +56,8 @@ EXPORTED_SYMBOLS = (
     "gq_moe_decode", "gq_mxfp4_grouped_gemm_fp4", "gq_mxfp4_grouped_gemm_fp4_swiglu",
     "gq_mxfp4_grouped_gemv_fp4", "gq_mxfp4_grouped_gemv_fp4_swiglu",
     "gq_mxfp8_quantize", "gq_rms_norm", "gq_rms_norm_backward", "gq_rms_norm_backward_workspace",
+    "gq_mxfp4_grouped_gemm_fp8", "gq_mxfp4_grouped_gemm_fp8_swiglu",
+    "gq_mxfp4_grouped_gemv_fp8", "gq_mxfp4_grouped_gemv_fp8_swiglu",
 )
 
 _i32, _i64, _p, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -122,6 +126,9 @@ _SIGNATURES = {
     "gq_moe_decode_workspace": (_i64, [_p, _i32]),
     "gq_moe_decode": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _i64, _p, _p]),
 }
+for _n in ("gemm_fp4", "gemm_fp4_swiglu", "gemv_fp4", "gemv_fp4_swiglu"):
+    _SIGNATURES["gq_mxfp4_grouped_" + _n.replace("fp4", "fp8")] = _SIGNATURES["gq_mxfp4_grouped_"
+                                                                              + _n]
 
 _lib = None
 _calls = None                      # the short calls (csrc/binding/calls.cpp), when built
@@ -994,31 +1001,35 @@ def gq_rms_norm_backward(d_y, h, weight, eps=1e-6, d_residual=None, d_x=None, d_
     return d_x, d_weight
 
 
-# ---- MXFP4 x MXFP4 products --------------------------------------------------------
-def _mx_pair(x, blocks, scales, unit):
-    """Checks of an MXFP4 x MXFP4 product: (x blocks, x scales, rows, E, N, K)."""
+# ---- MXFP4 or MXFP8 x MXFP4 products ------------------------------------------------
+def _mx_pair(x, bits, blocks, scales, unit):
+    """Checks of a product of MXFP4 or MXFP8 activations with MXFP4 experts: (x
+    codes, x scales, rows, E, N, K)."""
     xb, xs = x[0], x[1]
-    _dev(xb, "x blocks", torch.uint8, 3)
+    _dev(xb, "x blocks" if bits == 4 else "x codes", torch.uint8, 3 if bits == 4 else 2)
     _dev(xs, "x scales", torch.uint8, 2)
     E, N, K = _mx_bank(blocks, scales)
     rows, nb = xb.shape[0], K // 32
-    if xb.shape != (rows, nb, 16) or xs.shape != (rows, nb):
+    if bits == 4 and (xb.shape != (rows, nb, 16) or xs.shape != (rows, nb)):
         raise ValueError(f"x must be (blocks [rows, {nb}, 16], scales [rows, {nb}]) as "
                          "gq_mxfp4_quantize returns them")
+    if bits == 8 and (xb.shape != (rows, K) or xs.shape != (rows, nb)):
+        raise ValueError(f"x must be (codes [rows, {K}], scales [rows, {nb}]) as "
+                         "gq_mxfp8_quantize returns them")
     if unit and N % 2:
         raise ValueError("the gate_up width is odd")
     _beside(xb.get_device(), xs, blocks, scales)
     return xb, xs, rows, E, N, K
 
 
-def _fp4_gemm(what, x, blocks, scales, route, unit, pair_scale, out):
+def _mx_gemm(what, bits, x, blocks, scales, route, unit, pair_scale, out):
     lib = _lib or load_library()
-    if _calls and out is None:
+    if _calls and out is None and bits == 4:
         r = _calls.fp4_gemm(x[0], x[1], blocks, scales, route, pair_scale, unit is not None,
                             *(unit or (0.0, 0.0)))
         if r is not None:
             return _done(r, what)
-    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit is not None)
+    xb, xs, rows, E, N, K = _mx_pair(x, bits, blocks, scales, unit is not None)
     if route.rows != rows or route.num_experts != E:
         raise ValueError("x, blocks and route disagree")
     index = xb.get_device()
@@ -1040,25 +1051,25 @@ def _fp4_gemm(what, x, blocks, scales, route, unit, pair_scale, out):
 def gq_mxfp4_grouped_gemm_fp4(x, blocks, scales, route, pair_scale=None, out=None):
     """Prefill grouped GEMM of MXFP4 activations with MXFP4 experts; ``x`` =
     gq_mxfp4_quantize(activations [rows, K]).  Returns bf16 [rows*topk, N]."""
-    return _fp4_gemm("gq_mxfp4_grouped_gemm_fp4", x, blocks, scales, route, None, pair_scale, out)
+    return _mx_gemm("gq_mxfp4_grouped_gemm_fp4", 4, x, blocks, scales, route, None, pair_scale, out)
 
 
 def gq_mxfp4_grouped_gemm_fp4_swiglu(x, blocks, scales, route, alpha=OSS_ALPHA, limit=OSS_LIMIT,
                                      out=None):
     """gq_mxfp4_grouped_gemm_fp4 on gate_up experts [E, 2I, K] (gate row 2j,
     up row 2j + 1) with gpt-oss's gated unit: bf16 [rows*topk, I]."""
-    return _fp4_gemm("gq_mxfp4_grouped_gemm_fp4_swiglu", x, blocks, scales, route,
+    return _mx_gemm("gq_mxfp4_grouped_gemm_fp4_swiglu", 4, x, blocks, scales, route,
                      (float(alpha), float(limit)), None, out)
 
 
-def _fp4_gemv(what, x, blocks, scales, topk_ids, unit, pair_scale, out):
+def _mx_gemv(what, bits, x, blocks, scales, topk_ids, unit, pair_scale, out):
     lib = _lib or load_library()
-    if _calls and out is None:
+    if _calls and out is None and bits == 4:
         r = _calls.fp4_gemv(x[0], x[1], blocks, scales, topk_ids, pair_scale, unit is not None,
                             *(unit or (0.0, 0.0)))
         if r is not None:
             return _done(r, what)
-    xb, xs, rows, E, N, K = _mx_pair(x, blocks, scales, unit is not None)
+    xb, xs, rows, E, N, K = _mx_pair(x, bits, blocks, scales, unit is not None)
     index = xb.get_device()
     _dev(topk_ids, "topk_ids", torch.int32, 2)
     P = _gemv_pairs(topk_ids, rows)
@@ -1074,7 +1085,7 @@ def _fp4_gemv(what, x, blocks, scales, topk_ids, unit, pair_scale, out):
 def gq_mxfp4_grouped_gemv_fp4(x, blocks, scales, topk_ids, pair_scale=None, out=None):
     """Decode-time product (<= 256 pairs) of MXFP4 activations with MXFP4
     experts; ``x`` = gq_mxfp4_quantize(activations).  Returns bf16 [rows*topk, N]."""
-    return _fp4_gemv("gq_mxfp4_grouped_gemv_fp4", x, blocks, scales, topk_ids, None, pair_scale,
+    return _mx_gemv("gq_mxfp4_grouped_gemv_fp4", 4, x, blocks, scales, topk_ids, None, pair_scale,
                      out)
 
 
@@ -1082,8 +1093,38 @@ def gq_mxfp4_grouped_gemv_fp4_swiglu(x, blocks, scales, topk_ids, alpha=OSS_ALPH
                                      limit=OSS_LIMIT, out=None):
     """gq_mxfp4_grouped_gemv_fp4 on gate_up experts with gpt-oss's gated unit:
     bf16 [rows*topk, I]."""
-    return _fp4_gemv("gq_mxfp4_grouped_gemv_fp4_swiglu", x, blocks, scales, topk_ids,
+    return _mx_gemv("gq_mxfp4_grouped_gemv_fp4_swiglu", 4, x, blocks, scales, topk_ids,
                      (float(alpha), float(limit)), None, out)
+
+
+def gq_mxfp4_grouped_gemm_fp8(x, blocks, scales, route, pair_scale=None, out=None):
+    """Prefill grouped GEMM of MXFP8 activations with MXFP4 experts; ``x`` =
+    gq_mxfp8_quantize(activations [rows, K]) or gq_rms_norm's ``mxfp8``.
+    Returns bf16 [rows*topk, N]."""
+    return _mx_gemm("gq_mxfp4_grouped_gemm_fp8", 8, x, blocks, scales, route, None, pair_scale, out)
+
+
+def gq_mxfp4_grouped_gemm_fp8_swiglu(x, blocks, scales, route, alpha=OSS_ALPHA, limit=OSS_LIMIT,
+                                     out=None):
+    """gq_mxfp4_grouped_gemm_fp8 on gate_up experts [E, 2I, K] (gate row 2j,
+    up row 2j + 1) with gpt-oss's gated unit: bf16 [rows*topk, I]."""
+    return _mx_gemm("gq_mxfp4_grouped_gemm_fp8_swiglu", 8, x, blocks, scales, route,
+                    (float(alpha), float(limit)), None, out)
+
+
+def gq_mxfp4_grouped_gemv_fp8(x, blocks, scales, topk_ids, pair_scale=None, out=None):
+    """Decode-time product (<= 256 pairs) of MXFP8 activations with MXFP4
+    experts; ``x`` = gq_mxfp8_quantize(activations).  Returns bf16 [rows*topk, N]."""
+    return _mx_gemv("gq_mxfp4_grouped_gemv_fp8", 8, x, blocks, scales, topk_ids, None, pair_scale,
+                    out)
+
+
+def gq_mxfp4_grouped_gemv_fp8_swiglu(x, blocks, scales, topk_ids, alpha=OSS_ALPHA,
+                                     limit=OSS_LIMIT, out=None):
+    """gq_mxfp4_grouped_gemv_fp8 on gate_up experts with gpt-oss's gated unit:
+    bf16 [rows*topk, I]."""
+    return _mx_gemv("gq_mxfp4_grouped_gemv_fp8_swiglu", 8, x, blocks, scales, topk_ids,
+                    (float(alpha), float(limit)), None, out)
 
 
 # ---- expert routing --------------------------------------------------------------

@@ -21,18 +21,13 @@
 // (their rows start at any byte).  One barrier per stage.
 #include <type_traits>
 
-#include "gemm_common.hpp"
+#include "gemm_mx.hpp"
 #include "../../include/gq.h"
 
 namespace gq {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
-
 constexpr int kF4K = 256;                     // k per stage
 constexpr int kF4RowBytes = kF4K / 2;
-constexpr int kF4Rsrc = 0x00027000;           // flags of a raw buffer of 32-bit data
 // Tiles of up to this many rows: waves side by side, each over all of the rows
 // (the most that it can be: a wave holds four sub-tiles).  Inputs in turn, never
 // / up to 64 / up to 128 rows, us: 2048 tokens x 4 of 32, [5760, 2880] 154.3 /
@@ -40,65 +35,6 @@ constexpr int kF4Rsrc = 0x00027000;           // flags of a raw buffer of 32-bit
 // 16, [2400, 2880] 20.7 / 18.6 / 18.8; 20 x 2 of 4, [1024, 2880] 18.3 / 16.1 /
 // 16.3; balanced routing, whose tiles are full, 116 each.
 constexpr int kF4Small = 128;
-
-// 16 (gate, up) pairs of a transposed block -> 16 outputs, exchanged and
-// written as store_block_act does.
-__device__ __forceinline__ void store_unit(const float (&v)[16], uint16_t* orow, int lh,
-                                           float alpha, float limit) {
-  uint32_t o[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    o[q] = pack_bf16x2(clamped_unit(v[4 * q], v[4 * q + 1], alpha, limit),
-                       clamped_unit(v[4 * q + 2], v[4 * q + 3], alpha, limit));
-  const auto a = __builtin_amdgcn_permlane32_swap(o[0], o[2], false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(o[1], o[3], false, false);
-  *reinterpret_cast<u32x4*>(orow + 8 * lh) = u32x4{a[0], a[1], b[0], b[1]};
-}
-
-// The tile of a workgroup.  Blocks are dealt to the 8 XCDs in turn, each with
-// an L2 of its own; kGroup column tiles of a row tile go to one XCD, which so
-// fetches the tile's activations for all of them, and row tiles, full and
-// short ones, spread evenly (8192 pairs on 32 experts, gate_up / down: all
-// column tiles of a row tile on one XCD 162 / 79 us, one column tile at a
-// time 154 / 92, four 157 / 81).  Tiles past the last expert tile clear the
-// rows of dropped pairs.  A tile entry that cannot come from gq_route_sort is
-// rejected.
-constexpr int kGroup = 4;
-template <int kTNo>
-__device__ __forceinline__ bool fp4_head(const GemmArgs& g, int tid, TileInfo& t, int& pair) {
-  const int bid = blockIdx.x;
-  const int q = bid >> 3, xcd = bid & 7;
-  const int groups = (g.n_col_tiles + kGroup - 1) / kGroup;
-  const int unit = (q / kGroup) * 8 + xcd;
-  const int tile = unit / groups;
-  const int col = (unit % groups) * kGroup + q % kGroup;
-  if (tile >= g.max_tiles || col >= g.n_col_tiles) return false;
-  t.n0 = col * kTNo;
-  // the tile count and the tile's entry in one round trip (entries past the
-  // count hold no expert)
-  const int T = *g.num_tiles;
-  t.e = g.tiles[2 * tile];
-  t.start = g.tiles[2 * tile + 1];
-  if (tile >= T) {
-    const int dstart = g.offsets[g.E] + (tile - T) * kTM;
-    if (dstart >= g.P || dstart < 0) return false;
-    const int dvalid = min(kTM, g.P - dstart);
-    for (int idx = tid; idx < dvalid * (kTNo / 8); idx += kGemmThreads) {
-      const int r = idx / (kTNo / 8), c = t.n0 + idx % (kTNo / 8) * 8;
-      const int p = g.sorted_pairs[dstart + r];
-      if (c < g.Nout && (unsigned)p < (unsigned)g.P)
-        *reinterpret_cast<u32x4*>(g.out + (int64_t)p * g.Nout + c) = u32x4{0u, 0u, 0u, 0u};
-    }
-    return false;
-  }
-  if ((unsigned)t.e >= (unsigned)g.E || (unsigned)t.start >= (unsigned)g.P) return false;
-  // the segment's end and its pairs in the next
-  const int end = g.offsets[t.e + 1];
-  const int p = g.sorted_pairs[min(t.start + tid, g.P - 1)];
-  t.valid = min(kTM, min(end, g.P) - t.start);
-  pair = (unsigned)p < (unsigned)g.P ? p : 0;
-  return t.valid > 0;
-}
 
 // kWide: waves 2 x 2, a wave takes every second 32-row sub-tile (so that the
 // row halves stay balanced when the tile is not full) and 128 columns; else
@@ -128,10 +64,10 @@ __device__ __forceinline__ void fp4_tile(const GemmArgs& g, const TileInfo& t, i
   // 512 tokens x 4, gate_up 85.5-86.5 -> 84.2-84.9; one set of inputs 149.4-149.8
   // -> 146.7-147.3.)
   const __amdgpu_buffer_rsrc_t arsrc = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint16_t*>(g.x), 0, g.P / g.topk * (g.Kw / 2), kF4Rsrc);
+      const_cast<uint16_t*>(g.x), 0, g.P / g.topk * (g.Kw / 2), kRawBuffer);
   const __amdgpu_buffer_rsrc_t brsrc = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(g.codes) + (size_t)t.e * g.Nw * (size_t)(g.Kw / 2), 0,
-      g.Nw * (g.Kw / 2), kF4Rsrc);
+      g.Nw * (g.Kw / 2), kRawBuffer);
   // ---- loads: 8 rows of 128 bytes per instruction, rows 8 (4 j + wave) + ..;
   // lane L fills the 16-byte slot L % 8 of row L / 8 with the chunk that the
   // swizzle puts there ((row >> 1) & 7 = 4 (wave & 1) + (L >> 4)).  Rows past
@@ -364,7 +300,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_fp4_kernel(GemmA
   const int tid = threadIdx.x;
   TileInfo t;
   int pair = 0;
-  if (!fp4_head<kUnit ? kXN / 2 : kXN>(g, tid, t, pair)) return;
+  if (!mx_head<kUnit ? kXN / 2 : kXN>(g, tid, t, pair)) return;
   if (t.valid <= kF4Small)
     fp4_tile<false, kUnit>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s, scale_s,
                            pair);
@@ -380,41 +316,12 @@ static int fp4_entry(const uint8_t* x_blocks, const uint8_t* x_scales, int32_t r
                      const int32_t* expert_offsets, const int32_t* sorted_pairs,
                      const int32_t* tiles, const int32_t* num_tiles, int32_t max_tiles,
                      int32_t tile_m, uint16_t* out, hipStream_t stream) {
-  if (rows < 0 || topk < 1 || num_experts < 1 || N < 1 || N % 32 || K <= 0 || K % 32)
-    return kInvalid;
-  if (kUnit && !(limit >= 0.f && limit < 3.4e38f && alpha > -3.4e38f && alpha < 3.4e38f))
-    return kInvalid;                                       // finite alpha, limit >= 0
-  if (tile_m != kTM) return kNotSupported;
-  const int64_t P = (int64_t)rows * topk;
-  if (P >= INT32_MAX) return kNotSupported;
-  if (P == 0) return kOk;                                  // nothing to enqueue
-  // 32-bit offsets of a row inside the activations and inside one expert
-  if ((int64_t)rows * (K / 2) >= INT32_MAX || (int64_t)N * (K / 2) >= INT32_MAX)
-    return kNotSupported;
-  if (!x_blocks || !x_scales || !blocks || !scales || !expert_offsets || !sorted_pairs || !tiles ||
-      !num_tiles || !out)
-    return kInvalid;
-  if (!aligned16(x_blocks) || !aligned16(blocks) || !aligned16(out)) return kInvalid;
-  if (!aligned4(expert_offsets) || !aligned4(sorted_pairs) || !aligned4(tiles) ||
-      !aligned4(num_tiles) || (pair_scale && !aligned4(pair_scale)))
-    return kInvalid;
-  const int64_t need = (P + kTM - 1) / kTM + num_experts + 1;
-  if (max_tiles < need) return kInvalid;
   GemmArgs g{};
-  g.x = reinterpret_cast<const uint16_t*>(x_blocks);
-  g.xs = x_scales;
-  g.xs_stride = K / 32;
-  g.codes = blocks; g.scl = scales;
-  g.Nw = N; g.Kw = K; g.Kc = K; g.Nout = kUnit ? N / 2 : N;
-  g.E = num_experts; g.topk = topk; g.P = (int)P; g.pair_scale = pair_scale;
-  g.offsets = expert_offsets; g.sorted_pairs = sorted_pairs; g.tiles = tiles;
-  g.num_tiles = num_tiles; g.out = out;
-  g.act_alpha = alpha; g.act_limit = limit;
-  g.n_col_tiles = (N + kXN - 1) / kXN;                     // 256 weight rows per tile
-  const int64_t units = (int64_t)max_tiles * ceil_div64(g.n_col_tiles, kGroup);
-  const int64_t grid = ceil_div64(units, 8) * 8 * kGroup;
-  if (grid > most_groups(kGemmThreads)) return kNotSupported;
-  g.max_tiles = max_tiles;
+  int64_t grid = 0;
+  const int st = mx_gemm_args(g, grid, kUnit, x_blocks, x_scales, rows, K, K / 2, blocks, scales,
+                              num_experts, N, topk, pair_scale, alpha, limit, expert_offsets,
+                              sorted_pairs, tiles, num_tiles, max_tiles, tile_m, out);
+  if (st != kOk || grid == 0) return st;
   hipLaunchKernelGGL(grouped_gemm_fp4_kernel<kUnit>, dim3((unsigned)grid), dim3(kGemmThreads), 0,
                      stream, g);
   return launch_status();

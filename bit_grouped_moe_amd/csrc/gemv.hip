@@ -58,13 +58,14 @@ constexpr int kGemvMaxK = 8192;     // 256 segments of 32 weights
 // for a bank in pinned host memory (a separate instance, so that profiles
 // keep the host-link launches apart from the HBM ones).
 //
-// kXq (MXFP4 weights): the activations are MXFP4 too, x the blocks (row
-// stride x_stride bytes / 2, i.e. K / 4) and x_scales the scale bytes [rows,
-// K / 32].  A lane's segment is one block: 16 bytes and a scale instead of
-// 64 bytes, turned into the same bf16 pairs (exact), and the two scales are
-// applied to the segment's sum together (the sum of 32 products of e2m1
-// values is exact, so nothing rounds before the segments are added).
-template <bool kMx, int kIter, bool kWaveRows, int kAct, bool kHostBank = false, bool kXq = false>
+// kXq (MXFP4 weights): the activations are MXFP4 (4) or MXFP8 (8) too, x the
+// codes (row stride x_stride bytes / 2, i.e. K / 4 or K / 2) and x_scales the
+// scale bytes [rows, K / 32].  A lane's segment is one block: 16 or 32 bytes and
+// a scale instead of 64 bytes, turned into the same bf16 pairs (exact), and the
+// two scales are applied to the segment's sum together (the sum of 32 products
+// of e2m1 values is exact, so that nothing rounds before the segments are added;
+// of e4m3 with e2m1 values it is a float32 sum).
+template <bool kMx, int kIter, bool kWaveRows, int kAct, bool kHostBank = false, int kXq = 0>
 __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
     const int32_t* __restrict__ ids, const uint16_t* __restrict__ x,
     const uint8_t* __restrict__ codes, const void* __restrict__ scl, int K, int N, int E,
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
     uint16_t* __restrict__ out, float alpha, float limit,
     const uint8_t* __restrict__ x_scales) {
   constexpr bool kGlu = kAct != 0;
-  static_assert(!kXq || kMx, "MXFP4 activations go with MXFP4 weights");
+  static_assert(!kXq || kMx, "quantised activations go with MXFP4 weights");
   __shared__ __attribute__((aligned(4096))) LutT lut[kLutN];
   __shared__ float red[kWaveRows ? 1 : kIter * (kGemvMaxThreads + 32)];
 
@@ -131,10 +132,12 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
   }
   u32x4 xr[4];
   uint32_t sx = 0u;                                 // kXq: the block's scale byte
-  auto load_xq = [&](int p) {                       // codes in xr[0], expanded by compute_pair
+  auto load_xq = [&](int p) {                       // codes, expanded by compute_pair
     const int64_t row = p / topk;
     const int sg = active ? s : 0;
-    xr[0] = *reinterpret_cast<const u32x4*>(x + row * x_stride + sg * 8);
+    xr[0] = *reinterpret_cast<const u32x4*>(x + row * x_stride + sg * (2 * kXq));
+    if constexpr (kXq == 8)
+      xr[1] = *reinterpret_cast<const u32x4*>(x + row * x_stride + sg * (2 * kXq) + 8);
     sx = (uint32_t)x_scales[row * (K / 32) + sg];
   };
   if constexpr (kXq) {
@@ -228,7 +231,15 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
     }
   };
   auto compute_pair = [&]() {
-    if constexpr (kXq) {
+    if constexpr (kXq == 8) {
+      const u32x4 q[2] = {xr[0], xr[1]};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const uint32_t a = q[v / 2][2 * (v & 1)], b = q[v / 2][2 * (v & 1) + 1];
+        xr[v] = u32x4{e4m3_pair_bf16(a, 0), e4m3_pair_bf16(a, 1), e4m3_pair_bf16(b, 0),
+                      e4m3_pair_bf16(b, 1)};
+      }
+    } else if constexpr (kXq == 4) {
       const u32x4 q = xr[0];
 #pragma unroll
       for (int v = 0; v < 4; ++v)
@@ -371,7 +382,7 @@ __global__ __launch_bounds__(kGemvMaxThreads) void grouped_gemv_kernel(
   }
 }
 
-template <bool kMx, int kIter, int kAct, bool kHostBank, bool kXq>
+template <bool kMx, int kIter, int kAct, bool kHostBank, int kXq>
 static void launch_gemv_iter(dim3 grid, int NT, bool wave_rows, hipStream_t stream,
                              const uint16_t* x, int x_stride, int K, const uint8_t* codes,
                              const void* scl, int N, int E, const int32_t* ids, int topk, int P,
@@ -387,7 +398,7 @@ static void launch_gemv_iter(dim3 grid, int NT, bool wave_rows, hipStream_t stre
                        pair_scale, out, alpha, limit, xs);
 }
 
-template <bool kMx, int kAct, bool kHostBank = false, bool kXq = false>
+template <bool kMx, int kAct, bool kHostBank = false, int kXq = 0>
 static int launch_gemv(const uint16_t* x, int32_t rows, int32_t K, int64_t x_stride,
                        const uint8_t* codes, const void* scl, int32_t E, int32_t N,
                        const int32_t* ids, int32_t topk, const float* pair_scale, uint16_t* out,
@@ -791,7 +802,7 @@ extern "C" int gq_mxfp4_grouped_gemv_fp4(const uint8_t* x_blocks, const uint8_t*
                                          const int32_t* topk_ids, int32_t topk,
                                          const float* pair_scale, uint16_t* out,
                                          hipStream_t stream) {
-  return gq::launch_gemv<true, 0, false, true>(
+  return gq::launch_gemv<true, 0, false, 4>(
       reinterpret_cast<const uint16_t*>(x_blocks), rows, K, K / 4, blocks, scales, num_experts, N,
       topk_ids, topk, pair_scale, out, stream, 0.f, 0.f, x_scales);
 }
@@ -802,7 +813,29 @@ extern "C" int gq_mxfp4_grouped_gemv_fp4_swiglu(const uint8_t* x_blocks, const u
                                                 int32_t N, const int32_t* topk_ids, int32_t topk,
                                                 float alpha, float limit, uint16_t* act,
                                                 hipStream_t stream) {
-  return gq::launch_gemv<true, 2, false, true>(
+  return gq::launch_gemv<true, 2, false, 4>(
       reinterpret_cast<const uint16_t*>(x_blocks), rows, K, K / 4, blocks, scales, num_experts, N,
+      topk_ids, topk, nullptr, act, stream, alpha, limit, x_scales);
+}
+
+extern "C" int gq_mxfp4_grouped_gemv_fp8(const uint8_t* x_codes, const uint8_t* x_scales,
+                                         int32_t rows, int32_t K, const uint8_t* blocks,
+                                         const uint8_t* scales, int32_t num_experts, int32_t N,
+                                         const int32_t* topk_ids, int32_t topk,
+                                         const float* pair_scale, uint16_t* out,
+                                         hipStream_t stream) {
+  return gq::launch_gemv<true, 0, false, 8>(
+      reinterpret_cast<const uint16_t*>(x_codes), rows, K, K / 2, blocks, scales, num_experts, N,
+      topk_ids, topk, pair_scale, out, stream, 0.f, 0.f, x_scales);
+}
+
+extern "C" int gq_mxfp4_grouped_gemv_fp8_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,
+                                                int32_t rows, int32_t K, const uint8_t* blocks,
+                                                const uint8_t* scales, int32_t num_experts,
+                                                int32_t N, const int32_t* topk_ids, int32_t topk,
+                                                float alpha, float limit, uint16_t* act,
+                                                hipStream_t stream) {
+  return gq::launch_gemv<true, 2, false, 8>(
+      reinterpret_cast<const uint16_t*>(x_codes), rows, K, K / 2, blocks, scales, num_experts, N,
       topk_ids, topk, nullptr, act, stream, alpha, limit, x_scales);
 }

@@ -212,6 +212,14 @@ __device__ __forceinline__ uint32_t e2m1_pair_bf16_scaled(uint32_t d, int byte_i
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// ---- MXFP8 ---------------------------------------------------------------
+// Two e4m3 codes of half `half` of a dword as a bf16 pair (exact).
+__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t d, int half) {
+  const bf16x2 v = half ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true)
+                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false);
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // ---- wave / block helpers ---------------------------------------------------
 // Workgroup barrier that orders LDS only.  __syncthreads() fences every
 // address space, which makes each wave wait for ALL of its outstanding

@@ -595,6 +595,45 @@ int gq_mxfp4_grouped_gemv_fp4_swiglu(const uint8_t* x_blocks, const uint8_t* x_s
                                      float limit, uint16_t* act, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * MXFP8 activations times MXFP4 experts, on the e4m3 x e2m1 block-scaled
+ * matrix instruction: half the matrix work of the two-term split of
+ * gq_mxfp4_grouped_gemm_scaled, with the activations' rounding of 8 bits.
+ *
+ *   out[p, n] = bf16( pair_scale[p] * sum_k xq[p/topk, k] * W_{ids[p]}[n, k] )
+ *
+ * x_codes uint8 [rows, K] and x_scales uint8 [rows, K/32] are what
+ * gq_mxfp8_quantize and gq_rms_norm write; everything else, the errors
+ * included, is as for the _fp4 entry points of the same name (x_codes 16-byte
+ * aligned; NotSupported: rows*K >= 2^31 in the GEMM).  An e4m3 NaN code makes
+ * every output that it enters NaN, as scale byte 255 does.
+ */
+int gq_mxfp4_grouped_gemm_fp8(const uint8_t* x_codes, const uint8_t* x_scales, int32_t rows,
+                              int32_t K, const uint8_t* blocks, const uint8_t* scales,
+                              int32_t num_experts, int32_t N, int32_t topk,
+                              const float* pair_scale, const int32_t* expert_offsets,
+                              const int32_t* sorted_pairs, const int32_t* tiles,
+                              const int32_t* num_tiles, int32_t max_tiles, int32_t tile_m,
+                              uint16_t* out, hipStream_t stream);
+int gq_mxfp4_grouped_gemm_fp8_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,
+                                     int32_t rows, int32_t K, const uint8_t* blocks,
+                                     const uint8_t* scales, int32_t num_experts, int32_t N,
+                                     int32_t topk, float alpha, float limit,
+                                     const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                                     const int32_t* tiles, const int32_t* num_tiles,
+                                     int32_t max_tiles, int32_t tile_m, uint16_t* act,
+                                     hipStream_t stream);
+int gq_mxfp4_grouped_gemv_fp8(const uint8_t* x_codes, const uint8_t* x_scales, int32_t rows,
+                              int32_t K, const uint8_t* blocks, const uint8_t* scales,
+                              int32_t num_experts, int32_t N, const int32_t* topk_ids,
+                              int32_t topk, const float* pair_scale, uint16_t* out,
+                              hipStream_t stream);
+int gq_mxfp4_grouped_gemv_fp8_swiglu(const uint8_t* x_codes, const uint8_t* x_scales,
+                                     int32_t rows, int32_t K, const uint8_t* blocks,
+                                     const uint8_t* scales, int32_t num_experts, int32_t N,
+                                     const int32_t* topk_ids, int32_t topk, float alpha,
+                                     float limit, uint16_t* act, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Expert routing ([P4] "Functions": the routing tensor [M, top_k] and its
  * weights, which the other entry points take).
  *
