@@ -35,6 +35,7 @@ __all__ = [
     "gq_mxfp8_quantize", "gq_rms_norm", "gq_rms_norm_backward", "gq_rms_norm_backward_workspace",
     "gq_mxfp4_grouped_gemm_fp8", "gq_mxfp4_grouped_gemm_fp8_swiglu",
     "gq_mxfp4_grouped_gemv_fp8", "gq_mxfp4_grouped_gemv_fp8_swiglu",
+    "gq_moe_route", "gq_moe_route_backward",
     "OSS_ALPHA", "OSS_LIMIT", "Route", "RmsNorm",
 ]
 
@@ -58,6 +59,7 @@ EXPORTED_SYMBOLS = (
     "gq_mxfp8_quantize", "gq_rms_norm", "gq_rms_norm_backward", "gq_rms_norm_backward_workspace",
     "gq_mxfp4_grouped_gemm_fp8", "gq_mxfp4_grouped_gemm_fp8_swiglu",
     "gq_mxfp4_grouped_gemv_fp8", "gq_mxfp4_grouped_gemv_fp8_swiglu",
+    "gq_moe_route", "gq_moe_route_backward",
 )
 
 _i32, _i64, _p, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -117,6 +119,10 @@ _SIGNATURES = {
                                                  _p, _p, _p]),
     "gq_mxfp4_grouped_gemv_fp4_swiglu": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p, _i32, _i32,
                                                         _p, _i32, _f32, _f32, _p, _p]),
+    "gq_moe_route": (ctypes.c_int, [_p, _i32, _i64, _i32, _i64, _p, _i32, _i32, _i32, _i32, _i32,
+                                    _i32, _f32, _p, _p, _p]),
+    "gq_moe_route_backward": (ctypes.c_int, [_p, _p, _i32, _i64, _i32, _i64, _p, _i32, _i32, _i32,
+                                             _f32, _p, _p]),
     "gq_mxfp8_quantize": (ctypes.c_int, [_p, _i32, _i64, _i32, _i64, _p, _p, _p, _p]),
     "gq_rms_norm": (ctypes.c_int, [_p, _i64, _p, _i64, _i32, _i64, _i32, _p, _i32, _f32, _p, _p,
                                    _p, _p, _p, _p]),
@@ -1188,6 +1194,76 @@ def gq_moe_topk_backward(d_weights, logits, topk_ids, renormalize=True, out=None
     _on(index, lib.gq_moe_topk_backward, "gq_moe_topk_backward", d_weights.data_ptr(),
         logits.data_ptr(), code, rows, E, stride, topk_ids.data_ptr(), topk_ids.shape[1],
         1 if renormalize else 0, out.data_ptr())
+    return out
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score):
+    code = _SCORES.get(score)
+    if code is None:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid' (got {score!r})")
+    return code
+
+
+def gq_moe_route(logits, topk, score="softmax", bias=None, groups=1, topk_groups=None, group_top=1,
+                 renormalize=True, scale=1.0, topk_ids=None, topk_weights=None):
+    """Routing with groups: the ``topk`` experts of largest choice score + ``bias``
+    among the ``topk_groups`` (all when None) best of ``groups`` groups of
+    neighbouring experts, for logits [rows, E] (float32, bfloat16 or float16).
+    ``score``: "softmax" or "sigmoid" of the logits; ``bias`` float32 [E] only
+    enters the choice; a group counts as the sum of its ``group_top`` (1 or 2)
+    largest choices.  Returns (topk_ids int32 [rows, topk], topk_weights float32
+    [rows, topk]), the weights ``scale`` times the chosen scores, divided by their
+    sum with ``renormalize``.  Ties go to the lower index; a logit of -inf is never
+    chosen; a slot left without an expert has id -1 and weight 0."""
+    lib = _lib or load_library()
+    code = _typed(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
+    rows, E, stride = _rows(logits, "logits")
+    dev, index, topk, groups = logits.device, logits.get_device(), int(topk), int(groups)
+    kind = _score(score)
+    if topk < 1:
+        raise ValueError("topk must be at least 1")
+    if groups < 1 or E % groups:
+        raise ValueError(f"groups must divide the {E} experts (got {groups})")
+    topk_groups = groups if topk_groups is None else int(topk_groups)
+    if bias is not None and _dev(bias, "bias", torch.float32).shape != (E,):
+        raise ValueError(f"bias must be [{E}]")
+    _ints("gq_moe_route", E, topk, groups, topk_groups, int(group_top))
+    shape = torch.Size((rows, topk))
+    topk_ids = _like(topk_ids, "topk_ids", torch.int32, shape, dev)
+    topk_weights = _like(topk_weights, "topk_weights", torch.float32, shape, dev)
+    _beside(index, bias, topk_ids, topk_weights)
+    _on(index, lib.gq_moe_route, "gq_moe_route", logits.data_ptr(), code, rows, E, stride,
+        _ptr(bias), topk, kind, groups, topk_groups, int(group_top), 1 if renormalize else 0,
+        float(scale), topk_ids.data_ptr(), topk_weights.data_ptr())
+    return topk_ids, topk_weights
+
+
+def gq_moe_route_backward(d_weights, logits, topk_ids, score="softmax", renormalize=True,
+                          scale=1.0, out=None):
+    """Gradient of ``gq_moe_route``'s weights to its logits, the selection held
+    fixed: d_weights float32 [rows, topk] -> [rows, E] of the logits' type."""
+    lib = _lib or load_library()
+    code = _typed(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
+    rows, E, stride = _rows(logits, "logits")
+    kind = _score(score)
+    _dev(d_weights, "d_weights", torch.float32, 2)
+    _dev(topk_ids, "topk_ids", torch.int32, 2)
+    if topk_ids.shape[0] != rows or d_weights.shape != topk_ids.shape:
+        raise ValueError("d_weights and topk_ids must both be [rows, topk]")
+    _ints("gq_moe_route_backward", E, topk_ids.shape[1])
+    out = _like(out, "out", logits.dtype, torch.Size((rows, E)), logits.device)
+    index = logits.get_device()
+    _beside(index, d_weights, topk_ids, out)
+    _on(index, lib.gq_moe_route_backward, "gq_moe_route_backward", d_weights.data_ptr(),
+        logits.data_ptr(), code, rows, E, stride, topk_ids.data_ptr(), topk_ids.shape[1], kind,
+        1 if renormalize else 0, float(scale), out.data_ptr())
     return out
 
 

@@ -14,30 +14,9 @@
 // (moe_topk_group_kernel below): a quarter of the instructions and a longer
 // chain, for many rows of up to 256 experts and 16 slots.  Sums are DPP sums
 // in a fixed order.
-#include <type_traits>
-
-#include "topk.hpp"
-#include "gq_host.hpp"
-#include "../../include/gq.h"
+#include "router.hpp"
 
 namespace gq {
-
-constexpr int kRouterThreads = 256;
-constexpr int kWaveRows = kRouterThreads / kWave;        // rows of a workgroup, a wave each
-
-template <int kType>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if constexpr (kType == GQ_F32) return static_cast<const float*>(p)[i];
-  else if constexpr (kType == GQ_BF16)
-    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  else return (float)static_cast<const _Float16*>(p)[i];
-}
-template <int kType>
-__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-  if constexpr (kType == GQ_F32) static_cast<float*>(p)[i] = v;
-  else if constexpr (kType == GQ_BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16_bits(v);
-  else static_cast<_Float16*>(p)[i] = (_Float16)v;
-}
 
 template <int kType, int C>
 __global__ __launch_bounds__(kRouterThreads) void moe_topk_kernel(
@@ -72,10 +51,12 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_kernel(
   }
 }
 
-template <int kType, int C>
+// kSigmoid: the scores are sigmoids, w = s or s / sum s over the slots, whose
+// gradient is g s (1 - s) or w (1 - s) (g - sum w g).  factor: of the weights.
+template <int kType, int C, bool kSigmoid>
 __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
     const float* __restrict__ dw, const void* __restrict__ logits, int64_t rows, int E,
-    int64_t stride, const int32_t* __restrict__ ids, int topk, int renorm,
+    int64_t stride, const int32_t* __restrict__ ids, int topk, int renorm, float factor,
     void* __restrict__ dz) {
   const int lane = threadIdx.x & (kWave - 1);
   const int64_t row =
@@ -88,7 +69,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
   id = (unsigned)id < (unsigned)E ? id : -1;
   float g = 0.f, zs = -kInf;
   if (id >= 0) {
-    g = dw[row * topk + lane];
+    g = dw[row * topk + lane] * factor;
     zs = load1<kType>(logits, row * stride + id);
     if (zs == -kInf) { id = -1; g = 0.f; }               // a masked expert has no weight
   }
@@ -96,17 +77,19 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
 #pragma unroll
   for (int c = 0; c < C; ++c) key[c] = 0u;
   uint32_t best = id >= 0 ? logit_key(zs) : 0u;
-  if (!renorm) {
+  if (!kSigmoid && !renorm) {
     wave_keys<C>(E, lane, [&](int e) { return load1<kType>(logits, row * stride + e); }, key);
 #pragma unroll
     for (int c = 0; c < C; ++c) best = max(best, key[c]);
   }
   const uint32_t m = wave_umax(best);
   const float peak = m > kDeadKey ? key_logit(m) : 0.f;
-  const float part = id >= 0 ? expf(zs - peak) : 0.f;
+  const float part = id < 0     ? 0.f
+                     : kSigmoid ? sigmoid_over(zs, renorm && peak <= 0.f ? peak : 0.f)
+                                : expf(zs - peak);
   float p[C];
   float sum = part;
-  if (!renorm) {
+  if (!kSigmoid && !renorm) {
     sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -114,12 +97,13 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
       sum += p[c];
     }
   }
-  const float total = wave_fsum(sum);
+  const float total = kSigmoid && !renorm ? 1.f : wave_fsum(sum);
   const float inv = m > kDeadKey ? 1.f / total : 0.f;    // no live expert: no gradient
   const float w = part * inv;                            // slot weight
-  const float dot = wave_fsum(w * g);
+  const float dot = kSigmoid && !renorm ? 0.f : wave_fsum(w * g);
   // what slot s adds to its expert, in slot order
-  const float add = renorm ? w * (g - dot) : g;
+  float add = kSigmoid || renorm ? w * (g - dot) : g;
+  if (kSigmoid && id >= 0) add *= 1.0f / (1.0f + expf(zs));
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int e = 64 * c + lane;
@@ -130,7 +114,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
       const float as = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(add), s));
       acc += is == e ? as : 0.f;
     }
-    if (!renorm) acc = p[c] * inv * (acc - dot);
+    if (!kSigmoid && !renorm) acc = p[c] * inv * (acc - dot);
     if (e < E) store1<kType>(dz, row * E + e, acc);
   }
 }
@@ -329,11 +313,11 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_group_kernel(
 // Gradients of the slots meet in the row's floats in LDS, added slot by slot
 // (one lane a row at a time, so an expert that is named twice adds in slot
 // order), and every lane then writes its experts' gradients.
-template <int kType, int C>
+template <int kType, int C, bool kSigmoid>
 __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_group_kernel(
     const float* __restrict__ dw, const void* __restrict__ logits, int64_t rows, int E,
-    int64_t stride, const int32_t* __restrict__ ids, int topk, int renorm, int wide_in,
-    int wide_out, void* __restrict__ dz) {
+    int64_t stride, const int32_t* __restrict__ ids, int topk, int renorm, float factor,
+    int wide_in, int wide_out, void* __restrict__ dz) {
   using Row = GroupRow<kType, C>;
   using raw = typename Row::raw;
   __shared__ __align__(16) float acc[kGroupRows][C * kGroup];
@@ -349,13 +333,13 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_group_kernel
   id = (unsigned)id < (unsigned)E ? id : -1;
   float g = 0.f, zs = -kInf;
   if (id >= 0) {
-    g = dw[row * topk + l];
+    g = dw[row * topk + l] * factor;
     zs = Row::value(z[id]);
     if (zs == -kInf) { id = -1; g = 0.f; }               // a masked expert has no weight
   }
   uint32_t best = id >= 0 ? logit_key(zs) : 0u;
   Row x;
-  if (!renorm) {
+  if (!kSigmoid && !renorm) {
     x.load(z, l, E, wide_in);
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -363,10 +347,12 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_group_kernel
   }
   const uint32_t m = group_max(best);
   const float peak = m > kDeadKey ? key_logit(m) : 0.f;
-  const float part = id >= 0 ? expf(zs - peak) : 0.f;
+  const float part = id < 0     ? 0.f
+                     : kSigmoid ? sigmoid_over(zs, renorm && peak <= 0.f ? peak : 0.f)
+                                : expf(zs - peak);
   float p[C];
   float sum = part;
-  if (!renorm) {
+  if (!kSigmoid && !renorm) {
     sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -375,11 +361,12 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_group_kernel
       sum += p[c];
     }
   }
-  const float total = group_sum_last(sum, kGroup);
+  const float total = kSigmoid && !renorm ? 1.f : group_sum_last(sum, kGroup);
   const float inv = m > kDeadKey ? 1.f / total : 0.f;    // no live expert: no gradient
   const float w = part * inv;                            // slot weight
-  const float dot = group_sum_last(w * g, kGroup);
-  const float add = renorm ? w * (g - dot) : g;
+  const float dot = kSigmoid && !renorm ? 0.f : group_sum_last(w * g, kGroup);
+  float add = kSigmoid || renorm ? w * (g - dot) : g;
+  if (kSigmoid && id >= 0) add *= 1.0f / (1.0f + expf(zs));
   for (int s = 0; s < topk; ++s) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -391,7 +378,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_group_kernel
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     float v = sums[C * l + c];
-    if (!renorm) v = p[c] * inv * (v - dot);
+    if (!kSigmoid && !renorm) v = p[c] * inv * (v - dot);
     x.r[c] = Row::bits(v);
   }
   x.store(static_cast<raw*>(dz) + row * E, l, E, wide_out);
@@ -411,44 +398,6 @@ static bool group_wide(const void* p, int E, int64_t pitch) {
   constexpr int kSize = (int)sizeof(typename GroupRow<kType, C>::raw);
   constexpr uintptr_t kMask = GroupRow<kType, C>::kUnit - 1;
   return E % C == 0 && ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(pitch * kSize)) & kMask) == 0;
-}
-
-template <typename F>
-static void by_width(int E, F&& f) {
-  if (E <= 64) f(std::integral_constant<int, 1>{});
-  else if (E <= 128) f(std::integral_constant<int, 2>{});
-  else if (E <= 256) f(std::integral_constant<int, 4>{});
-  else if (E <= 512) f(std::integral_constant<int, 8>{});
-  else f(std::integral_constant<int, 16>{});
-}
-
-// launch(first row, rows) over pieces of the rows: a launch takes 2^24 - 1
-// workgroups of `group` rows (2^26 - 4 rows a wave each, 2^28 - 16 sixteen lanes).
-template <typename F>
-static void by_rows(int64_t rows, int group, F&& launch) {
-  const int64_t most = most_groups(kRouterThreads) * group;
-  for (int64_t at = 0; at < rows; at += most) launch(at, rows - at < most ? rows - at : most);
-}
-template <int kType>
-static const void* row_at(const void* p, int64_t element) {
-  return static_cast<const char*>(p) + element * (kType == GQ_F32 ? 4 : 2);
-}
-template <int kType>
-static void* row_at(void* p, int64_t element) {
-  return static_cast<char*>(p) + element * (kType == GQ_F32 ? 4 : 2);
-}
-
-static int router_checks(const void* logits, int32_t dtype, int64_t rows, int32_t E,
-                         int64_t stride, int32_t topk, const void* a, const void* b,
-                         const void* c) {
-  if (dtype != GQ_F32 && dtype != GQ_BF16 && dtype != GQ_F16) return kInvalid;
-  if (rows < 0 || E < 1 || topk < 1 || stride < E) return kInvalid;
-  if (E > kTopkMaxExperts || topk > kTopkMax) return kNotSupported;
-  if (rows == 0) return kOk;
-  const uintptr_t mask = dtype == GQ_F32 ? 3 : 1;
-  if (!logits || !a || !b || !c || (reinterpret_cast<uintptr_t>(logits) & mask)) return kInvalid;
-  if (rows > (int64_t)1 << 33 || stride > INT64_MAX / 4 / rows) return kNotSupported;
-  return kOk;
 }
 
 }  // namespace gq
@@ -494,11 +443,13 @@ extern "C" int gq_moe_topk(const void* logits, int32_t dtype, int64_t rows, int3
   return launch_status();
 }
 
-extern "C" int gq_moe_topk_backward(const float* d_weights, const void* logits, int32_t dtype,
-                                    int64_t rows, int32_t num_experts, int64_t stride,
-                                    const int32_t* topk_ids, int32_t topk, int32_t renormalize,
-                                    void* d_logits, hipStream_t stream) {
-  using namespace gq;
+namespace gq {
+
+template <bool kSigmoid>
+static int backward_entry(const float* d_weights, const void* logits, int32_t dtype, int64_t rows,
+                          int32_t num_experts, int64_t stride, const int32_t* topk_ids,
+                          int32_t topk, int32_t renormalize, float factor, void* d_logits,
+                          hipStream_t stream) {
   const int st = router_checks(logits, dtype, rows, num_experts, stride, topk, d_weights,
                                topk_ids, d_logits);
   if (st != kOk || rows == 0) return st;
@@ -512,10 +463,10 @@ extern "C" int gq_moe_topk_backward(const float* d_weights, const void* logits, 
       by_group<kGroupMaxExperts>(num_experts, [&](auto c) {
         constexpr int C = decltype(c)::value;
         by_rows(rows, kGroupRows, [&](int64_t at, int64_t n) {
-          hipLaunchKernelGGL((moe_topk_backward_group_kernel<T, C>),
+          hipLaunchKernelGGL((moe_topk_backward_group_kernel<T, C, kSigmoid>),
                              dim3((unsigned)ceil_div64(n, kGroupRows)), dim3(kRouterThreads), 0,
                              stream, d_weights + at * topk, row_at<T>(logits, at * stride), n,
-                             num_experts, stride, topk_ids + at * topk, topk, renormalize,
+                             num_experts, stride, topk_ids + at * topk, topk, renormalize, factor,
                              (int)group_wide<T, C>(logits, num_experts, stride),
                              (int)group_wide<T, C>(d_logits, num_experts, num_experts),
                              row_at<T>(d_logits, at * num_experts));
@@ -525,10 +476,10 @@ extern "C" int gq_moe_topk_backward(const float* d_weights, const void* logits, 
     }
     by_width(num_experts, [&](auto c) {
       by_rows(rows, kWaveRows, [&](int64_t at, int64_t n) {
-        hipLaunchKernelGGL((moe_topk_backward_kernel<T, decltype(c)::value>),
+        hipLaunchKernelGGL((moe_topk_backward_kernel<T, decltype(c)::value, kSigmoid>),
                            dim3((unsigned)ceil_div64(n, kWaveRows)), dim3(kRouterThreads), 0,
                            stream, d_weights + at * topk, row_at<T>(logits, at * stride), n,
-                           num_experts, stride, topk_ids + at * topk, topk, renormalize,
+                           num_experts, stride, topk_ids + at * topk, topk, renormalize, factor,
                            row_at<T>(d_logits, at * num_experts));
       });
     });
@@ -537,4 +488,29 @@ extern "C" int gq_moe_topk_backward(const float* d_weights, const void* logits, 
   else if (dtype == GQ_BF16) go(std::integral_constant<int, GQ_BF16>{});
   else go(std::integral_constant<int, GQ_F16>{});
   return launch_status();
+}
+
+}  // namespace gq
+
+extern "C" int gq_moe_topk_backward(const float* d_weights, const void* logits, int32_t dtype,
+                                    int64_t rows, int32_t num_experts, int64_t stride,
+                                    const int32_t* topk_ids, int32_t topk, int32_t renormalize,
+                                    void* d_logits, hipStream_t stream) {
+  return gq::backward_entry<false>(d_weights, logits, dtype, rows, num_experts, stride, topk_ids,
+                                   topk, renormalize, 1.0f, d_logits, stream);
+}
+
+extern "C" int gq_moe_route_backward(const float* d_weights, const void* logits, int32_t dtype,
+                                     int64_t rows, int32_t num_experts, int64_t stride,
+                                     const int32_t* topk_ids, int32_t topk, int32_t score,
+                                     int32_t renormalize, float scale, void* d_logits,
+                                     hipStream_t stream) {
+  using namespace gq;
+  if ((score != GQ_SOFTMAX && score != GQ_SIGMOID) || !(scale > -3.4e38f && scale < 3.4e38f))
+    return kInvalid;
+  return score == GQ_SIGMOID
+             ? backward_entry<true>(d_weights, logits, dtype, rows, num_experts, stride, topk_ids,
+                                    topk, renormalize, scale, d_logits, stream)
+             : backward_entry<false>(d_weights, logits, dtype, rows, num_experts, stride, topk_ids,
+                                     topk, renormalize, scale, d_logits, stream);
 }

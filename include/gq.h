@@ -670,6 +670,52 @@ int gq_moe_topk_backward(const float* d_weights, const void* logits, int32_t dty
                          int32_t topk, int32_t renormalize, void* d_logits, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Expert routing as models with many experts do it: scores of either kind, a
+ * bias that balances the experts' load, and groups of experts.
+ *
+ *   s_e = softmax(z)_e or sigmoid(z_e);   c_e = s_e + bias_e
+ * gq_moe_route: the experts lie in `groups` groups of E / groups neighbours.  A
+ * group counts as the sum of its group_top (1 or 2) largest c; the topk_groups
+ * largest groups are open, equal ones by lower index.  topk_ids are the topk
+ * largest c of the open groups, largest first, equal ones by lower index.
+ * Weights are of the scores without the bias:
+ *   w_s = scale s_s   or   scale s_s / sum of the chosen s   (renormalize != 0)
+ * c and the groups' sums are compared in float64.  Without a bias the experts are
+ * in the order of their logits (and so are groups of group_top 1), of which the
+ * scores are increasing functions.  groups = 1 leaves groups out.  The bias
+ * takes no gradient.
+ * A logit of -inf, or a c of -inf, is a masked expert: it is never chosen, a group
+ * counts without it, a group of masked experts is never open, and a slot that
+ * only masked experts are left for gets id -1 and weight 0.  A NaN counts above
+ * every number; a sigmoid's NaN makes its own weight NaN and, renormalised, its
+ * row's; a NaN or +inf logit makes a softmax row's weights NaN.  Renormalised
+ * weights are right also where every chosen score is too small for a float32.
+ *   logits   dtype [rows, E], row stride `stride` elements; bias float [E] or NULL
+ *   topk_ids int32 [rows, topk], topk_weights float [rows, topk]      out
+ *
+ * gq_moe_route_backward: gradient of the weights to the logits, the selection
+ * held fixed.  For each slot s of expert j, with G = scale d_weights:
+ *   sigmoid  d_z_j += G_s s_j (1 - s_j), or renormalised, with n = s / sum s,
+ *            d_z_j += n_s (1 - s_j) (G_s - sum_i n_i G_i)
+ *   softmax  as gq_moe_topk_backward of G
+ * ids outside [0, E) and masked logits take none; an id in several slots counts
+ * once per slot.
+ * InvalidValue: as gq_moe_topk / gq_moe_topk_backward; unknown score, groups < 1
+ *   or not a divisor of E, topk_groups outside [1, groups], group_top not 1 or
+ *   2, topk > topk_groups * E / groups, scale not finite, bias misaligned.
+ * NotSupported: as there; groups > 64.
+ */
+enum { GQ_SOFTMAX = 0, GQ_SIGMOID = 1 };
+int gq_moe_route(const void* logits, int32_t dtype, int64_t rows, int32_t num_experts,
+                 int64_t stride, const float* bias, int32_t topk, int32_t score, int32_t groups,
+                 int32_t topk_groups, int32_t group_top, int32_t renormalize, float scale,
+                 int32_t* topk_ids, float* topk_weights, hipStream_t stream);
+int gq_moe_route_backward(const float* d_weights, const void* logits, int32_t dtype, int64_t rows,
+                          int32_t num_experts, int64_t stride, const int32_t* topk_ids,
+                          int32_t topk, int32_t score, int32_t renormalize, float scale,
+                          void* d_logits, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * A whole mixture-of-experts layer for a few tokens: router product,
  * selection, the experts' gated products and the weighted combine.
  *

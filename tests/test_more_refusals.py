@@ -87,8 +87,8 @@ def test_fp8_products_reject(lib):
     gemm = dict(x=F, xs=F, rows=2048, K=2880, b=F, s=F, E=32, N=5760, k=4, off=F, sp=F, tl=F, nt=F,
                 mt=32 + 33 + 1, tm=256, out=F)
     head, tail = "x xs rows K b s E N k".split(), "off sp tl nt mt tm out".split()
-    plain = _caller(lib.gq_mxfp8_grouped_gemm_fp8, head + ["ps"] + tail, dict(gemm, ps=NULL))
-    unit = _caller(lib.gq_mxfp8_grouped_gemm_fp8_swiglu, head + ["al", "li"] + tail,
+    plain = _caller(lib.gq_mxfp4_grouped_gemm_fp8, head + ["ps"] + tail, dict(gemm, ps=NULL))
+    unit = _caller(lib.gq_mxfp4_grouped_gemm_fp8_swiglu, head + ["al", "li"] + tail,
                    dict(gemm, al=1.702, li=7.0))
     for call in (plain, unit):
         for bad in (dict(x=NULL), dict(xs=NULL), dict(b=NULL), dict(s=NULL), dict(off=NULL),
@@ -105,8 +105,8 @@ def test_fp8_products_reject(lib):
     assert plain(ps=F2) == INVALID
     gemv = dict(x=F, xs=F, rows=1, K=2880, b=F, s=F, E=32, N=5760, ids=F, k=4, out=F)
     head = "x xs rows K b s E N ids k".split()
-    plain = _caller(lib.gq_mxfp8_grouped_gemv_fp8, head + ["ps", "out"], dict(gemv, ps=NULL))
-    unit = _caller(lib.gq_mxfp8_grouped_gemv_fp8_swiglu, head + ["al", "li", "out"],
+    plain = _caller(lib.gq_mxfp4_grouped_gemv_fp8, head + ["ps", "out"], dict(gemv, ps=NULL))
+    unit = _caller(lib.gq_mxfp4_grouped_gemv_fp8_swiglu, head + ["al", "li", "out"],
                    dict(gemv, al=1.702, li=7.0))
     for call in (plain, unit):
         for bad in (dict(x=NULL), dict(xs=NULL), dict(b=NULL), dict(s=NULL), dict(ids=NULL),
@@ -119,10 +119,43 @@ def test_fp8_products_reject(lib):
     assert unit(al=nan) == INVALID and unit(li=-1.0) == INVALID
 
 
+def test_moe_route_rejects(lib):
+    call = _caller(lib.gq_moe_route, "z dt rows E zs b k sc G kG top renorm f ids w".split(),
+                   dict(z=F, dt=0, rows=4, E=256, zs=256, b=F, k=8, sc=1, G=8, kG=4, top=2,
+                        renorm=1, f=2.5, ids=F, w=F))
+    nan, inf = float("nan"), float("inf")
+    for bad in (dict(z=NULL), dict(ids=NULL), dict(w=NULL), dict(dt=7), dict(rows=-1), dict(E=0),
+                dict(k=0), dict(k=129), dict(zs=255), dict(z=F2), dict(z=F1, dt=1), dict(ids=F2),
+                dict(w=F2), dict(b=F2), dict(sc=2), dict(sc=-1), dict(G=0), dict(G=-8), dict(G=7),
+                dict(kG=0), dict(kG=9), dict(top=0), dict(top=3), dict(f=nan), dict(f=inf),
+                dict(f=-inf)):
+        assert call(**bad) == INVALID, bad
+    assert call(E=1032, zs=1032) == NOT_SUPPORTED
+    assert call(k=65) == NOT_SUPPORTED
+    assert call(G=128, kG=64) == NOT_SUPPORTED
+    assert call(rows=1 << 40) == NOT_SUPPORTED
+    assert call(rows=0, z=NULL, ids=NULL, w=NULL) == 0
+
+
+def test_moe_route_backward_rejects(lib):
+    call = _caller(lib.gq_moe_route_backward, "dw z dt rows E zs ids k sc renorm f dz".split(),
+                   dict(dw=F, z=F, dt=1, rows=4, E=32, zs=32, ids=F, k=4, sc=1, renorm=0, f=1.0,
+                        dz=F))
+    for bad in (dict(dw=NULL), dict(z=NULL), dict(ids=NULL), dict(dz=NULL), dict(dt=3),
+                dict(rows=-1), dict(E=0), dict(k=0), dict(zs=31), dict(dw=F2), dict(sc=2),
+                dict(sc=-1), dict(f=float("nan")), dict(f=float("inf")), dict(z=F1), dict(ids=F2),
+                dict(dz=F1), dict(dz=F2, dt=0, z=F)):
+        assert call(**bad) == INVALID, bad
+    assert call(E=2000, zs=2000) == NOT_SUPPORTED
+    assert call(k=65) == NOT_SUPPORTED
+    assert call(rows=0) == 0
+
+
 def test_binding_takes_device_tensors_only():
     x, w = torch.zeros(2, 64), torch.ones(64)
     for call in (lambda: gq.gq_mxfp8_quantize(x), lambda: gq.gq_rms_norm(x, w),
-                 lambda: gq.gq_rms_norm_backward(x, x, w)):
+                 lambda: gq.gq_rms_norm_backward(x, x, w), lambda: gq.gq_moe_route(x, 2),
+                 lambda: gq.gq_moe_route_backward(x, x, x)):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: gq.gq_mxfp8_quantize(None), lambda: gq.gq_rms_norm([1.0], w),
