@@ -880,6 +880,10 @@ def gq_mxfp8_quantize(x, values=None, codes=None, scales=None):
     or a bf16 tensor of x's shape (x itself, if bf16 and contiguous) also
     returns the values that the codes stand for."""
     lib = _lib or load_library()
+    if _calls and codes is scales is None and (values is None or values is True):
+        r = _calls.quantize8(x, values is True)
+        if r is not None:
+            return _done(r, "gq_mxfp8_quantize")
     code = _typed(x, "x")
     dev, index = x.device, x.get_device()
     rows, K, stride = _rows(x, "x")
@@ -934,6 +938,12 @@ def gq_rms_norm(x, weight, eps=1e-6, residual=None, y=True, sum=None, mxfp8=Fals
     ``sum`` (for h) may be tensors to write to, x or residual among them;
     ``mxfp8`` a pair of tensors and ``values`` a tensor likewise."""
     lib = _lib or load_library()
+    if (_calls and y is True and sum is None and (mxfp8 is False or mxfp8 is True)
+            and (values is False or values is True)):
+        r = _calls.rms_norm(x, weight, eps, residual, mxfp8, values)
+        if r is not None:
+            y, sum, codes, scales, values = _done(r, "gq_rms_norm")
+            return RmsNorm(y, sum, None if codes is None else (codes, scales), values)
     code = _typed(x, "x")
     dev, index = x.device, x.get_device()
     rows, H, stride = _rows(x, "x")
@@ -982,6 +992,10 @@ def gq_rms_norm_backward(d_y, h, weight, eps=1e-6, d_residual=None, d_x=None, d_
     tensors to write to (d_x: d_y, h or d_residual among them); ``workspace``: a
     uint8 tensor of at least gq_rms_norm_backward_workspace bytes."""
     lib = _lib or load_library()
+    if _calls and d_x is workspace is None and (d_weight is True or d_weight is False):
+        r = _calls.rms_norm_backward(d_y, h, weight, eps, d_residual, d_weight)
+        if r is not None:
+            return _done(r, "gq_rms_norm_backward")
     code = _typed(h, "h")
     dev, index = h.device, h.get_device()
     rows, H, stride = _rows(h, "h")
@@ -1030,9 +1044,9 @@ def _mx_pair(x, bits, blocks, scales, unit):
 
 def _mx_gemm(what, bits, x, blocks, scales, route, unit, pair_scale, out):
     lib = _lib or load_library()
-    if _calls and out is None and bits == 4:
-        r = _calls.fp4_gemm(x[0], x[1], blocks, scales, route, pair_scale, unit is not None,
-                            *(unit or (0.0, 0.0)))
+    if _calls and out is None:
+        r = (_calls.fp4_gemm if bits == 4 else _calls.fp8_gemm)(
+            x[0], x[1], blocks, scales, route, pair_scale, unit is not None, *(unit or (0.0, 0.0)))
         if r is not None:
             return _done(r, what)
     xb, xs, rows, E, N, K = _mx_pair(x, bits, blocks, scales, unit is not None)
@@ -1070,9 +1084,10 @@ def gq_mxfp4_grouped_gemm_fp4_swiglu(x, blocks, scales, route, alpha=OSS_ALPHA, 
 
 def _mx_gemv(what, bits, x, blocks, scales, topk_ids, unit, pair_scale, out):
     lib = _lib or load_library()
-    if _calls and out is None and bits == 4:
-        r = _calls.fp4_gemv(x[0], x[1], blocks, scales, topk_ids, pair_scale, unit is not None,
-                            *(unit or (0.0, 0.0)))
+    if _calls and out is None:
+        r = (_calls.fp4_gemv if bits == 4 else _calls.fp8_gemv)(
+            x[0], x[1], blocks, scales, topk_ids, pair_scale, unit is not None,
+            *(unit or (0.0, 0.0)))
         if r is not None:
             return _done(r, what)
     xb, xs, rows, E, N, K = _mx_pair(x, bits, blocks, scales, unit is not None)
@@ -1219,6 +1234,12 @@ def gq_moe_route(logits, topk, score="softmax", bias=None, groups=1, topk_groups
     sum with ``renormalize``.  Ties go to the lower index; a logit of -inf is never
     chosen; a slot left without an expert has id -1 and weight 0."""
     lib = _lib or load_library()
+    if _calls and topk_ids is topk_weights is None:
+        r = _calls.moe_route(logits, topk, _score(score), bias, groups,
+                             groups if topk_groups is None else topk_groups, group_top,
+                             bool(renormalize), scale)
+        if r is not None:
+            return _done(r, "gq_moe_route")
     code = _typed(logits, "logits")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")
@@ -1248,6 +1269,11 @@ def gq_moe_route_backward(d_weights, logits, topk_ids, score="softmax", renormal
     """Gradient of ``gq_moe_route``'s weights to its logits, the selection held
     fixed: d_weights float32 [rows, topk] -> [rows, E] of the logits' type."""
     lib = _lib or load_library()
+    if _calls and out is None:
+        r = _calls.moe_route_backward(d_weights, logits, topk_ids, _score(score),
+                                      bool(renormalize), scale)
+        if r is not None:
+            return _done(r, "gq_moe_route_backward")
     code = _typed(logits, "logits")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [rows, E] (got shape {tuple(logits.shape)})")

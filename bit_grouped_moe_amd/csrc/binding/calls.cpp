@@ -30,6 +30,16 @@ struct Library {
   decltype(&gq_mxfp4_grouped_gemm_fp4_swiglu) gemm_unit;
   decltype(&gq_route_sort) route_sort;
   decltype(&gq_route_max_tiles) max_tiles;
+  decltype(&gq_mxfp8_quantize) quantize8;
+  decltype(&gq_mxfp4_grouped_gemv_fp8) gemv8;
+  decltype(&gq_mxfp4_grouped_gemv_fp8_swiglu) gemv8_unit;
+  decltype(&gq_mxfp4_grouped_gemm_fp8) gemm8;
+  decltype(&gq_mxfp4_grouped_gemm_fp8_swiglu) gemm8_unit;
+  decltype(&gq_rms_norm) norm;
+  decltype(&gq_rms_norm_backward) norm_backward;
+  decltype(&gq_rms_norm_backward_workspace) norm_workspace;
+  decltype(&gq_moe_route) route;
+  decltype(&gq_moe_route_backward) route_backward;
 } lib{};
 PyObject* current_device = nullptr;          // torch's callables
 PyObject* raw_stream = nullptr;
@@ -144,35 +154,147 @@ Tensor output(const Tensor& like, at::ScalarType type, at::IntArrayRef sizes) {
     if (!ok) Py_RETURN_NONE;                                      \
   }
 
-// quantize(x, want_values) -> (blocks, scales[, values])
-PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// rows, width and row stride of a tensor [..., width] without a gap between its
+// leading dimensions, or of two dimensions at any stride; false: neither
+bool value_rows(const Tensor& x, int64_t& rows, int64_t& K, int64_t& stride) {
+  if (x.dim() < 1 || x.numel() == 0) return false;
+  K = x.size(-1);
+  rows = x.numel() / K;
+  stride = K;
+  if (!x.is_contiguous()) {
+    if (x.dim() != 2 || x.stride(1) != 1) return false;
+    if (rows > 1) stride = x.stride(0);
+  }
+  return K <= INT32_MAX;
+}
+
+// quantize(x, want_values) -> (blocks, scales[, values]); quantize8: codes for blocks
+template <bool k8>
+PyObject* quantize_call(PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   GQ_ARGS(2)
   const Tensor* x = device_tensor(a[0]);
   const int code = x ? float_code(*x) : -1;
-  if (code < 0 || x->dim() < 1) Py_RETURN_NONE;
-  const int64_t K = x->size(-1);
-  if (K <= 0 || K % 32 || K > INT32_MAX || x->numel() == 0) Py_RETURN_NONE;
-  const int64_t rows = x->numel() / K;
-  int64_t stride = K;
-  if (!x->is_contiguous()) {
-    if (x->dim() != 2 || x->stride(1) != 1) Py_RETURN_NONE;
-    if (rows > 1) stride = x->stride(0);
-  }
+  int64_t rows, K, stride;
+  if (code < 0 || !value_rows(*x, rows, K, stride) || K % 32) Py_RETURN_NONE;
   GQ_STREAM(*x)
   const bool want = a[1] == Py_True;
   auto shape = x->sizes().vec();
   shape.back() = K / 32;
   Tensor scales = output(*x, at::kByte, shape);
   shape.push_back(16);
-  Tensor blocks = output(*x, at::kByte, shape);
+  Tensor codes = output(*x, at::kByte, k8 ? x->sizes() : at::IntArrayRef(shape));
   Tensor values;
   if (want) values = output(*x, at::kBFloat16, x->sizes());
-  const int st = launch(lib.quantize, x->data_ptr(), code, rows, (int32_t)K, stride,
-                        data<uint8_t>(blocks), data<uint8_t>(scales),
+  const int st = launch(k8 ? lib.quantize8 : lib.quantize, x->data_ptr(), code, rows, (int32_t)K,
+                        stride, data<uint8_t>(codes), data<uint8_t>(scales),
                         want ? data<uint16_t>(values) : nullptr, stream);
   if (st) return PyLong_FromLong(st);
-  return want ? pack({blocks, scales, values}) : pack({blocks, scales});
+  return want ? pack({codes, scales, values}) : pack({codes, scales});
+  END_HANDLE_TH_ERRORS
+}
+PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return quantize_call<false>(a, n);
+}
+PyObject* quantize8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return quantize_call<true>(a, n);
+}
+
+// A norm's gain [H], of the rows' type or float32: its type code, -1 where it is none.
+int gain(PyObject* o, const Tensor& x, int64_t H) {
+  const Tensor* w = device_tensor(o);
+  if (!w || w->dim() != 1 || w->size(0) != H || !w->is_contiguous() || !(
+          w->scalar_type() == x.scalar_type() || w->scalar_type() == at::kFloat) ||
+      w->get_device() != x.get_device())
+    return -1;
+  return float_code(*w);
+}
+// An optional tensor of x's shape, type and device: false where it is not one.
+bool same_rows(PyObject* o, const Tensor& x, const Tensor*& t, int64_t& stride) {
+  t = nullptr;
+  stride = 0;
+  if (o == Py_None) return true;
+  t = device_tensor(o);
+  int64_t rows, K;
+  return t && t->scalar_type() == x.scalar_type() && t->sizes() == x.sizes() &&
+         t->get_device() == x.get_device() && value_rows(*t, rows, K, stride);
+}
+// A number as a double; false (and no error) where it is none.
+bool number(PyObject* o, double& v) {
+  v = PyFloat_AsDouble(o);
+  if (!PyErr_Occurred()) return true;
+  PyErr_Clear();
+  return false;
+}
+
+// rms_norm(x, weight, eps, residual, want_mxfp8, want_values)
+//   -> (y, sum or None, codes or None, scales or None, values or None)
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GQ_ARGS(6)
+  const Tensor* x = device_tensor(a[0]);
+  const int code = x ? float_code(*x) : -1;
+  int64_t rows, H, stride, rstride;
+  const Tensor* res;
+  double eps;
+  if (code < 0 || !value_rows(*x, rows, H, stride)) Py_RETURN_NONE;
+  const int wcode = gain(a[1], *x, H);
+  const bool eight = a[4] == Py_True, want = a[5] == Py_True;
+  if (wcode < 0 || !number(a[2], eps) || !same_rows(a[3], *x, res, rstride) || (eight && H % 32) ||
+      (want && !eight))
+    Py_RETURN_NONE;
+  GQ_STREAM(*x)
+  Tensor y = output(*x, x->scalar_type(), x->sizes()), sum, codes, scales, values;
+  if (res) sum = output(*x, x->scalar_type(), x->sizes());
+  if (eight) {
+    auto shape = x->sizes().vec();
+    shape.back() = H / 32;
+    codes = output(*x, at::kByte, x->sizes());
+    scales = output(*x, at::kByte, shape);
+    if (want) values = output(*x, at::kBFloat16, x->sizes());
+  }
+  const int st = launch(lib.norm, x->data_ptr(), stride, res ? res->data_ptr() : nullptr, rstride,
+                        code, rows, (int32_t)H, THPVariable_Unpack(a[1]).data_ptr(), wcode,
+                        (float)eps, res ? sum.data_ptr() : nullptr, y.data_ptr(),
+                        eight ? data<uint8_t>(codes) : nullptr,
+                        eight ? data<uint8_t>(scales) : nullptr,
+                        want ? data<uint16_t>(values) : nullptr, stream);
+  if (st) return PyLong_FromLong(st);
+  return pack({y, sum, codes, scales, values});
+  END_HANDLE_TH_ERRORS
+}
+
+// rms_norm_backward(d_y, h, weight, eps, d_residual, want_d_weight) -> (d_x, d_weight or None)
+PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GQ_ARGS(6)
+  const Tensor* h = device_tensor(a[1]);
+  const int code = h ? float_code(*h) : -1;
+  int64_t rows, H, stride, dstride, rstride;
+  const Tensor *dy, *res;
+  double eps;
+  if (code < 0 || !value_rows(*h, rows, H, stride)) Py_RETURN_NONE;
+  const int wcode = gain(a[2], *h, H);
+  if (wcode < 0 || !number(a[3], eps) || !same_rows(a[0], *h, dy, dstride) || !dy ||
+      !same_rows(a[4], *h, res, rstride))
+    Py_RETURN_NONE;
+  const int64_t need = lib.norm_workspace(rows, (int32_t)H);
+  if (need < 0) Py_RETURN_NONE;
+  GQ_STREAM(*h)
+  const Tensor& w = THPVariable_Unpack(a[2]);
+  const bool want = a[5] == Py_True;
+  Tensor dx = output(*h, h->scalar_type(), h->sizes()), dw, space;
+  if (want) {
+    dw = output(*h, w.scalar_type(), w.sizes());
+    space = output(*h, at::kByte, {need});
+  }
+  const int st = launch(lib.norm_backward, dy->data_ptr(), dstride, h->data_ptr(), stride,
+                        res ? res->data_ptr() : nullptr, rstride, code, rows, (int32_t)H,
+                        w.data_ptr(), wcode, (float)eps, dx.data_ptr(),
+                        want ? dw.data_ptr() : nullptr, want ? space.data_ptr() : nullptr, need,
+                        stream);
+  if (st) return PyLong_FromLong(st);
+  return pack({dx, dw});
   END_HANDLE_TH_ERRORS
 }
 
@@ -232,6 +354,72 @@ PyObject* moe_topk_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// moe_route(logits, topk, score, bias, groups, topk_groups, group_top, renormalize, scale)
+//   -> (ids, weights)
+PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GQ_ARGS(9)
+  const Tensor* z = device_tensor(a[0]);
+  const int code = z ? float_code(*z) : -1;
+  int64_t rows, E, stride, v[5];
+  double scale;
+  if (code < 0 || !logit_rows(*z, rows, E, stride) || !number(a[8], scale)) Py_RETURN_NONE;
+  const int at[5] = {1, 2, 4, 5, 6};                   // topk, score, groups, topk_groups, group_top
+  for (int i = 0; i < 5; ++i) {
+    if (!PyLong_Check(a[at[i]])) Py_RETURN_NONE;
+    v[i] = whole(a[at[i]]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    if (v[i] < 0 || v[i] > INT32_MAX) Py_RETURN_NONE;
+  }
+  if (v[0] < 1 || v[0] > E || v[2] < 1 || E % v[2]) Py_RETURN_NONE;
+  const Tensor* bias = nullptr;
+  if (a[3] != Py_None) {
+    bias = contiguous(a[3], at::kFloat, 1);
+    if (!bias || bias->size(0) != E || !together(*z, *bias)) Py_RETURN_NONE;
+  }
+  GQ_STREAM(*z)
+  const int renorm = PyObject_IsTrue(a[7]);
+  Tensor ids = output(*z, at::kInt, {rows, v[0]});
+  Tensor w = output(*z, at::kFloat, {rows, v[0]});
+  const int st = launch(lib.route, z->data_ptr(), code, rows, (int32_t)E, stride,
+                        bias ? data<float>(*bias) : nullptr, (int32_t)v[0], (int32_t)v[1],
+                        (int32_t)v[2], (int32_t)v[3], (int32_t)v[4], renorm, (float)scale,
+                        data<int32_t>(ids), data<float>(w), stream);
+  if (st) return PyLong_FromLong(st);
+  return pack({ids, w});
+  END_HANDLE_TH_ERRORS
+}
+
+// moe_route_backward(d_weights, logits, ids, score, renormalize, scale) -> d_logits
+PyObject* moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GQ_ARGS(6)
+  const Tensor* dw = contiguous(a[0], at::kFloat, 2);
+  const Tensor* z = device_tensor(a[1]);
+  const Tensor* ids = contiguous(a[2], at::kInt, 2);
+  const int code = z ? float_code(*z) : -1;
+  int64_t rows, E, stride;
+  double scale;
+  if (code < 0 || !dw || !ids || !logit_rows(*z, rows, E, stride) || ids->size(0) != rows ||
+      dw->sizes() != ids->sizes() || ids->size(1) > INT32_MAX || !together(*z, *dw, *ids) ||
+      !PyLong_Check(a[3]) || !number(a[5], scale))
+    Py_RETURN_NONE;
+  const int64_t score = whole(a[3]);
+  if (PyErr_Occurred()) return nullptr;
+  GQ_STREAM(*z)
+  const int renorm = PyObject_IsTrue(a[4]);
+  Tensor dz = output(*z, z->scalar_type(), {rows, E});
+  const int st = launch(lib.route_backward, data<float>(*dw), z->data_ptr(), code, rows,
+                        (int32_t)E, stride, data<int32_t>(*ids), (int32_t)ids->size(1),
+                        (int32_t)score, renorm, (float)scale, dz.data_ptr(), stream);
+  if (st) return PyLong_FromLong(st);
+  return wrap(dz);
+  END_HANDLE_TH_ERRORS
+}
+
 // moe_decode(layer struct address, device, workspace bytes, x) -> y
 PyObject* moe_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -256,13 +444,14 @@ PyObject* moe_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The operands of an MXFP4 x MXFP4 product.
+// The operands of a product of MXFP4 or (k8) MXFP8 activations with MXFP4 weights.
 struct Pair {
   const Tensor *xb, *xs, *blocks, *scales;
   int64_t rows, E, N, K;
 };
+template <bool k8>
 bool mx_pair(PyObject* const* a, Pair& p) {
-  p.xb = contiguous(a[0], at::kByte, 3);
+  p.xb = contiguous(a[0], at::kByte, k8 ? 2 : 3);
   p.xs = contiguous(a[1], at::kByte, 2);
   p.blocks = contiguous(a[2], at::kByte, 4);
   p.scales = contiguous(a[3], at::kByte, 3);
@@ -273,7 +462,8 @@ bool mx_pair(PyObject* const* a, Pair& p) {
   p.N = p.blocks->size(1);
   p.K = nb * 32;
   return p.blocks->size(3) == 16 && p.scales->size(0) == p.E && p.scales->size(1) == p.N &&
-         p.scales->size(2) == nb && p.xb->size(1) == nb && p.xb->size(2) == 16 &&
+         p.scales->size(2) == nb &&
+         (k8 ? p.xb->size(1) == p.K : p.xb->size(1) == nb && p.xb->size(2) == 16) &&
          p.xs->size(0) == p.rows && p.xs->size(1) == nb && p.rows >= 1 && p.rows <= INT32_MAX &&
          p.E <= INT32_MAX && p.N <= INT32_MAX && p.K <= INT32_MAX &&
          together(*p.xb, *p.xs, *p.blocks, *p.scales);
@@ -291,13 +481,14 @@ bool pair_weights(PyObject* o, int64_t P, const Tensor& beside, const float*& w)
 }
 
 // fp4_gemv(x blocks, x scales, blocks, scales, ids, pair_scale, unit, alpha, limit)
-PyObject* fp4_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <bool k8>
+PyObject* gemv_call(PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   GQ_ARGS(9)
   Pair p;
   const Tensor* ids = contiguous(a[4], at::kInt, 2);
   const bool unit = a[6] == Py_True;
-  if (!mx_pair(a, p) || !ids || ids->size(0) != p.rows || ids->size(1) < 1 ||
+  if (!mx_pair<k8>(a, p) || !ids || ids->size(0) != p.rows || ids->size(1) < 1 ||
       !together(*p.xb, *ids) || (unit && p.N % 2))
     Py_RETURN_NONE;
   const int64_t P = p.rows * ids->size(1);
@@ -312,22 +503,26 @@ PyObject* fp4_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* id = data<int32_t>(*ids);
   const int32_t k = (int32_t)ids->size(1);
   uint16_t* o = data<uint16_t>(out);
-  const int st = unit ? launch(lib.gemv_unit, xb, xs, p.rows, p.K, b, s, p.E, p.N, id, k,
+  const int st = unit ? launch(k8 ? lib.gemv8_unit : lib.gemv_unit, xb, xs, p.rows, p.K, b, s, p.E, p.N, id, k,
                                (float)alpha, (float)limit, o, stream)
-                      : launch(lib.gemv, xb, xs, p.rows, p.K, b, s, p.E, p.N, id, k, ps, o, stream);
+                      : launch(k8 ? lib.gemv8 : lib.gemv, xb, xs, p.rows, p.K, b, s, p.E, p.N, id, k, ps,
+                               o, stream);
   if (st) return PyLong_FromLong(st);
   return wrap(out);
   END_HANDLE_TH_ERRORS
 }
+PyObject* fp4_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) { return gemv_call<false>(a, n); }
+PyObject* fp8_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) { return gemv_call<true>(a, n); }
 
 // fp4_gemm(x blocks, x scales, blocks, scales, route, pair_scale, unit, alpha, limit)
-PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <bool k8>
+PyObject* gemm_call(PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   GQ_ARGS(9)
   Pair p;
   const bool unit = a[6] == Py_True;
   // expert_offsets, sorted_pairs, tiles, num_tiles, max_tiles, tile_m, rows, topk, num_experts
-  if (!mx_pair(a, p) || !PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 9 || (unit && p.N % 2))
+  if (!mx_pair<k8>(a, p) || !PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 9 || (unit && p.N % 2))
     Py_RETURN_NONE;
   const Tensor* r[4];
   int64_t v[5];
@@ -354,14 +549,16 @@ PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto *off = data<int32_t>(*r[0]), *sp = data<int32_t>(*r[1]), *tl = data<int32_t>(*r[2]),
              *nt = data<int32_t>(*r[3]);
   uint16_t* o = data<uint16_t>(out);
-  const int st = unit ? launch(lib.gemm_unit, xb, xs, p.rows, p.K, b, s, p.E, p.N, k, (float)alpha,
+  const int st = unit ? launch(k8 ? lib.gemm8_unit : lib.gemm_unit, xb, xs, p.rows, p.K, b, s, p.E, p.N, k, (float)alpha,
                                (float)limit, off, sp, tl, nt, v[0], v[1], o, stream)
-                      : launch(lib.gemm, xb, xs, p.rows, p.K, b, s, p.E, p.N, k, ps, off, sp, tl,
-                               nt, v[0], v[1], o, stream);
+                      : launch(k8 ? lib.gemm8 : lib.gemm, xb, xs, p.rows, p.K, b, s, p.E, p.N, k, ps, off,
+                               sp, tl, nt, v[0], v[1], o, stream);
   if (st) return PyLong_FromLong(st);
   return wrap(out);
   END_HANDLE_TH_ERRORS
 }
+PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) { return gemm_call<false>(a, n); }
+PyObject* fp8_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) { return gemm_call<true>(a, n); }
 
 // route_sort(ids, num_experts, tile_m) -> (offsets, sorted, tiles, num_tiles)
 PyObject* route_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -417,6 +614,16 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   GQ_BIND(gemm_unit, gq_mxfp4_grouped_gemm_fp4_swiglu)
   GQ_BIND(route_sort, gq_route_sort)
   GQ_BIND(max_tiles, gq_route_max_tiles)
+  GQ_BIND(quantize8, gq_mxfp8_quantize)
+  GQ_BIND(gemv8, gq_mxfp4_grouped_gemv_fp8)
+  GQ_BIND(gemv8_unit, gq_mxfp4_grouped_gemv_fp8_swiglu)
+  GQ_BIND(gemm8, gq_mxfp4_grouped_gemm_fp8)
+  GQ_BIND(gemm8_unit, gq_mxfp4_grouped_gemm_fp8_swiglu)
+  GQ_BIND(norm, gq_rms_norm)
+  GQ_BIND(norm_backward, gq_rms_norm_backward)
+  GQ_BIND(norm_workspace, gq_rms_norm_backward_workspace)
+  GQ_BIND(route, gq_moe_route)
+  GQ_BIND(route_backward, gq_moe_route_backward)
   lib = l;
   Py_XINCREF(a[1]);
   Py_XINCREF(a[2]);
@@ -433,6 +640,10 @@ PyMethodDef methods[] = {GQ_METHOD(bind),       GQ_METHOD(quantize),
                          GQ_METHOD(moe_topk),   GQ_METHOD(moe_topk_backward),
                          GQ_METHOD(moe_decode), GQ_METHOD(fp4_gemv),
                          GQ_METHOD(fp4_gemm),   GQ_METHOD(route_sort),
+                         GQ_METHOD(quantize8),  GQ_METHOD(rms_norm),
+                         GQ_METHOD(fp8_gemv),   GQ_METHOD(rms_norm_backward),
+                         GQ_METHOD(fp8_gemm),   GQ_METHOD(moe_route),
+                         GQ_METHOD(moe_route_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
