@@ -8,8 +8,9 @@
 //
 // Ties go to the lower index; an expert whose logit or choice is -inf is masked.
 // Which of two experts is larger is decided in 64 bits: the selection of a row
-// then does not depend on the last bits of a float32 exponential.  Weights are
-// float32, from the chosen logits.
+// then does not depend on the last bits of a float32 exponential.  That takes
+// 64-bit arithmetic only where 32 bits leave a doubt (below).  Weights are float32,
+// from the chosen logits.
 //
 // One wave a row, at most 16 experts a lane, expert 64 c + l in lane l.
 #include "router.hpp"
@@ -22,6 +23,7 @@ struct RouteArgs {
   const float* bias;             // [E] or null
   int E, topk, sigmoid, groups, topk_groups, group_top, renorm;
   uint32_t size_magic;           // expert / (E / groups) = expert * size_magic >> 20
+  int share;                     // log2 of the lanes that look through a group
   float scale;
   int32_t* ids;
   float* weights;
@@ -135,6 +137,53 @@ __device__ __forceinline__ void select64(const RouteArgs& g, const float (&z)[C]
   logit = __uint_as_float(won);
 }
 
+// ---- in 32 bits, where that decides -------------------------------------------
+// Scores in float32 from the hardware exponential and reciprocal.  A sigmoid is off
+// by less than 2^-22 (s (1 - s) |z| < 1/4 times the argument's rounding, and an ulp
+// each of the exponential, the sum and the reciprocal), a softmax by less than
+// 2^-19 (up to 22 additions of its sum), the sum with the bias by 2^-24 of itself.
+// Two choices further apart than both errors are in the order of float64; so are
+// choices of equal logits and biases, by index.  A row that this does not decide is
+// selected again in 64 bits: 2% of rows with random float32 logits and biases.
+__device__ __forceinline__ float fast_exp(float d) {
+  return __builtin_amdgcn_exp2f(d * 1.44269504088896341f);
+}
+__device__ __forceinline__ float fast_sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + fast_exp(-z));
+}
+// Whether a choice a (at least) lies clearly above a choice b (at most); false with
+// a NaN.  `twice`: they are sums of two.
+__device__ __forceinline__ bool clearly(float a, float b, bool sigmoid, bool twice) {
+  const float room = (sigmoid ? 0x1p-20f : 0x1p-18f) + 0x1p-22f * (fabsf(a) + fabsf(b));
+  return a - b > (twice ? 2.f * room : room);
+}
+
+// The two largest of this lane's two and another lane's.
+template <int kCtrl>
+__device__ __forceinline__ void two_largest(uint32_t& first, uint32_t& second) {
+  const uint32_t f = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)first, kCtrl, 0xF, 0xF, false);
+  const uint32_t s = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)second, kCtrl, 0xF, 0xF, false);
+  second = max(min(first, f), max(second, s));
+  first = max(first, f);
+}
+
+// A slot's weight before the division by their sum, from the logit zs of its expert
+// id (-1: none), and the peak that the sum is taken over.
+struct RowWeights {
+  float peak, part;
+  // slots, all: the largest key of the slots' logits and (softmax) of the row's
+  __device__ __forceinline__ RowWeights(const RouteArgs& g, int id, float zs, uint32_t slots,
+                                        uint32_t all) {
+    const bool broken = !g.sigmoid && all >= 0xFF800000u;  // a softmax with a NaN or +inf
+    const uint32_t m = !g.sigmoid && !g.renorm ? all : slots;
+    peak = broken ? __uint_as_float(0x7FC00000u) : m > kDeadKey ? key_logit(m) : 0.f;
+    part = id < 0      ? 0.f
+           : g.sigmoid ? sigmoid_over(zs, g.renorm && peak <= 0.f ? peak : 0.f)
+                       : expf(zs - peak);
+  }
+};
+
+// One wave a row.  LDS: the larger of 64-bit and 32-bit keys of the row.
 template <int kType, int C>
 __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
     const void* __restrict__ logits, int64_t rows, int64_t stride, RouteArgs g) {
@@ -144,41 +193,311 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
   const int64_t row = (int64_t)blockIdx.x * kWaveRows + wave;
   if (row >= rows) return;
   const float kInf = __builtin_inff();
-  float z[C];
+  float z[C], b[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) z[c] = load1<kType>(logits, row * stride + min(64 * c + lane, g.E - 1));
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    if (64 * c + lane >= g.E) z[c] = -kInf;
-  int id;
-  float zs;
-  select64<C>(g, z, lane, keys[wave], id, zs);
-  // weights: over the largest logit of the slots, or of the row
-  uint32_t best = id >= 0 ? logit_key(zs) : 0u;
-  bool broken = false;                                   // a softmax with a NaN or +inf
-  if (!g.sigmoid) {
-    uint32_t all = 0u;
+  for (int c = 0; c < C; ++c) b[c] = g.bias ? g.bias[min(64 * c + lane, g.E - 1)] : 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) all = max(all, logit_key(z[c]));
-    broken = wave_umax(all) >= 0xFF800000u;              // the key of +inf
-    if (!g.renorm) best = all;
+  for (int c = 0; c < C; ++c) asm volatile("" : "+v"(z[c]), "+v"(b[c]));
+  uint32_t all = 0u;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (64 * c + lane >= g.E) z[c] = -kInf;
+    all = max(all, logit_key(z[c]));
   }
-  const uint32_t m = wave_umax(best);
-  const float peak = broken ? __uint_as_float(0x7FC00000u) : m > kDeadKey ? key_logit(m) : 0.f;
-  const float part = id < 0 ? 0.f
-                     : g.sigmoid ? sigmoid_over(zs, g.renorm && peak <= 0.f ? peak : 0.f)
-                                 : expf(zs - peak);
-  float total = part;
+  if (!g.sigmoid) all = wave_umax(all);
+
+  const bool sums = g.groups > 1 && g.group_top > 1;
+  float score[C];
+  if (g.bias || sums) {
+    if (g.sigmoid) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) score[c] = fast_sigmoid(z[c]);
+    } else {
+      const float peak = all > kDeadKey ? key_logit(all) : 0.f;
+      float total = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        score[c] = fast_exp(z[c] - peak);
+        total += score[c];
+      }
+      total = __builtin_amdgcn_rcpf(wave_fsum(total));
+#pragma unroll
+      for (int c = 0; c < C; ++c) score[c] *= total;
+    }
+  }
+  uint32_t key[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    key[c] = z[c] == -kInf ? kDeadKey : logit_key(g.bias ? score[c] + b[c] : z[c]);
+    if (64 * c + lane >= g.E) key[c] = 0u;
+  }
+  bool sure = true;                                      // uniform
+  if (g.groups > 1) {
+    uint32_t* k32 = reinterpret_cast<uint32_t*>(keys[wave]);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      k32[64 * c + lane] = sums && !g.bias && key[c] > kDeadKey ? logit_key(score[c]) : key[c];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    // 2^share lanes a group (at most 16), each every 2^share-th of its experts
+    uint32_t first = 0u, second = 0u;
+    const int group = lane >> g.share;
+    if (group < g.groups) {
+      const int size = g.E / g.groups;
+      for (int i = lane & ((1 << g.share) - 1); i < size; i += 1 << g.share) {
+        const uint32_t k = k32[group * size + i];
+        second = max(second, min(first, k));
+        first = max(first, k);
+      }
+    }
+    if (g.share > 0) two_largest<0xB1>(first, second);
+    if (g.share > 1) two_largest<0x4E>(first, second);
+    if (g.share > 2) two_largest<0x141>(first, second);
+    if (g.share > 3) two_largest<0x140>(first, second);
+    float v = first > kDeadKey ? key_logit(first) : -kInf;
+    if (sums && second > kDeadKey) v += key_logit(second);
+    const uint32_t mine = first > kDeadKey ? logit_key(v) : 0u;
+    int before = 0;                                      // groups ahead of this one
+    for (int j = 0; j < g.groups; ++j) {
+      const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)mine, j << g.share);
+      before += k > mine || (k == mine && j < group);
+    }
+    const bool in = group < g.groups && before < g.topk_groups;
+    const uint64_t open = __ballot(in);
+    if (g.bias || sums) {
+      // the least open and the largest closed group
+      const uint32_t least = ~wave_umax(in ? ~mine : 0u);
+      const uint32_t most = wave_umax(group < g.groups && !in ? mine : 0u);
+      sure = most <= kDeadKey || clearly(key_logit(least), key_logit(most), g.sigmoid, sums);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = 64 * c + lane;
+      const uint32_t bit = (((uint32_t)e * g.size_magic) >> 20) << g.share & 63u;
+      if (!((open >> bit) & 1ull)) key[c] = 0u;
+    }
+  }
+  int id = -1;
+  float zs = -kInf, won = -kInf;
+  if (sure) {
+    wave_topk<C>(key, g.topk, id, won);
+    zs = id >= 0 ? load1<kType>(logits, row * stride + id) : -kInf;
+    if (g.bias) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int c = 1; c < C; ++c) best = max(best, key[c]);
+      best = wave_umax(best);                            // the largest that was not chosen
+      float next = __shfl_down(won, 1, kWave);
+      int next_id = __shfl_down(id, 1, kWave);
+      if (lane == g.topk - 1) {
+        next = best > kDeadKey ? key_logit(best) : -kInf;
+        next_id = -1;
+      }
+      const bool slot = lane < g.topk && id >= 0 && next != -kInf;
+      bool close = slot && !clearly(won, next, g.sigmoid, false);
+      if (__ballot(close)) {
+        // slots of equal logits and biases are in the order of their indices
+        const float zn = __shfl_down(zs, 1, kWave);
+        const float bs = id >= 0 ? g.bias[id] : 0.f, bn = next_id >= 0 ? g.bias[next_id] : 0.f;
+        close = close && !(next_id >= 0 && zs == zn && bs == bn);
+        sure = !__ballot(close);
+      }
+    }
+  }
+  if (!sure) select64<C>(g, z, lane, keys[wave], id, zs);
+  const uint32_t slots = wave_umax(id >= 0 ? logit_key(zs) : 0u);
+  const RowWeights w(g, id, zs, slots, all);
+  float total = w.part;
   if (!g.sigmoid && !g.renorm) {
     total = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) total += z[c] == -kInf ? 0.f : expf(z[c] - peak);
+    for (int c = 0; c < C; ++c) total += z[c] == -kInf ? 0.f : expf(z[c] - w.peak);
   }
   total = g.sigmoid && !g.renorm ? 1.f : wave_fsum(total);
   if (lane < g.topk) {
     g.ids[row * g.topk + lane] = id;
-    g.weights[row * g.topk + lane] = id >= 0 ? part / total * g.scale : 0.f;
+    g.weights[row * g.topk + lane] = id >= 0 ? w.part / total * g.scale : 0.f;
   }
+}
+
+// ---- many rows of up to 256 experts and 16 slots: sixteen lanes a row ----------
+// Lane l of a row holds experts C l .. C l + C - 1.  A group is 2^j whole lanes (the
+// host checks): its best are found in the lane and merged with DPP moves, its rank
+// by rotating the groups' values past each other.  Experts are selected as in the
+// softmax top-k's kernel, from sorted lists of keys that no two experts share: the
+// choice's key without its last 8 bits, and the expert.  What the 8 bits may have
+// hidden is one more case for the selection in 64 bits, by the whole wave, one row
+// after the other.  (16-bit logits' own order needs no more than the other 24.)
+constexpr int kRouteGroupFrom = 4096;                    // rows
+
+template <int kType, int C>
+__global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
+    const void* __restrict__ logits, int64_t rows, int64_t stride, int wide, int lanes,
+    RouteArgs g) {
+  using Row = GroupRow<kType, C>;
+  constexpr int kC64 = C * kGroup / kWave;
+  constexpr uint32_t kLive = (kDeadKey + 1) & ~255u;     // keys of live experts are not below
+  __shared__ uint64_t keys[kWaveRows][kC64 * kWave];
+  const int lane = threadIdx.x & (kWave - 1), l = lane & (kGroup - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t base = (int64_t)blockIdx.x * kGroupRows + wave * (kWave / kGroup);
+  const int64_t own = base + lane / kGroup;
+  const int64_t row = own < rows ? own : rows - 1;       // every lane takes part in the maxima
+  const typename Row::raw* zrow = static_cast<const typename Row::raw*>(logits) + row * stride;
+  const float kInf = __builtin_inff();
+  Row x;
+  x.load(zrow, l, g.E, wide);
+  float z[C], b[C];
+  if (g.bias && C * l + C <= g.E) {
+    typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int c = 0; c < C; c += 4) {
+      const vec v = *reinterpret_cast<const vec*>(g.bias + C * l + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[c + i] = __uint_as_float(v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) b[c] = g.bias ? g.bias[min(C * l + c, g.E - 1)] : 0.f;
+  }
+  uint32_t all = 0u;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    z[c] = C * l + c < g.E ? Row::value(x.r[c]) : -kInf;
+    if (!g.sigmoid) all = max(all, logit_key(z[c]));
+  }
+  if (!g.sigmoid) all = group_max(all);
+  const bool sums = g.groups > 1 && g.group_top > 1;
+  float score[C];
+  if (g.bias || sums) {
+    if (g.sigmoid) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) score[c] = fast_sigmoid(z[c]);
+    } else {
+      const float peak = all > kDeadKey ? key_logit(all) : 0.f;
+      float total = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        score[c] = fast_exp(z[c] - peak);
+        total += score[c];
+      }
+      total = __builtin_amdgcn_rcpf(group_sum_last(total, kGroup));
+#pragma unroll
+      for (int c = 0; c < C; ++c) score[c] *= total;
+    }
+  }
+  uint32_t key[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    key[c] = z[c] == -kInf ? 0u : logit_key(g.bias ? score[c] + b[c] : z[c]);
+  bool doubt = false;
+  if (g.groups > 1) {
+    uint32_t first = 0u, second = 0u;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t k = sums && !g.bias && key[c] > kDeadKey ? logit_key(score[c]) : key[c];
+      second = max(second, min(first, k));
+      first = max(first, k);
+    }
+    if (lanes > 1) two_largest<0xB1>(first, second);
+    if (lanes > 2) two_largest<0x4E>(first, second);
+    if (lanes > 4) two_largest<0x141>(first, second);
+    float v = first > kDeadKey ? key_logit(first) : -kInf;
+    if (sums && second > kDeadKey) v += key_logit(second);
+    const uint32_t mine = first > kDeadKey ? logit_key(v) : 0u;
+    int before = 0;                                      // groups ahead of this one
+    auto turn = [&](auto by) {
+      constexpr int kBy = decltype(by)::value + 1;
+      if (kBy & (lanes - 1)) return;                     // uniform
+      const uint32_t k =
+          (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0x120 + kBy, 0xF, 0xF, false);
+      const int from = __builtin_amdgcn_update_dpp(0, l, 0x120 + kBy, 0xF, 0xF, false);
+      before += k > mine || (k == mine && from < l);
+    };
+    each_of(turn, std::make_integer_sequence<int, kGroup - 1>{});
+    const bool in = before < g.topk_groups;
+    if (g.bias || sums) {
+      // the least open and the largest closed group (lanes past the experts are
+      // empty groups behind all others)
+      const uint32_t least = ~group_max(in && mine ? ~mine : 0u);
+      const uint32_t most = group_max(in ? 0u : mine);
+      doubt = most > kDeadKey && !clearly(key_logit(least), key_logit(most), g.sigmoid, sums);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) key[c] = in ? key[c] : 0u;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    key[c] = key[c] > kDeadKey ? (key[c] & ~255u) | (255u - (uint32_t)(C * l + c)) : 0u;
+  sort_down<C>(key);
+  uint32_t won = 0u;
+  for (int s = 0; s < g.topk; ++s) {
+    const uint32_t m = group_max(key[0]);
+    won = l == s ? m : won;
+    drop_first<C>(key, key[0] == m);
+  }
+  int id = won >= kLive ? 255 - (int)(won & 255u) : -1;
+  float zs = id >= 0 ? Row::value(zrow[id]) : -kInf;
+  if (g.bias || kType == GQ_F32) {
+    const uint32_t left = group_max(key[0]);             // the largest that was not chosen
+    const uint32_t right = (uint32_t)__shfl_down((int)won, 1, kGroup);
+    const uint32_t next = l == g.topk - 1 ? left : right;
+    bool close = l < g.topk && id >= 0 && next >= kLive;
+    if (g.bias) close = close && !clearly(key_logit(won & ~255u), key_logit(next | 255u), g.sigmoid, false);
+    else close = close && (won ^ next) < 256u;
+    if (__ballot(close)) {
+      // slots of equal logits and biases are in the order of their indices
+      const int n = 255 - (int)(next & 255u);
+      if (close && l != g.topk - 1)
+        close = !(zs == Row::value(zrow[n]) && (!g.bias || g.bias[id] == g.bias[n]));
+    }
+    doubt = doubt || close;
+  }
+  const uint64_t doubts = __ballot(doubt && own < rows);
+  if (doubts) {
+    for (int r = 0; r < kWave / kGroup; ++r) {
+      if (!((doubts >> (kGroup * r)) & 0xFFFFull)) continue;
+      float zr[kC64];
+#pragma unroll
+      for (int c = 0; c < kC64; ++c) {
+        const int e = 64 * c + lane;
+        zr[c] = e < g.E ? load1<kType>(logits, (base + r) * stride + e) : -kInf;
+      }
+      int wid;
+      float wz;
+      select64<kC64>(g, zr, lane, keys[wave], wid, wz);
+      const int tid = __shfl(wid, l, kWave);
+      const float tz = __shfl(wz, l, kWave);
+      if (lane / kGroup == r) {
+        id = tid;
+        zs = tz;
+      }
+    }
+  }
+  const uint32_t slots = group_max(id >= 0 ? logit_key(zs) : 0u);
+  const RowWeights w(g, id, zs, slots, all);
+  float total = w.part;
+  if (!g.sigmoid && !g.renorm) {
+    total = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) total += z[c] == -kInf ? 0.f : expf(z[c] - w.peak);
+  }
+  total = g.sigmoid && !g.renorm ? 1.f : group_sum_last(total, kGroup);
+  if (l < g.topk && own < rows) {
+    g.ids[row * g.topk + l] = id;
+    g.weights[row * g.topk + l] = id >= 0 ? w.part / total * g.scale : 0.f;
+  }
+}
+
+// Lanes of a group where C experts a lane make it 1, 2, 4 or 8 whole ones (1 without
+// groups), else 0.
+static int route_lanes(int E, int groups, int C) {
+  if (groups == 1) return 1;
+  const int size = E / groups;
+  const int lanes = size / C;
+  return size % C == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 8 ? lanes : 0;
 }
 
 }  // namespace gq
@@ -208,8 +527,26 @@ extern "C" int gq_moe_route(const void* logits, int32_t dtype, int64_t rows, int
   // exact for every expert below 1024: the error of an expert e's quotient is
   // below e / 2^20 < 1 / size
   g.size_magic = (1u << 20) / (uint32_t)(num_experts / groups) + 1;
+  while (g.share < 4 && groups << (g.share + 1) <= kWave) ++g.share;
   auto go = [&](auto type) {
     constexpr int T = decltype(type)::value;
+    bool done = false;
+    if (num_experts <= kGroupMaxExperts && topk <= kGroup && rows >= kRouteGroupFrom)
+      by_group<kGroupMaxExperts>(num_experts, [&](auto c) {
+        constexpr int C = decltype(c)::value;
+        const int lanes = route_lanes(num_experts, groups, C);
+        if (!lanes) return;
+        done = true;
+        by_rows(rows, kGroupRows, [&](int64_t at, int64_t n) {
+          g.ids = topk_ids + at * topk;
+          g.weights = topk_weights + at * topk;
+          hipLaunchKernelGGL((moe_route_group_kernel<T, C>),
+                             dim3((unsigned)ceil_div64(n, kGroupRows)), dim3(kRouterThreads), 0,
+                             stream, row_at<T>(logits, at * stride), n, stride,
+                             (int)group_wide<T, C>(logits, num_experts, stride), lanes, g);
+        });
+      });
+    if (done) return;
     by_width(num_experts, [&](auto c) {
       by_rows(rows, kWaveRows, [&](int64_t at, int64_t n) {
         g.ids = topk_ids + at * topk;

@@ -140,22 +140,8 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
 // Below 4096 rows the softmax over all experts (not renormalised) is up to
 // 0.8 us slower in sixteen lanes; hence kGroupFrom.  The 64-bit keys of float32
 // pay from 64 rows an expert on and not at all above 128 experts.
-constexpr int kGroup = 16;
-constexpr int kGroupRows = kRouterThreads / kGroup;
-constexpr int kGroupMaxExperts = 16 * kGroup;
 constexpr int kGroupFrom = 4096;                         // rows
 
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  auto step = [&](auto ctrl) {
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xF, 0xF,
-                                                     false));
-  };
-  step(std::integral_constant<int, 0xB1>{});
-  step(std::integral_constant<int, 0x4E>{});
-  step(std::integral_constant<int, 0x141>{});
-  step(std::integral_constant<int, 0x140>{});
-  return v;
-}
 __device__ __forceinline__ uint64_t group_max(uint64_t v) {
   const uint32_t hi = group_max((uint32_t)(v >> 32));
   const uint32_t lo = group_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
@@ -206,55 +192,6 @@ struct GroupKey<GQ_F32> {
   static __device__ __forceinline__ float logit(uint64_t k) { return key_logit((uint32_t)(k >> 32)); }
 };
 
-// A lane's C raw logits: one or more wide loads where every row's and lane's
-// place allows them (`wide`, from the host), else C narrow ones.  Lanes and
-// elements past the row's experts load some of the row's own.
-template <int kType, int C>
-struct GroupRow {
-  using raw = std::conditional_t<kType == GQ_F32, uint32_t, uint16_t>;
-  static constexpr int kBytes = C * (int)sizeof(raw);
-  static constexpr int kUnit = kBytes < 16 ? kBytes : 16;
-  typedef uint32_t vec __attribute__((ext_vector_type(kUnit / 4)));
-  union {
-    vec v[kBytes / kUnit];
-    raw r[C];
-  };
-  __device__ __forceinline__ void load(const void* row, int l, int E, bool wide) {
-    const raw* p = static_cast<const raw*>(row);
-    if (wide) {
-      const vec* q = reinterpret_cast<const vec*>(p + (C * l < E ? C * l : 0));
-#pragma unroll
-      for (int i = 0; i < kBytes / kUnit; ++i) v[i] = q[i];
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c) r[c] = p[min(C * l + c, E - 1)];
-    }
-  }
-  __device__ __forceinline__ void store(void* row, int l, int E, bool wide) const {
-    raw* p = static_cast<raw*>(row) + C * l;
-    if (wide) {
-      if (C * l < E) {
-#pragma unroll
-        for (int i = 0; i < kBytes / kUnit; ++i) reinterpret_cast<vec*>(p)[i] = v[i];
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (C * l + c < E) p[c] = r[c];
-    }
-  }
-  static __device__ __forceinline__ float value(raw b) {
-    if constexpr (kType == GQ_F32) return __uint_as_float(b);
-    else if constexpr (kType == GQ_BF16) return __uint_as_float((uint32_t)b << 16);
-    else return (float)__builtin_bit_cast(_Float16, b);
-  }
-  static __device__ __forceinline__ raw bits(float v) {
-    if constexpr (kType == GQ_F32) return __float_as_uint(v);
-    else if constexpr (kType == GQ_BF16) return f32_to_bf16_bits(v);
-    else return __builtin_bit_cast(uint16_t, (_Float16)v);
-  }
-};
-
 template <int kType, int C>
 __global__ __launch_bounds__(kRouterThreads) void moe_topk_group_kernel(
     const void* __restrict__ logits, int64_t rows, int E, int64_t stride, int topk, int renorm,
@@ -270,22 +207,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_group_kernel(
   key_t key[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) key[c] = C * l + c < E ? Key::make(x.r[c], C * l + c) : (key_t)0;
-#pragma unroll
-  for (int p = 1; p < C; p *= 2)
-#pragma unroll
-    for (int k = p; k >= 1; k /= 2)
-#pragma unroll
-      for (int j = k % p; j + k < C; j += 2 * k)
-#pragma unroll
-        for (int i = 0; i < k; ++i) {
-          const int u = i + j, v = i + j + k;
-          if (v < C && u / (2 * p) == v / (2 * p)) {
-            const bool swap = key[u] < key[v];
-            const key_t hi = swap ? key[v] : key[u], lo = swap ? key[u] : key[v];
-            key[u] = hi;
-            key[v] = lo;
-          }
-        }
+  sort_down<C>(key);
   const key_t first = group_max(key[0]);
   const float peak = Key::live(first) ? Key::logit(first) : 0.f;
   float total = 0.f;
@@ -297,9 +219,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_group_kernel(
   for (int s = 0; s < topk; ++s) {
     const key_t m = group_max(key[0]);
     won = l == s ? m : won;
-    const bool mine = key[0] == m;
-#pragma unroll
-    for (int c = 0; c < C; ++c) key[c] = mine ? (c + 1 < C ? key[c + 1] : (key_t)0) : key[c];
+    drop_first<C>(key, key[0] == m);
   }
   const bool live = Key::live(won);
   const float part = live ? expf(Key::logit(won) - peak) : 0.f;
@@ -382,22 +302,6 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_group_kernel
     x.r[c] = Row::bits(v);
   }
   x.store(static_cast<raw*>(dz) + row * E, l, E, wide_out);
-}
-
-template <int kMost, typename F>
-static void by_group(int E, F&& f) {
-  if (E <= 4 * kGroup) f(std::integral_constant<int, 4>{});
-  else if (E <= 8 * kGroup) f(std::integral_constant<int, 8>{});
-  else if constexpr (kMost > 8 * kGroup) f(std::integral_constant<int, 16>{});
-}
-
-// Whether rows of E elements of the type, `pitch` elements apart, can be read or
-// written C elements at once.
-template <int kType, int C>
-static bool group_wide(const void* p, int E, int64_t pitch) {
-  constexpr int kSize = (int)sizeof(typename GroupRow<kType, C>::raw);
-  constexpr uintptr_t kMask = GroupRow<kType, C>::kUnit - 1;
-  return E % C == 0 && ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(pitch * kSize)) & kMask) == 0;
 }
 
 }  // namespace gq

@@ -151,7 +151,10 @@ def test_routes(E, groups, topk_groups, topk, score):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("E,groups,topk_groups,topk", [(128, 1, 1, 8), (256, 8, 4, 8), (60, 12, 3, 6),
                                                        (288, 8, 4, 8), (256, 4, 2, 16),
-                                                       (64, 16, 5, 9), (512, 16, 4, 8)])
+                                                       (64, 16, 5, 9), (512, 16, 4, 8),
+                                                       (128, 8, 3, 8), (256, 2, 1, 16),
+                                                       (200, 1, 1, 5), (48, 3, 2, 6),
+                                                       (96, 2, 1, 4), (256, 16, 3, 16)])
 def test_many_rows(E, groups, topk_groups, topk, dtype):
     dev = device()
     g = torch.Generator().manual_seed(E + groups)
