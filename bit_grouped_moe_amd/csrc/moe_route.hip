@@ -89,27 +89,33 @@ __device__ __forceinline__ void select64(const RouteArgs& g, const float (&z)[C]
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     uint64_t first = 0ull, second = 0ull;
-    if (lane < g.groups) {
+    const int group = lane >> g.share;
+    if (group < g.groups) {
       const int size = g.E / g.groups;
-      for (int i = 0; i < size; ++i) {
-        const uint64_t k = keys[lane * size + i];
+      for (int i = lane & ((1 << g.share) - 1); i < size; i += 1 << g.share) {
+        const uint64_t k = keys[group * size + i];
         second = max(second, min(first, k));
         first = max(first, k);
       }
-      if (g.group_top > 1 && second > kDeadKey64) first = key64(key_value(first) + key_value(second));
     }
+    for (int by = 1; by < 1 << g.share; by *= 2) {
+      const uint64_t f = __shfl_xor(first, by, kWave), s = __shfl_xor(second, by, kWave);
+      second = max(min(first, f), max(second, s));
+      first = max(first, f);
+    }
+    if (g.group_top > 1 && second > kDeadKey64) first = key64(key_value(first) + key_value(second));
     int before = 0;                                      // groups ahead of this one
     for (int j = 0; j < g.groups; ++j) {
       const uint64_t k =
-          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(first >> 32), j) << 32) |
-          (uint32_t)__builtin_amdgcn_readlane((int)first, j);
-      before += k > first || (k == first && j < lane);
+          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(first >> 32), j << g.share) << 32) |
+          (uint32_t)__builtin_amdgcn_readlane((int)first, j << g.share);
+      before += k > first || (k == first && j < group);
     }
-    const uint64_t open = __ballot(lane < g.groups && before < g.topk_groups);
+    const uint64_t open = __ballot(group < g.groups && before < g.topk_groups);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int e = 64 * c + lane;
-      if (!((open >> (((uint32_t)e * g.size_magic) >> 20 & 63u)) & 1ull)) key[c] = 0ull;
+      if (!((open >> ((((uint32_t)e * g.size_magic) >> 20) << g.share & 63u)) & 1ull)) key[c] = 0ull;
     }
   }
   uint32_t ids = 0xFFFFFFFFu, won = __float_as_uint(-__builtin_inff());
@@ -327,9 +333,11 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
 // host checks): its best are found in the lane and merged with DPP moves, its rank
 // by rotating the groups' values past each other.  Experts are selected as in the
 // softmax top-k's kernel, from sorted lists of keys that no two experts share: the
-// choice's key without its last 8 bits, and the expert.  What the 8 bits may have
-// hidden is one more case for the selection in 64 bits, by the whole wave, one row
-// after the other.  (16-bit logits' own order needs no more than the other 24.)
+// choice's key without its last 8 bits, and the expert.  (16-bit logits' own order
+// needs no more than the other 24.)  Where two neighbours in a row's slots are too
+// close for that, in 4% of rows, its sixteen largest are put in order in 64 bits, a
+// lane each; what is left, groups that are too close among them (one row in 10^4),
+// goes to the selection in 64 bits, by the whole wave, one row after the other.
 constexpr int kRouteGroupFrom = 4096;                    // rows
 
 template <int kType, int C>
@@ -441,17 +449,64 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
   int id = won >= kLive ? 255 - (int)(won & 255u) : -1;
   float zs = id >= 0 ? Row::value(zrow[id]) : -kInf;
   if (g.bias || kType == GQ_F32) {
-    const uint32_t left = group_max(key[0]);             // the largest that was not chosen
+    uint32_t left = group_max(key[0]);                   // the largest that was not chosen
     const uint32_t right = (uint32_t)__shfl_down((int)won, 1, kGroup);
     const uint32_t next = l == g.topk - 1 ? left : right;
     bool close = l < g.topk && id >= 0 && next >= kLive;
     if (g.bias) close = close && !clearly(key_logit(won & ~255u), key_logit(next | 255u), g.sigmoid, false);
     else close = close && (won ^ next) < 256u;
     if (__ballot(close)) {
-      // slots of equal logits and biases are in the order of their indices
-      const int n = 255 - (int)(next & 255u);
-      if (close && l != g.topk - 1)
-        close = !(zs == Row::value(zrow[n]) && (!g.bias || g.bias[id] == g.bias[n]));
+      // The sixteen largest by these keys in the order of their choices in 64 bits.
+      // That settles a row whose last slot then lies clearly above every other expert.
+      for (int s = g.topk; s < kGroup; ++s) {
+        won = l == s ? left : won;
+        drop_first<C>(key, key[0] == left);
+        left = group_max(key[0]);
+      }
+      const int cand = won >= kLive ? 255 - (int)(won & 255u) : -1;
+      const float zc = cand >= 0 ? Row::value(zrow[cand]) : -kInf;
+      double value = (double)zc;
+      if (g.bias) {
+        double total = 1.0, peak = 0.0;
+        if (!g.sigmoid) {
+          peak = all > kDeadKey ? (double)key_logit(all) : 0.0;
+          total = 0.0;
+#pragma unroll 1
+          for (int e = l; e < g.E; e += kGroup) {
+            const float v = Row::value(zrow[e]);
+            total += v == -kInf ? 0.0 : exp((double)v - peak);
+          }
+#pragma unroll
+          for (int off = kGroup / 2; off > 0; off >>= 1) total += __shfl_xor(total, off, kWave);
+        }
+        value = cand < 0    ? -(double)kInf
+                : g.sigmoid ? 1.0 / (1.0 + exp(-(double)zc)) + (double)g.bias[cand]
+                            : exp((double)zc - peak) / total + (double)g.bias[cand];
+      }
+      const uint64_t mine = cand < 0 ? 0ull : key64(value);
+      const int tie = cand < 0 ? 256 + l : cand;
+      int rank = 0;
+      each_of(
+          [&](auto by) {
+            constexpr int kCtrl = 0x121 + decltype(by)::value;
+            const uint64_t k =
+                ((uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(mine >> 32), kCtrl, 0xF,
+                                                                 0xF, false) << 32) |
+                (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, kCtrl, 0xF, 0xF, false);
+            const int other = __builtin_amdgcn_update_dpp(0, tie, kCtrl, 0xF, 0xF, false);
+            rank += k > mine || (k == mine && other < tie);
+          },
+          std::make_integer_sequence<int, kGroup - 1>{});
+      const bool row_close = (__ballot(close) >> (lane & ~(kGroup - 1)) & 0xFFFFull) != 0;
+      close = row_close && rank < g.topk && cand >= 0 && left >= kLive &&
+              !clearly((float)value, key_logit(left | 255u), g.sigmoid, false);
+      const int to = 4 * ((lane & ~(kGroup - 1)) + rank);
+      const int sent = __builtin_amdgcn_ds_permute(to, cand);
+      const int sent_z = __builtin_amdgcn_ds_permute(to, __float_as_int(zc));
+      if (row_close) {
+        id = l < g.topk ? sent : -1;
+        zs = l < g.topk ? __int_as_float(sent_z) : -kInf;
+      }
     }
     doubt = doubt || close;
   }
