@@ -147,20 +147,21 @@ __device__ __forceinline__ void select64(const RouteArgs& g, const float (&z)[C]
 // Scores in float32 from the hardware exponential and reciprocal.  A sigmoid is off
 // by less than 2^-22 (s (1 - s) |z| < 1/4 times the argument's rounding, and an ulp
 // each of the exponential, the sum and the reciprocal), a softmax by less than
-// 2^-19 (up to 22 additions of its sum), the sum with the bias by 2^-24 of itself.
+// 2^-19 of itself (up to 22 additions of its sum) and so of the row's largest, the
+// sum with the bias by 2^-24 of itself.
 // Two choices further apart than both errors are in the order of float64; so are
 // choices of equal logits and biases, by index.  A row that this does not decide is
-// selected again in 64 bits: 2% of rows with random float32 logits and biases.
+// selected again in 64 bits: one row in 10^3 with random float32 logits and biases.
 __device__ __forceinline__ float fast_exp(float d) {
   return __builtin_amdgcn_exp2f(d * 1.44269504088896341f);
 }
 __device__ __forceinline__ float fast_sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + fast_exp(-z));
 }
-// Whether a choice a (at least) lies clearly above a choice b (at most); false with
-// a NaN.  `twice`: they are sums of two.
-__device__ __forceinline__ bool clearly(float a, float b, bool sigmoid, bool twice) {
-  const float room = (sigmoid ? 0x1p-20f : 0x1p-18f) + 0x1p-22f * (fabsf(a) + fabsf(b));
+// Whether a choice a (at least) lies clearly above a choice b (at most), whose scores
+// are off by less than `off`; false with a NaN.  `twice`: they are sums of two.
+__device__ __forceinline__ bool clearly(float a, float b, float off, bool twice) {
+  const float room = 2.f * off + 0x1p-23f * (fabsf(a) + fabsf(b));
   return a - b > (twice ? 2.f * room : room);
 }
 
@@ -216,6 +217,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
 
   const bool sums = g.groups > 1 && g.group_top > 1;
   float score[C];
+  float off = 0x1p-22f;
   if (g.bias || sums) {
     if (g.sigmoid) {
 #pragma unroll
@@ -229,6 +231,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
         total += score[c];
       }
       total = __builtin_amdgcn_rcpf(wave_fsum(total));
+      off = 0x1p-19f * total;
 #pragma unroll
       for (int c = 0; c < C; ++c) score[c] *= total;
     }
@@ -276,7 +279,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
       // the least open and the largest closed group
       const uint32_t least = ~wave_umax(in ? ~mine : 0u);
       const uint32_t most = wave_umax(group < g.groups && !in ? mine : 0u);
-      sure = most <= kDeadKey || clearly(key_logit(least), key_logit(most), g.sigmoid, sums);
+      sure = most <= kDeadKey || clearly(key_logit(least), key_logit(most), off, sums);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -289,7 +292,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
   float zs = -kInf, won = -kInf;
   if (sure) {
     wave_topk<C>(key, g.topk, id, won);
-    zs = id >= 0 ? load1<kType>(logits, row * stride + id) : -kInf;
+    zs = g.bias && id >= 0 ? load1<kType>(logits, row * stride + id) : won;
     if (g.bias) {
       uint32_t best = key[0];
 #pragma unroll
@@ -302,7 +305,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
         next_id = -1;
       }
       const bool slot = lane < g.topk && id >= 0 && next != -kInf;
-      bool close = slot && !clearly(won, next, g.sigmoid, false);
+      bool close = slot && !clearly(won, next, off, false);
       if (__ballot(close)) {
         // slots of equal logits and biases are in the order of their indices
         const float zn = __shfl_down(zs, 1, kWave);
@@ -338,7 +341,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
 // close for that, in 4% of rows, its sixteen largest are put in order in 64 bits, a
 // lane each; what is left, groups that are too close among them (one row in 10^4),
 // goes to the selection in 64 bits, by the whole wave, one row after the other.
-constexpr int kRouteGroupFrom = 4096;                    // rows
+constexpr int kRouteGroupFrom = 2048;                    // rows
 
 template <int kType, int C>
 __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
@@ -379,6 +382,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
   if (!g.sigmoid) all = group_max(all);
   const bool sums = g.groups > 1 && g.group_top > 1;
   float score[C];
+  float off = 0x1p-22f;
   if (g.bias || sums) {
     if (g.sigmoid) {
 #pragma unroll
@@ -392,6 +396,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
         total += score[c];
       }
       total = __builtin_amdgcn_rcpf(group_sum_last(total, kGroup));
+      off = 0x1p-19f * total;
 #pragma unroll
       for (int c = 0; c < C; ++c) score[c] *= total;
     }
@@ -431,7 +436,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
       // empty groups behind all others)
       const uint32_t least = ~group_max(in && mine ? ~mine : 0u);
       const uint32_t most = group_max(in ? 0u : mine);
-      doubt = most > kDeadKey && !clearly(key_logit(least), key_logit(most), g.sigmoid, sums);
+      doubt = most > kDeadKey && !clearly(key_logit(least), key_logit(most), off, sums);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) key[c] = in ? key[c] : 0u;
@@ -453,7 +458,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
     const uint32_t right = (uint32_t)__shfl_down((int)won, 1, kGroup);
     const uint32_t next = l == g.topk - 1 ? left : right;
     bool close = l < g.topk && id >= 0 && next >= kLive;
-    if (g.bias) close = close && !clearly(key_logit(won & ~255u), key_logit(next | 255u), g.sigmoid, false);
+    if (g.bias) close = close && !clearly(key_logit(won & ~255u), key_logit(next | 255u), off, false);
     else close = close && (won ^ next) < 256u;
     if (__ballot(close)) {
       // The sixteen largest by these keys in the order of their choices in 64 bits.
@@ -499,7 +504,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
           std::make_integer_sequence<int, kGroup - 1>{});
       const bool row_close = (__ballot(close) >> (lane & ~(kGroup - 1)) & 0xFFFFull) != 0;
       close = row_close && rank < g.topk && cand >= 0 && left >= kLive &&
-              !clearly((float)value, key_logit(left | 255u), g.sigmoid, false);
+              !clearly((float)value, key_logit(left | 255u), off, false);
       const int to = 4 * ((lane & ~(kGroup - 1)) + rank);
       const int sent = __builtin_amdgcn_ds_permute(to, cand);
       const int sent_z = __builtin_amdgcn_ds_permute(to, __float_as_int(zc));
