@@ -209,8 +209,8 @@ def test_backward(dtype, wtype, rows, H, pad):
         want, room, wsum, wabs = _backward(dy, h, w, extra, 1e-5)
         _close(dx, want, room, dtype, "dx")
         # rows are added one after the other in a wave (at most rows / 512 of
-        # them), then 4 waves, 32 workgroups and 16 runs
-        deep = (rows + 511) // 512 + 4 + 32 + 16 + 3
+        # them), then 4 waves, 8 of 512 workgroups, 4 and 16 runs
+        deep = (rows + 511) // 512 + 4 + 8 + 4 + 16 + 3
         assert dw.dtype == wtype
         _close(dw, wsum, (deep * U + NORM) * wabs, wtype, "dw")
     alone, none = gq.gq_rms_norm_backward(dyd, hd, wd, eps=1e-5, d_weight=False)
