@@ -30,7 +30,9 @@
 namespace gq {
 
 constexpr int kF8RowBytes = 128;
-// Tiles of up to this many rows: waves side by side, each over all of the rows.
+// Tiles of up to this many rows: waves side by side, each over all of the rows (32
+// experts of 5760 rows of K 2880 with 32, 64 and 128 pairs each: 88, 95 and 103 us; as
+// larger tiles 100, 102 and 112).
 constexpr int kF8Small = 128;
 
 // kWide: waves 2 x 2, a wave takes every second 32-row sub-tile (so that the
@@ -61,27 +63,30 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
   // ---- loads: 8 rows of 128 bytes per instruction, rows 8 (4 j + wave) + ..;
   // lane L fills the 16-byte slot L % 8 of row L / 8 with the chunk that the
   // swizzle puts there ((row >> 1) & 7 = 4 (wave & 1) + (L >> 4)).  Rows past
-  // the tile re-read its last one, chunks past a row's end that row's last
-  // (in bounds, never used): no branch, so that the loads can be placed
-  // between the matrix instructions
+  // the tile re-read its last one; chunks past a row's end are the next row's, or
+  // past the buffer, which its range check answers with zeros, and are never
+  // used.  So a lane's offsets stay as they are and the step is a scalar: an
+  // address that is formed for each load holds the wave up until the load before
+  // has read its own from the same register (8192 pairs evenly on 32 experts,
+  // gate_up with clamped chunks 156 us, so 148)
   const uint32_t chunk = (uint32_t)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
   constexpr int kJA = kWide ? 8 : 4;                      // 8-row groups of activations a wave loads
   uint32_t aoff[kJA], boff[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     boff[j] = (uint32_t)min(wn0 + 8 * (4 * j + wave) + (lane >> 3), g.Nw - 1) *
-              (uint32_t)(g.Kw / 2);
-  // byte offsets in a row of the lane's chunk of step s's activations, and of
-  // the weights of steps 2 s and 2 s + 1
-  auto a_chunk = [&](int s) { return 16u * min((uint32_t)s * 8 + chunk, (uint32_t)(2 * nb - 1)); };
-  auto b_chunk = [&](int s) { return 16u * min((uint32_t)s * 8 + chunk, (uint32_t)(nb - 1)); };
-  auto load_a = [&](int j, uint32_t c, uint8_t* A) {
+                  (uint32_t)(g.Kw / 2) +
+              16 * chunk;
+  // s: of a, the step; of b, half of it (a buffer holds two steps' weights)
+  auto load_a = [&](int j, int s, uint8_t* A) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        arsrc, (lds_void_t*)(A + 8 * (4 * j + wave) * kF8RowBytes), 16, (int)(aoff[j] + c), 0, 0, 0);
+        arsrc, (lds_void_t*)(A + 8 * (4 * j + wave) * kF8RowBytes), 16, (int)aoff[j],
+        s * kF8RowBytes, 0, 0);
   };
-  auto load_b = [&](int j, uint32_t c, uint8_t* B) {
+  auto load_b = [&](int j, int s, uint8_t* B) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        brsrc, (lds_void_t*)(B + 8 * (4 * j + wave) * kF8RowBytes), 16, (int)(boff[j] + c), 0, 0, 0);
+        brsrc, (lds_void_t*)(B + 8 * (4 * j + wave) * kF8RowBytes), 16, (int)boff[j],
+        s * kF8RowBytes, 0, 0);
   };
   // 8 scale bytes of a row for steps 2 s and 2 s + 1.  The first ones of a short
   // row are taken one by one (past its end the last again); later ones, whose
@@ -130,15 +135,16 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
 
   // first step: the weight rows need no routing and go first
 #pragma unroll
-  for (int j = 0; j < 8; ++j) load_b(j, b_chunk(0), B0);
+  for (int j = 0; j < 8; ++j) load_b(j, 0, B0);
   const u32x2 sa_first = first_scales(as_row), sb_first = first_scales(bs_row);
   lds_barrier();                                          // row_s
 #pragma unroll
   for (int j = 0; j < kJA; ++j)
     aoff[j] =
-        (uint32_t)row_s[min(8 * (4 * j + wave) + (lane >> 3), t.valid - 1)] * (uint32_t)g.Kw;
+        (uint32_t)row_s[min(8 * (4 * j + wave) + (lane >> 3), t.valid - 1)] * (uint32_t)g.Kw +
+        16 * chunk;
 #pragma unroll
-  for (int j = 0; j < kJA; ++j) load_a(j, a_chunk(0), A0);
+  for (int j = 0; j < kJA; ++j) load_a(j, 0, A0);
   // the pairs' weights arrive with the first step; added after the loop
   const float own_scale = !kUnit && g.pair_scale ? g.pair_scale[pair] : 1.f;
   SA0[tid] = sa_first;
@@ -150,19 +156,21 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
   auto run_loop = [&](auto rows_c) {
     constexpr int kA = decltype(rows_c)::value;           // active sub-tiles of the wave
     // One step, as 2 kA groups of kC matrix instructions that the scheduler keeps
-    // in order: the second depth's fragment reads and the next loads stand
-    // between the groups.  kOdd: the step's weights are its buffer's second half.
+    // in order: the second depth's fragment reads stand between the first half of
+    // the groups, the next loads between three quarters of them, so that the last
+    // ones have a quarter of the step's time to arrive (8192 pairs on 32 experts of
+    // K 2880, gate_up 192 us with the loads over all groups, 193 over half, so 189.5;
+    // down 109, 107, 105).  kOdd: the step's weights are its buffer's second half.
     auto step = [&](auto odd_c, int s, const uint8_t* A, const uint8_t* B, const u32x2* SA,
                     const u32x2* SB, uint8_t* An, uint8_t* Bn, u32x2* SAn, u32x2* SBn) {
       constexpr int kOdd = decltype(odd_c)::value;
-      constexpr int kR = 2 * kA + kC, kV = kJA + 4, kG = 2 * kA;
+      constexpr int kR = 2 * kA + kC, kV = kJA + 4, kG = (3 * kA + 1) / 2;
       __builtin_amdgcn_sched_barrier(0);
       u32x2 na, nbs;
       if constexpr (kOdd) {
         na = load_scales(as_row, s / 2 + 1);
         nbs = load_scales(bs_row, s / 2 + 1);
       }
-      const uint32_t ca = a_chunk(s + 1), cb = b_chunk(s / 2 + 1);
       uint32_t sa[kA], sb[kC];
       u32x4 fa[2][kA][2], fb[2][kC];
       auto read = [&](int u, int r) {
@@ -185,9 +193,9 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
           __builtin_amdgcn_sched_barrier(0);
           const int gi = u * kA + i;
 #pragma unroll
-          for (int v = kV * gi / kG; v < kV * (gi + 1) / kG; ++v) {
-            if (v < 4) load_b(4 * kOdd + v, cb, Bn);
-            else load_a(v - 4, ca, An);
+          for (int v = kV * gi / kG; v < (gi < kG ? kV * (gi + 1) / kG : 0); ++v) {
+            if (v < 4) load_b(4 * kOdd + v, s / 2 + 1, Bn);
+            else load_a(v - 4, s + 1, An);
           }
           if (u == 0) {
 #pragma unroll
