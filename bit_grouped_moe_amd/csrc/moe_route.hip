@@ -341,7 +341,13 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
 // close for that, in 4% of rows, its sixteen largest are put in order in 64 bits, a
 // lane each; what is left, groups that are too close among them (one row in 10^4),
 // goes to the selection in 64 bits, by the whole wave, one row after the other.
-constexpr int kRouteGroupFrom = 2048;                    // rows
+// From how many rows: a wave a row until the chip is full of waves (bf16 logits without
+// groups, a wave against sixteen lanes a row, of 256 experts: 2048 rows 5.5 and 6.7 us,
+// 4096 9.7 and 6.8, 16384 16.6 and 11.3; of 128: 4.5 and 5.6, 6.5 and 5.6, 13.8 and 8.0;
+// float32 with groups, of 64: 4.8 and 5.5, 6.0 and 5.6, 13.7 and 7.6; of 256 in 8
+// groups, whose selection holds a wave twice as long: 1024 rows 6.0 and 8.0, 2048 10.3
+// and 8.1, 16384 23.1 and 14.8).
+constexpr int kRouteGroupFrom = 4096, kRouteGroupFromWide = 2048;
 
 template <int kType, int C>
 __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
@@ -591,7 +597,8 @@ extern "C" int gq_moe_route(const void* logits, int32_t dtype, int64_t rows, int
   auto go = [&](auto type) {
     constexpr int T = decltype(type)::value;
     bool done = false;
-    if (num_experts <= kGroupMaxExperts && topk <= kGroup && rows >= kRouteGroupFrom)
+    if (num_experts <= kGroupMaxExperts && topk <= kGroup &&
+        rows >= (groups > 1 && num_experts > 128 ? kRouteGroupFromWide : kRouteGroupFrom))
       by_group<kGroupMaxExperts>(num_experts, [&](auto c) {
         constexpr int C = decltype(c)::value;
         const int lanes = route_lanes(num_experts, groups, C);

@@ -238,7 +238,7 @@ struct NormBackArgs {
 // A workgroup takes every gridDim.x-th group of rows and adds what its lanes'
 // columns give to dw in registers; its sums go to one row of `partial`.  A row's
 // loads go out before the row before it is worked on: a row is one memory latency
-// and a barrier otherwise (16384 rows of 2048 in bf16, 73 -> 61 us).
+// and a barrier otherwise (16384 rows of 2048 in bf16, 73 us, so 48).
 template <int kType, int kWType, int kWaves, int kC>
 __global__ __launch_bounds__(kNormThreads<kWaves>) void rms_norm_backward_kernel(NormBackArgs g) {
   constexpr int kLanes = kWaves * kWave;
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(kNormThreads<kWaves>) void rms_norm_backward_kernel
 
 // dw: the sums of the workgroups' rows, 16 columns a workgroup and 64 runs of rows
 // side by side, then the runs in a fixed order.  (Bound by latency: columns 64 at a
-// time and 16 runs took 12 us for 512 rows of 2048, this 4.)
+// time and 16 runs took 12 us for 512 rows of 2048, this 6.)
 constexpr int kGainCols = 16, kGainRuns = 64;
 template <int kWType>
 __global__ __launch_bounds__(kGainCols * kGainRuns) void rms_norm_gain_kernel(
@@ -399,14 +399,27 @@ __global__ __launch_bounds__(kGainCols * kGainRuns) void rms_norm_gain_kernel(
   }
 }
 
-// f(waves a row, steps) for rows of H values.
+// f(waves a row, steps) for rows of H values.  A wave a row needs no barrier and many
+// rows want few instructions a row; up to a row for each compute unit, a row's own
+// latency counts and its values are spread over all the lanes there are.  bf16, us,
+// forward and backward with the gain's gradient, fewer waves a row against more:
+//   rows    1024 wide (1, 4 waves)    2880 (4, 16)            8192 (4, 16)
+//      1    3.3 5.9   2.9 5.1         3.6  6.0   3.1  5.4     5.2  8.1   3.6  6.2
+//    256    3.9 6.3   3.2 6.8         4.2  9.2   3.8  8.6     6.5 16.3   5.0 14.4
+//    512    4.0 6.9   3.4 7.7         4.8 11.8   5.3 12.7     8.4 19.9   7.5 20.1
+//   1024    4.3 8.0   4.5 8.7         6.1 13.4   8.2 13.9    12.5 23.2  14.3 24.7
+// 16384 rows of 512: a wave a row 13.2 and 16.5, four 18.1 and 34.2; of 2048: one wave
+// 43.3 and 47.8, four 41.1 and 47.7.
+constexpr int kNormFew = 256;
 template <typename F>
-static void by_row(int H, F&& f) {
+static void by_row(int64_t rows, int H, F&& f) {
   auto go = [&](auto w, auto c) { f(w, c); };
   using std::integral_constant;
+  const bool few = rows <= kNormFew;
   if (H <= 512) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  else if (H <= 1024) go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+  else if (H <= 1024 && !few) go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
   else if (H <= 2048) go(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else if (H <= 8192 && few) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   else if (H <= 4096) go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
   else if (H <= 8192) go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
   else if (H <= 16384) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
@@ -442,11 +455,13 @@ static bool element_aligned(const void* p, int32_t dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(type_size(dtype) - 1)) == 0;
 }
 
-// Workgroups of the backward pass: its partial sums are one row each.
+// Workgroups of the backward pass: its partial sums are one row each.  (Two a compute
+// unit: 16384 rows of 2048 in bf16 take 63 us with 256 workgroups, 47.7 with 512, 48.4
+// with 1024; 2048 rows of 8192 30, 31.6 and 43.)
 constexpr int64_t kBackGroups = 512;
 static int64_t back_groups(int64_t rows, int H) {
   int64_t groups = 0;
-  by_row(H, [&](auto w, auto) {
+  by_row(rows, H, [&](auto w, auto) {
     constexpr int kRows = kNormThreads<decltype(w)::value> / (decltype(w)::value * kWave);
     groups = ceil_div64(rows, kRows);
   });
@@ -480,7 +495,7 @@ extern "C" int gq_rms_norm(const void* x, int64_t x_stride, const void* residual
              reinterpret_cast<u32x2*>(codes), scales, reinterpret_cast<u32x4*>(values), rows,
              x_stride * size, residual_stride * size, H, eps};
   by_types(dtype, weight_dtype, [&](auto t, auto wt) {
-    by_row(H, [&](auto w, auto c) {
+    by_row(rows, H, [&](auto w, auto c) {
       constexpr int kWaves = decltype(w)::value, kThreads = kNormThreads<kWaves>;
       const int64_t groups = ceil_div64(rows, kThreads / (kWaves * kWave));
       const int64_t most = most_groups(kThreads);
@@ -531,7 +546,7 @@ extern "C" int gq_rms_norm_backward(const void* d_y, int64_t d_y_stride, const v
   by_types(dtype, weight_dtype, [&](auto t, auto wt) {
     constexpr int T = decltype(t)::value, WT = decltype(wt)::value;
     if (rows > 0)
-      by_row(H, [&](auto w, auto c) {
+      by_row(rows, H, [&](auto w, auto c) {
         constexpr int kWaves = decltype(w)::value;
         hipLaunchKernelGGL((rms_norm_backward_kernel<T, WT, kWaves, decltype(c)::value>),
                            dim3((unsigned)groups), dim3(kNormThreads<kWaves>), 0, stream, g);

@@ -219,6 +219,34 @@ def test_backward(dtype, wtype, rows, H, pad):
     assert none is None and torch.equal(alone, both)
 
 
+@pytest.mark.parametrize("rows", [256, 257])
+@pytest.mark.parametrize("H", [513, 1024, 2049, 2880, 4096, 4097, 8192])
+def test_few_and_many_rows(rows, H):
+    """Widths whose rows take more waves while there are few of them, at both
+    sides of the border: outputs, codes and gradients, and the first rows in a
+    call of their own."""
+    dev = device()
+    x, r, w = _inputs(rows, H, torch.bfloat16, torch.bfloat16, 3, seed=9)
+    xd, rd, wd = x.to(dev), r.to(dev), w.to(dev)
+    say("norm of few and many rows", rows, H)
+    q = H % 32 == 0
+    got = gq.gq_rms_norm(xd, wd, residual=rd, mxfp8=q, values=q)
+    dx, dw = gq.gq_rms_norm_backward(xd, got.residual, wd, d_residual=rd)
+    own = gq.gq_rms_norm(xd[:3], wd, residual=rd[:3])
+    torch.cuda.synchronize()
+    h = _sum(x, r)
+    assert torch.equal(got.residual.cpu(), h) and torch.equal(own.residual.cpu(), h[:3])
+    want = _norm(h, w, 1e-6)
+    _close(got.y, want, NORM * want.abs(), torch.bfloat16, "y")
+    _close(own.y, want[:3], NORM * want[:3].abs(), torch.bfloat16, "own y")
+    if q:
+        _values_are_nearest(*got.mxfp8, got.values, want)
+    wx, room, ws, wabs = _backward(x, h, w, r, 1e-6)
+    _close(dx, wx, room, torch.bfloat16, "dx")
+    deep = 1 + 4 + 8 + 4 + 16 + 3
+    _close(dw, ws, (deep * U + NORM) * wabs, torch.bfloat16, "dw")
+
+
 def test_backward_against_differences():
     """The gradient of a random linear function of y and h, against central
     differences of the forward kernel in float32."""
