@@ -506,7 +506,9 @@ int gq_mxfp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, i
  *   codes, scales, values  or NULL: y in MXFP8, as gq_mxfp8_quantize would
  *             write it for a float32 y (H a multiple of 32)            out
  * float32 throughout; h and y are rounded once each, the codes are made of
- * the unrounded y.  The norm is the norm of the rounded h.
+ * the unrounded y.  The norm is the norm of the rounded h.  A finite row whose
+ * squares' sum passes float32's largest value gives zeros; with eps = 0 one whose
+ * squares vanish in float32 (a zero row among them) gives infinities or NaN.
  * sum and y may each be x or residual where that is contiguous (they must not
  * both be the same one); no other output may overlap an input.
  * InvalidValue: null x or weight, no output, sum without a residual, codes
