@@ -159,11 +159,31 @@ __device__ __forceinline__ float fast_sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + fast_exp(-z));
 }
 // Whether a choice a (at least) lies clearly above a choice b (at most), whose scores
-// are off by less than `off`; false with a NaN.  `twice`: they are sums of two.
-__device__ __forceinline__ bool clearly(float a, float b, float off, bool twice) {
-  const float room = 2.f * off + 0x1p-23f * (fabsf(a) + fabsf(b));
-  return a - b > (twice ? 2.f * room : room);
+// are off by less than `off`; false with a NaN.
+__device__ __forceinline__ bool clearly(float a, float b, float off) {
+  return a - b > 2.f * off + 0x1p-23f * (fabsf(a) + fabsf(b));
 }
+// A group's value from the keys of its largest and (sums) second largest choice, as
+// a key (0: all masked), and the keys of bounds of what it is in 64 bits.  The
+// choices may cancel: their roundings count by their own size, not by their sum's.
+struct GroupValue {
+  uint32_t key, low, high;
+  __device__ __forceinline__ GroupValue(uint32_t first, uint32_t second, float off, bool sums) {
+    float v = first > kDeadKey ? key_logit(first) : -__builtin_inff();
+    float size = fabsf(v);
+    if (sums && second > kDeadKey) {
+      const float w = key_logit(second);
+      v += w;
+      size += fabsf(w);
+    }
+    key = first > kDeadKey ? logit_key(v) : 0u;
+    // off for each choice; half a step for each, for v and for a bound itself
+    const float room = (sums ? 2.f : 1.f) * off + 0x1p-22f * size;
+    const bool sound = room < __builtin_inff();          // no NaN, nothing overflowed
+    low = sound ? logit_key(v - room) : 0u;
+    high = sound ? logit_key(v + room) : ~0u;
+  }
+};
 
 // The two largest of this lane's two and another lane's.
 template <int kCtrl>
@@ -265,9 +285,8 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
     if (g.share > 1) two_largest<0x4E>(first, second);
     if (g.share > 2) two_largest<0x141>(first, second);
     if (g.share > 3) two_largest<0x140>(first, second);
-    float v = first > kDeadKey ? key_logit(first) : -kInf;
-    if (sums && second > kDeadKey) v += key_logit(second);
-    const uint32_t mine = first > kDeadKey ? logit_key(v) : 0u;
+    const GroupValue value(first, second, off, sums);
+    const uint32_t mine = value.key;
     int before = 0;                                      // groups ahead of this one
     for (int j = 0; j < g.groups; ++j) {
       const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)mine, j << g.share);
@@ -277,9 +296,9 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
     const uint64_t open = __ballot(in);
     if (g.bias || sums) {
       // the least open and the largest closed group
-      const uint32_t least = ~wave_umax(in ? ~mine : 0u);
-      const uint32_t most = wave_umax(group < g.groups && !in ? mine : 0u);
-      sure = most <= kDeadKey || clearly(key_logit(least), key_logit(most), off, sums);
+      const uint32_t least = ~wave_umax(in && mine ? ~value.low : 0u);
+      const uint32_t most = wave_umax(group < g.groups && !in && mine ? value.high : 0u);
+      sure = most <= kDeadKey || least > most;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -305,7 +324,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_kernel(
         next_id = -1;
       }
       const bool slot = lane < g.topk && id >= 0 && next != -kInf;
-      bool close = slot && !clearly(won, next, off, false);
+      bool close = slot && !clearly(won, next, off);
       if (__ballot(close)) {
         // slots of equal logits and biases are in the order of their indices
         const float zn = __shfl_down(zs, 1, kWave);
@@ -423,9 +442,8 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
     if (lanes > 1) two_largest<0xB1>(first, second);
     if (lanes > 2) two_largest<0x4E>(first, second);
     if (lanes > 4) two_largest<0x141>(first, second);
-    float v = first > kDeadKey ? key_logit(first) : -kInf;
-    if (sums && second > kDeadKey) v += key_logit(second);
-    const uint32_t mine = first > kDeadKey ? logit_key(v) : 0u;
+    const GroupValue value(first, second, off, sums);
+    const uint32_t mine = value.key;
     int before = 0;                                      // groups ahead of this one
     auto turn = [&](auto by) {
       constexpr int kBy = decltype(by)::value + 1;
@@ -440,9 +458,9 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
     if (g.bias || sums) {
       // the least open and the largest closed group (lanes past the experts are
       // empty groups behind all others)
-      const uint32_t least = ~group_max(in && mine ? ~mine : 0u);
-      const uint32_t most = group_max(in ? 0u : mine);
-      doubt = most > kDeadKey && !clearly(key_logit(least), key_logit(most), off, sums);
+      const uint32_t least = ~group_max(in && mine ? ~value.low : 0u);
+      const uint32_t most = group_max(!in && mine ? value.high : 0u);
+      doubt = most > kDeadKey && least <= most;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) key[c] = in ? key[c] : 0u;
@@ -464,7 +482,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
     const uint32_t right = (uint32_t)__shfl_down((int)won, 1, kGroup);
     const uint32_t next = l == g.topk - 1 ? left : right;
     bool close = l < g.topk && id >= 0 && next >= kLive;
-    if (g.bias) close = close && !clearly(key_logit(won & ~255u), key_logit(next | 255u), off, false);
+    if (g.bias) close = close && !clearly(key_logit(won & ~255u), key_logit(next | 255u), off);
     else close = close && (won ^ next) < 256u;
     if (__ballot(close)) {
       // The sixteen largest by these keys in the order of their choices in 64 bits.
@@ -510,7 +528,7 @@ __global__ __launch_bounds__(kRouterThreads) void moe_route_group_kernel(
           std::make_integer_sequence<int, kGroup - 1>{});
       const bool row_close = (__ballot(close) >> (lane & ~(kGroup - 1)) & 0xFFFFull) != 0;
       close = row_close && rank < g.topk && cand >= 0 && left >= kLive &&
-              !clearly((float)value, key_logit(left | 255u), off, false);
+              !clearly((float)value, key_logit(left | 255u), off);
       const int to = 4 * ((lane & ~(kGroup - 1)) + rank);
       const int sent = __builtin_amdgcn_ds_permute(to, cand);
       const int sent_z = __builtin_amdgcn_ds_permute(to, __float_as_int(zc));

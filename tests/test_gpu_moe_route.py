@@ -179,6 +179,33 @@ def test_many_rows(E, groups, topk_groups, topk, dtype):
                 _check_weights(w, zn, want, score, n % 3 != 0, 1.0)
 
 
+@pytest.mark.parametrize("rows", [5, 700, 4500])
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (60, 12)])
+def test_groups_whose_choices_cancel(E, groups, rows):
+    """Biases of both signs in each group, far above the scores: a group's sum is
+    small where its choices' own roundings in float32 are not; and a masked-out
+    group of the lowest value."""
+    dev = device()
+    g = np.random.default_rng(23)
+    size = E // groups
+    b = np.full((groups, size), -40000.0, dtype=np.float32)
+    b[:, 0] = 16384.0
+    b[:, size // 2] = -16384.0 + np.float32(2.0 ** -10) * g.integers(-40, 40, groups)
+    b[1] = -3.4e38
+    b = b.reshape(-1)
+    z = (g.standard_normal((rows, E)) * 2).astype(np.float32)
+    topk = min(6, 2 * size)
+    for score in ("sigmoid", "softmax"):
+        say("route cancelling", E, groups, rows, score)
+        ids, w = gq.gq_moe_route(torch.tensor(z).to(dev), topk, score=score,
+                                 bias=torch.tensor(b).to(dev), groups=groups, topk_groups=4,
+                                 group_top=2)
+        torch.cuda.synchronize()
+        want = _select(z, topk, score, b, groups, 4, 2)
+        assert np.array_equal(ids.cpu().numpy(), want), score
+        _check_weights(w, z, want, score, True, 1.0)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_choices_as_close_as_float64_tells(score):
     """Biases that make up for the scores' differences, so that choices agree to
