@@ -455,6 +455,12 @@ static bool element_aligned(const void* p, int32_t dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(type_size(dtype) - 1)) == 0;
 }
 
+// An output in place of an input that lies at another stride would overwrite rows
+// that are still to be read.
+static bool apart(const void* out, const void* in, int64_t rows, int64_t stride, int32_t H) {
+  return !out || out != in || rows == 1 || stride == H;
+}
+
 // Workgroups of the backward pass: its partial sums are one row each.  (Two a compute
 // unit: 16384 rows of 2048 in bf16 take 63 us with 256 workgroups, 47.7 with 512, 48.4
 // with 1024; 2048 rows of 8192 30, 31.6 and 43.)
@@ -489,6 +495,10 @@ extern "C" int gq_rms_norm(const void* x, int64_t x_stride, const void* residual
   if (!strides_fit(rows, x_stride) || (residual && !strides_fit(rows, residual_stride)) ||
       !strides_fit(rows, H))
     return kNotSupported;
+  if ((sum && sum == y) || !apart(sum, x, rows, x_stride, H) || !apart(y, x, rows, x_stride, H) ||
+      !apart(sum, residual, rows, residual_stride, H) ||
+      !apart(y, residual, rows, residual_stride, H))
+    return kInvalid;
   const int size = type_size(dtype);
   NormArgs g{static_cast<const char*>(x), static_cast<const char*>(residual),
              static_cast<const char*>(weight), static_cast<char*>(sum), static_cast<char*>(y),
@@ -538,6 +548,9 @@ extern "C" int gq_rms_norm_backward(const void* d_y, int64_t d_y_stride, const v
   if (!strides_fit(rows, d_y_stride) || !strides_fit(rows, h_stride) ||
       (d_h && !strides_fit(rows, d_h_stride)) || !strides_fit(rows, H))
     return kNotSupported;
+  if (rows > 0 && (!apart(d_x, d_y, rows, d_y_stride, H) || !apart(d_x, h, rows, h_stride, H) ||
+                   !apart(d_x, d_h, rows, d_h_stride, H)))
+    return kInvalid;
   const int size = type_size(dtype);
   NormBackArgs g{static_cast<const char*>(d_y), static_cast<const char*>(h),
                  static_cast<const char*>(d_h), static_cast<const char*>(weight),

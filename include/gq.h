@@ -515,7 +515,8 @@ int gq_mxfp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, i
  *   without scales or the reverse, values without codes, codes with H % 32,
  *   unknown dtype, a weight_dtype that is neither, rows < 0, H < 1, a stride
  *   < H, eps < 0 or not finite, a pointer not aligned to its element, codes or
- *   values not 16-byte aligned.
+ *   values not 16-byte aligned, sum and y at one address, or one of them in place
+ *   of an input that is not contiguous.
  * NotSupported: H > 32768, rows*stride >= 2^60.  rows == 0 enqueues nothing.
  *
  * gq_rms_norm_backward: gradients of y to x (and residual, the same) and to

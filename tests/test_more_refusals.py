@@ -59,6 +59,24 @@ def test_norm_rejects(lib):
     assert call(rows=0, x=NULL, w=NULL, y=NULL) == 0
 
 
+def test_outputs_in_place_of_strided_inputs(lib):
+    """In place only where rows do not lie at another stride; the same for both
+    of a norm's outputs and for the gradient."""
+    G, D = ctypes.c_void_p(0x200000), ctypes.c_void_p(0x300000)
+    call = _caller(lib.gq_rms_norm, "x xs r rs dt rows H w wdt eps sum y c s v".split(),
+                   dict(x=F, xs=72, r=G, rs=80, dt=1, rows=4, H=64, w=F, wdt=1, eps=1e-6,
+                        sum=NULL, y=NULL, c=NULL, s=NULL, v=NULL))
+    for bad in (dict(y=F), dict(sum=F), dict(y=G), dict(sum=G), dict(sum=D, y=D),
+                dict(sum=F, y=F, xs=64), dict(y=F, rows=2)):
+        assert call(**bad) == INVALID, bad
+    call = _caller(lib.gq_rms_norm_backward,
+                   "dy dys h hs dh dhs dt rows H w wdt eps dx dw ws wn".split(),
+                   dict(dy=F, dys=72, h=G, hs=72, dh=D, dhs=72, dt=2, rows=4, H=64, w=F, wdt=2,
+                        eps=1e-6, dx=F, dw=NULL, ws=NULL, wn=0))
+    for bad in (dict(dx=F), dict(dx=G), dict(dx=D)):
+        assert call(**bad) == INVALID, bad
+
+
 def test_norm_backward_rejects(lib):
     call = _caller(lib.gq_rms_norm_backward,
                    "dy dys h hs dh dhs dt rows H w wdt eps dx dw ws wn".split(),
