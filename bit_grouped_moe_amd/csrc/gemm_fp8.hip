@@ -65,9 +65,12 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
   // swizzle puts there ((row >> 1) & 7 = 4 (wave & 1) + (L >> 4)).  Rows past
   // the tile re-read its last one; chunks past a row's end are the next row's, or
   // past the buffer, which its range check answers with zeros, and are never
-  // used.  So a lane's offsets stay as they are and the step is a scalar: an
-  // address that is formed for each load holds the wave up until the load before
-  // has read its own from the same register (8192 pairs evenly on 32 experts,
+  // used.  (The check takes the lane's offset against the buffer's length less the
+  // scalar one, which is below the length: a step of the activations starts inside
+  // a row, a piece of the weights at most 64 bytes past a row's length, of which an
+  // expert has 32 or more.)  So a lane's offsets stay as they are and the step is a
+  // scalar: an address that is formed for each load holds the wave up until the load
+  // before has read its own from the same register (8192 pairs evenly on 32 experts,
   // gate_up with clamped chunks 156 us, so 148)
   const uint32_t chunk = (uint32_t)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
   constexpr int kJA = kWide ? 8 : 4;                      // 8-row groups of activations a wave loads
