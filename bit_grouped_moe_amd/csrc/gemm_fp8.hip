@@ -34,16 +34,32 @@ constexpr int kF8RowBytes = 128;
 // experts of 5760 rows of K 2880 with 32, 64 and 128 pairs each: 88, 95 and 103 us; as
 // larger tiles 100, 102 and 112).
 constexpr int kF8Small = 128;
+// Column tiles of 128 instead of 256 where all of a call's tiles then still run at
+// once, on a compute unit each: a tile's time is what counts there (us, 256 and 128
+// columns: 4096 pairs of 8 experts, [1024, 2048] 28.9 and 22.7, 8192 of 8, [512, 768]
+// 16.9 and 12.0, 1024 of 4, [2880, 2880] 36.5 and 30.2, 666 of 6, [544, 1056] 11.4 and
+// 9.6).  Tiles that need more rounds read the activations twice as often (256 of 16,
+// [2400, 2880] 23.6 and 38.9), and where an expert has few rows the waves side by side
+// of the wide tile make up for it (32 of 8, [1536, 2048] 11.5 and 12.2).
+constexpr int kF8Narrow = 128, kF8Units = 256, kF8FewRows = 32;
+static bool narrow_tiles(int64_t P, int E, int N) {
+  return P > (int64_t)kF8FewRows * E &&
+         (P / kTM + E) * ceil_div64(N, kF8Narrow) <= kF8Units;
+}
+
 
 // kWide: waves 2 x 2, a wave takes every second 32-row sub-tile (so that the
-// row halves stay balanced when the tile is not full) and 128 columns; else
-// (tiles of at most 128 rows) four waves side by side, 64 columns each.
-template <bool kWide, bool kUnit>
+// row halves stay balanced when the tile is not full) and half of the tile's kCols
+// columns; else (tiles of 256 columns and at most 128 rows) four waves side by
+// side, 64 columns each.
+template <bool kWide, bool kUnit, int kCols>
 __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, int tid,
                                          uint8_t* A0, uint8_t* A1, uint8_t* B0, uint8_t* B1,
                                          u32x2* SA0, u32x2* SA1, u32x2* SB0, u32x2* SB1,
                                          int* pair_s, int* row_s, float* scale_s, int pair) {
-  constexpr int kC = kWide ? 4 : 2;                       // column blocks of a wave
+  constexpr int kC = kWide ? kCols / 64 : 2;              // column blocks of a wave
+  constexpr int kJB = kCols / 32;                         // 8-row groups of weights a wave loads
+  static_assert(kWide || kCols == kXN);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lr = lane & 31, lh = lane >> 5;
   const int nb = g.Kw / 32;                               // K blocks
@@ -74,9 +90,9 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
   // gate_up with clamped chunks 156 us, so 148)
   const uint32_t chunk = (uint32_t)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
   constexpr int kJA = kWide ? 8 : 4;                      // 8-row groups of activations a wave loads
-  uint32_t aoff[kJA], boff[8];
+  uint32_t aoff[kJA], boff[kJB];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < kJB; ++j)
     boff[j] = (uint32_t)min(wn0 + 8 * (4 * j + wave) + (lane >> 3), g.Nw - 1) *
                   (uint32_t)(g.Kw / 2) +
               16 * chunk;
@@ -113,7 +129,7 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
 
   // sub-tile i of this wave / its column block c, as rows of the LDS tiles
   auto arow = [&](int i) { return 32 * (kWide ? 2 * i + (wave >> 1) : i) + lr; };
-  auto bcol = [&](int c) { return (kWide ? 128 * (wave & 1) : 64 * wave) + 32 * c + lr; };
+  auto bcol = [&](int c) { return (kWide ? kCols / 2 * (wave & 1) : 64 * wave) + 32 * c + lr; };
   const int swz = (lr >> 1) & 7;                          // of every row of a lane
   auto piece = [&](const uint8_t* buf, int row, int c) -> u32x4 {
     return *reinterpret_cast<const u32x4*>(buf + row * kF8RowBytes + 16 * (c ^ swz));
@@ -138,7 +154,7 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
 
   // first step: the weight rows need no routing and go first
 #pragma unroll
-  for (int j = 0; j < 8; ++j) load_b(j, 0, B0);
+  for (int j = 0; j < kJB; ++j) load_b(j, 0, B0);
   const u32x2 sa_first = first_scales(as_row), sb_first = first_scales(bs_row);
   lds_barrier();                                          // row_s
 #pragma unroll
@@ -167,7 +183,7 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
     auto step = [&](auto odd_c, int s, const uint8_t* A, const uint8_t* B, const u32x2* SA,
                     const u32x2* SB, uint8_t* An, uint8_t* Bn, u32x2* SAn, u32x2* SBn) {
       constexpr int kOdd = decltype(odd_c)::value;
-      constexpr int kR = 2 * kA + kC, kV = kJA + 4, kG = (3 * kA + 1) / 2;
+      constexpr int kR = 2 * kA + kC, kV = kJA + kJB / 2, kG = (3 * kA + 1) / 2;
       __builtin_amdgcn_sched_barrier(0);
       u32x2 na, nbs;
       if constexpr (kOdd) {
@@ -197,8 +213,8 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
           const int gi = u * kA + i;
 #pragma unroll
           for (int v = kV * gi / kG; v < (gi < kG ? kV * (gi + 1) / kG : 0); ++v) {
-            if (v < 4) load_b(4 * kOdd + v, s / 2 + 1, Bn);
-            else load_a(v - 4, s + 1, An);
+            if (v < kJB / 2) load_b(kJB / 2 * kOdd + v, s / 2 + 1, Bn);
+            else load_a(v - kJB / 2, s + 1, An);
           }
           if (u == 0) {
 #pragma unroll
@@ -305,13 +321,13 @@ __device__ __forceinline__ void fp8_tile(const GemmArgs& g, const TileInfo& t, i
   }
 }
 
-template <bool kUnit>
+template <bool kUnit, int kCols>
 __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_fp8_kernel(GemmArgs g) {
   // separate arrays: a load into one buffer does not alias reads of the other
   __shared__ __attribute__((aligned(16))) uint8_t A0[kTM * kF8RowBytes];
   __shared__ __attribute__((aligned(16))) uint8_t A1[kTM * kF8RowBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t B0[kXN * kF8RowBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t B1[kXN * kF8RowBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t B0[kCols * kF8RowBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t B1[kCols * kF8RowBytes];
   __shared__ u32x2 SA0[kTM];
   __shared__ u32x2 SA1[kTM];
   __shared__ u32x2 SB0[kXN];
@@ -322,13 +338,15 @@ __global__ __launch_bounds__(kGemmThreads, 1) void grouped_gemm_fp8_kernel(GemmA
   const int tid = threadIdx.x;
   TileInfo t;
   int pair = 0;
-  if (!mx_head<kUnit ? kXN / 2 : kXN>(g, tid, t, pair)) return;
-  if (t.valid <= kF8Small)
-    fp8_tile<false, kUnit>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s, scale_s,
-                           pair);
-  else
-    fp8_tile<true, kUnit>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s, scale_s,
-                          pair);
+  if (!mx_head<kUnit ? kCols / 2 : kCols>(g, tid, t, pair)) return;
+  if constexpr (kCols == kXN)
+    if (t.valid <= kF8Small) {
+      fp8_tile<false, kUnit, kCols>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s,
+                                    scale_s, pair);
+      return;
+    }
+  fp8_tile<true, kUnit, kCols>(g, t, tid, A0, A1, B0, B1, SA0, SA1, SB0, SB1, pair_s, row_s,
+                               scale_s, pair);
 }
 
 template <bool kUnit>
@@ -344,8 +362,14 @@ static int fp8_entry(const uint8_t* x_codes, const uint8_t* x_scales, int32_t ro
                               num_experts, N, topk, pair_scale, alpha, limit, expert_offsets,
                               sorted_pairs, tiles, num_tiles, max_tiles, tile_m, out);
   if (st != kOk || grid == 0) return st;
-  hipLaunchKernelGGL(grouped_gemm_fp8_kernel<kUnit>, dim3((unsigned)grid), dim3(kGemmThreads), 0,
-                     stream, g);
+  GemmArgs n = g;
+  const int64_t narrow = mx_grid(n, kF8Narrow);
+  if (narrow_tiles(g.P, num_experts, N) && narrow <= most_groups(kGemmThreads))
+    hipLaunchKernelGGL((grouped_gemm_fp8_kernel<kUnit, kF8Narrow>), dim3((unsigned)narrow),
+                       dim3(kGemmThreads), 0, stream, n);
+  else
+    hipLaunchKernelGGL((grouped_gemm_fp8_kernel<kUnit, kXN>), dim3((unsigned)grid),
+                       dim3(kGemmThreads), 0, stream, g);
   return launch_status();
 }
 

@@ -73,6 +73,12 @@ __device__ __forceinline__ bool mx_head(const GemmArgs& g, int tid, TileInfo& t,
   return t.valid > 0;
 }
 
+// Host: the workgroups for column tiles of `cols` weight rows.
+static inline int64_t mx_grid(GemmArgs& g, int cols) {
+  g.n_col_tiles = (g.Nw + cols - 1) / cols;
+  return ceil_div64((int64_t)g.max_tiles * ceil_div64(g.n_col_tiles, kGroup), 8) * 8 * kGroup;
+}
+
 // Host: the checks of a product's arguments, its argument block and its grid (0:
 // nothing to enqueue).  row_bytes: an activation row's codes.
 static inline int mx_gemm_args(GemmArgs& g, int64_t& grid, bool unit, const uint8_t* x_codes,
@@ -112,12 +118,9 @@ static inline int mx_gemm_args(GemmArgs& g, int64_t& grid, bool unit, const uint
   g.offsets = expert_offsets; g.sorted_pairs = sorted_pairs; g.tiles = tiles;
   g.num_tiles = num_tiles; g.out = out;
   g.act_alpha = alpha; g.act_limit = limit;
-  g.n_col_tiles = (N + kXN - 1) / kXN;                     // 256 weight rows per tile
-  const int64_t units = (int64_t)max_tiles * ceil_div64(g.n_col_tiles, kGroup);
-  grid = ceil_div64(units, 8) * 8 * kGroup;
-  if (grid > most_groups(kGemmThreads)) return kNotSupported;
   g.max_tiles = max_tiles;
-  return kOk;
+  grid = mx_grid(g, kXN);
+  return grid > most_groups(kGemmThreads) ? kNotSupported : kOk;
 }
 
 }  // namespace gq

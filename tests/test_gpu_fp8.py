@@ -117,6 +117,13 @@ def test_tile_edges(K, N, unit):
     _check(out, ref)
 
 
+@pytest.mark.parametrize("unit", [False, True])
+@pytest.mark.parametrize("K", [32, 96, 160, 256, 384, 512, 672, 1056, 2880])
+def test_tile_edges_of_many_tiles(K, unit):
+    """The same with more tiles than run at once, whose columns are 256 wide."""
+    test_tile_edges(K, 1312, unit)
+
+
 @pytest.mark.parametrize("K", [32, 96, 256, 352, 512, 1056])
 def test_one_hot_probe_is_bit_exact(K):
     """x = e_k (1 = 256 2^-8 in its block): the output row is the decoded weight
