@@ -188,3 +188,40 @@ def test_a_stream_of_its_own():
     s.synchronize()
     _same(got, ref)
     _same((dx, dw), gq.gq_rms_norm_backward(ref.y, ref.residual, gain))
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, workspaces and outputs of their own: the
+    bytes of the same calls one after the other."""
+    dev = device()
+    g = torch.Generator().manual_seed(31)
+    E, H, N, rows = 6, 512, 320, 700
+    w = torch.rand(H, generator=g).to(torch.bfloat16).to(dev)
+    blocks = torch.randint(0, 256, (E, N, H // 32, 16), dtype=torch.uint8, generator=g).to(dev)
+    scales = torch.randint(120, 128, (E, N, H // 32), dtype=torch.uint8, generator=g).to(dev)
+    bias = (0.1 * torch.randn(E, generator=g)).to(dev)
+    sets = [[torch.randn(rows, n, generator=g).to(torch.bfloat16).to(dev) for n in (H, H, H, E)]
+            for _ in range(2)]
+
+    def block(x, r, dy, z):
+        n = gq.gq_rms_norm(x, w, residual=r, mxfp8=True)
+        ids, weights = gq.gq_moe_route(z, 2, score="sigmoid", bias=bias, groups=3, topk_groups=2)
+        y = gq.gq_mxfp4_grouped_gemm_fp8(n.mxfp8, blocks, scales, gq.gq_route_sort(ids, E),
+                                         pair_scale=weights.reshape(-1))
+        dx, dw = gq.gq_rms_norm_backward(dy, n.residual, w, d_residual=x)
+        dz = gq.gq_moe_route_backward(weights, z, ids, score="sigmoid")
+        return n.y, *n.mxfp8, ids, weights, y, dx, dw, dz
+
+    say("two streams")
+    want = [block(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(block(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for one in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(one, want[i]))
