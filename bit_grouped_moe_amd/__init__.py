@@ -976,7 +976,8 @@ def gq_rms_norm(x, weight, eps=1e-6, residual=None, y=True, sum=None, mxfp8=Fals
 
 
 def gq_rms_norm_backward_workspace(rows, H):
-    """Bytes of workspace for gq_rms_norm_backward; -1 where it does not take the sizes."""
+    """Bytes of workspace for gq_rms_norm_backward of up to ``rows`` rows; -1 where it does
+    not take the sizes."""
     if not 0 <= rows < 1 << 63 or not 0 <= H < 1 << 31:
         return -1
     return int(load_library().gq_rms_norm_backward_workspace(rows, H))

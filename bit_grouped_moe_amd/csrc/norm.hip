@@ -473,6 +473,14 @@ static int64_t back_groups(int64_t rows, int H) {
   });
   return groups < kBackGroups ? groups : kBackGroups;
 }
+// The most of them for up to that many rows.  (Rows of 513 to 1024 values are one to a
+// workgroup up to kNormFew rows and four from there on: the number falls at that border
+// and nowhere else.)
+static int64_t most_back_groups(int64_t rows, int H) {
+  const int64_t all = back_groups(rows, H);
+  const int64_t few = back_groups(rows < kNormFew ? rows : kNormFew, H);
+  return all > few ? all : few;
+}
 
 }  // namespace gq
 
@@ -521,7 +529,7 @@ extern "C" int gq_rms_norm(const void* x, int64_t x_stride, const void* residual
 extern "C" int64_t gq_rms_norm_backward_workspace(int64_t rows, int32_t H) {
   using namespace gq;
   if (rows < 0 || H < 1 || H > kNormMaxWidth) return -1;
-  return back_groups(rows, H) * H * 4;
+  return most_back_groups(rows, H) * H * 4;
 }
 
 extern "C" int gq_rms_norm_backward(const void* d_y, int64_t d_y_stride, const void* h,

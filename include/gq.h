@@ -527,9 +527,10 @@ int gq_mxfp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t K, i
  *   d_x       dtype [rows, H]                                          out
  *   d_weight  weight_dtype [H] or NULL: not wanted                     out
  *   workspace 16-byte aligned device memory of at least
- *             gq_rms_norm_backward_workspace(rows, H) bytes (with d_weight);
- *             carries nothing from one call to the next; two calls that may
- *             run at the same time need one each
+ *             gq_rms_norm_backward_workspace(rows, H) bytes (with d_weight),
+ *             which never falls as rows grow: one made for the most rows
+ *             serves any number of them; carries nothing from one call to the
+ *             next; two calls that may run at the same time need one each
  * float32 sums in a fixed order; rows == 0 writes d_weight = 0.  The gradient
  * of codes is taken as y's (straight through).  d_x may be d_y, h or d_h where
  * that is contiguous.
