@@ -144,22 +144,34 @@ __device__ __forceinline__ void select64(const RouteArgs& g, const float (&z)[C]
 }
 
 // ---- in 32 bits, where that decides -------------------------------------------
-// Scores in float32 from the hardware exponential and reciprocal.  A sigmoid is off
-// by less than 2^-22 (s (1 - s) |z| < 1/4 times the argument's rounding, and an ulp
-// each of the exponential, the sum and the reciprocal), a softmax by less than
-// 2^-19 of itself (up to 22 additions of its sum) and so of the row's largest, the
-// sum with the bias by 2^-24 of itself.
-// Two choices further apart than both errors are in the order of float64; so are
-// choices of equal logits and biases, by index.  A row that this does not decide is
-// selected again in 64 bits: one row in 10^3 with random float32 logits and biases.
+// Scores in float32 from the hardware exponential and reciprocal (an ulp each).  A
+// sigmoid is off by less than off = 2^-22 (s (1 - s) |z| < 1/4 times the argument's
+// rounding, and an ulp each of the exponential, the sum and the reciprocal), the sum
+// with the bias by 2^-24 of itself.
+// A softmax's score is e^-x / sum, x how far its logit lies below the peak.  Far below,
+// where x's rounding counts x times, it is off by several 2^-19 of itself; what is
+// needed and holds is a bound on differences of choices, by off = 2^-19 of the row's
+// largest score.  In units of 2^-24 of that score: the argument x log2 e is off by 2.3 x
+// (x, log2 e and their product rounded), so a numerator by e^-x (2.3 x + 2) <= 2.1, and
+// by 1 where it is multiplied by the sum's inverse: 3.1 of a score's own.  The inverse
+// is off by 2.3 times the row's mean of x weighted by e^-x (at most 4.5 for 1024
+// experts), 2 for the exponentials, 22 additions and 2 for the reciprocal: 37 for the
+// largest score and in proportion for every other, the same way for all.  Two scores'
+// difference is so off by 37 + 2 3.1 < 64 = 2 off, that of two sums of two by
+// 2 37 + 4 3.1 < 128 = 4 off, and one score against its value in 64 bits by
+// 37 + 3.1 < 2 off.
+// Two choices further apart than that and their sums' roundings are in the order of
+// float64; so are choices of equal logits and biases, by index.  A row that this does
+// not decide is selected again in 64 bits: one row in 10^3 with random float32 logits
+// and biases.
 __device__ __forceinline__ float fast_exp(float d) {
   return __builtin_amdgcn_exp2f(d * 1.44269504088896341f);
 }
 __device__ __forceinline__ float fast_sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + fast_exp(-z));
 }
-// Whether a choice a (at least) lies clearly above a choice b (at most), whose scores
-// are off by less than `off`; false with a NaN.
+// Whether a choice a (at least) lies clearly above a choice b (at most), the difference
+// of whose scores is off by less than 2 `off`; false with a NaN.
 __device__ __forceinline__ bool clearly(float a, float b, float off) {
   return a - b > 2.f * off + 0x1p-23f * (fabsf(a) + fabsf(b));
 }
@@ -177,7 +189,8 @@ struct GroupValue {
       size += fabsf(w);
     }
     key = first > kDeadKey ? logit_key(v) : 0u;
-    // off for each choice; half a step for each, for v and for a bound itself
+    // off for each choice (against another group's as many); half a step for each, for v
+    // and for a bound itself
     const float room = (sums ? 2.f : 1.f) * off + 0x1p-22f * size;
     const bool sound = room < __builtin_inff();          // no NaN, nothing overflowed
     low = sound ? logit_key(v - room) : 0u;
