@@ -248,7 +248,9 @@ __global__ __launch_bounds__(kNormThreads<kWaves>) void rms_norm_backward_kernel
   const int lane = threadIdx.x & (kLanes - 1);
   const int H = g.H, chunks = (H + 7) / 8;
   // what the registers hold: rows of one to four waves the next row's values too, of
-  // sixteen waves and 32 values a lane not even this row's (they are read again)
+  // sixteen waves and 32 values a lane not even this row's (they are read again).  The
+  // 128 registers of 1024 threads do not quite do: bf16 rows of 8193 to 16384 values
+  // spill 36 bytes a lane, float32 rows beyond 12
   constexpr bool kNext = kWaves < 16 && (kType != GQ_F32 || kC < 4), kKeep = kWaves * kC < 64;
   float acc[kC][8];
 #pragma unroll
@@ -410,6 +412,11 @@ __global__ __launch_bounds__(kGainCols * kGainRuns) void rms_norm_gain_kernel(
 //   1024    4.3 8.0   4.5 8.7         6.1 13.4   8.2 13.9    12.5 23.2  14.3 24.7
 // 16384 rows of 512: a wave a row 13.2 and 16.5, four 18.1 and 34.2; of 2048: one wave
 // 43.3 and 47.8, four 41.1 and 47.7.
+// float32 in the forms chosen, forward and backward with the gain's gradient: 16384
+// rows of 512 22.1 and 24.1, of 2048 95 and 103, 2048 of 8192 45 and 53 (4 bytes of each
+// of four tensors, 5.0 to 6.1 TB/s).  Few wide rows are held up by the partial sums, a
+// row of them a workgroup: 1024 of 16384 50 and 69, 512 of 32768 48 and 106, without the
+// gain's gradient 45 and 67.
 constexpr int kNormFew = 256;
 template <typename F>
 static void by_row(int64_t rows, int H, F&& f) {

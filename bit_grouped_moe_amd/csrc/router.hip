@@ -130,16 +130,19 @@ __global__ __launch_bounds__(kRouterThreads) void moe_topk_backward_kernel(
 //
 // Measured, top-8, wave -> group, us (graph-replayed, launch included):
 //                    bf16 E = 128   bf16 E = 256   f32 E = 128    f32 E = 256
-//   256 rows forward  2.89 -> 2.69   3.44 -> 3.28   2.88 -> 3.84   3.37 -> 5.71
-//   4096     forward  3.86 -> 2.86   4.73 -> 3.50   3.82 -> 4.39   4.62 -> 6.06
-//   8192     forward  5.14 -> 3.13   6.62 -> 4.18   5.15 -> 4.81   6.50 -> 9.42
-//   16384    forward  8.22 -> 4.16  10.56 -> 5.75   7.86 -> 6.63  10.43 -> 12.85
-//   256     backward  2.76 -> 2.72   3.27 -> 2.86   2.59 -> 2.69   3.31 -> 3.22
-//   4096    backward  3.66 -> 2.93   4.79 -> 3.27   3.67 -> 3.11   5.12 -> 4.31
-//   16384   backward  8.00 -> 3.64  12.12 -> 4.95   8.56 -> 4.68  12.70 -> 9.29
-// Below 4096 rows the softmax over all experts (not renormalised) is up to
-// 0.8 us slower in sixteen lanes; hence kGroupFrom.  The 64-bit keys of float32
-// pay from 64 rows an expert on and not at all above 128 experts.
+//   256 rows forward  3.09 -> 2.85   3.61 -> 3.47   3.12 -> 3.30   3.58 -> 4.57
+//   4096     forward  4.03 -> 3.01   4.91 -> 3.72   4.05 -> 3.79   4.84 -> 4.84
+//   8192     forward  5.28 -> 3.35   6.69 -> 4.38   5.32 -> 4.03   6.66 -> 6.04
+//   16384    forward  8.11 -> 4.27  10.66 -> 5.97   8.13 -> 5.51  10.51 -> 8.82
+//   256     backward  2.85 -> 2.85   3.59 -> 3.10   2.84 -> 2.96   3.55 -> 3.42
+//   4096    backward  3.80 -> 3.06   5.01 -> 3.53   4.15 -> 3.35   5.23 -> 4.46
+//   16384   backward  8.03 -> 3.77  12.19 -> 5.17   8.43 -> 4.89  12.67 -> 9.38
+// Below 4096 rows the softmax over all experts (not renormalised) is up to 1 us
+// slower in sixteen lanes (bf16; float32 2); hence kGroupFrom.  The 64-bit keys of
+// float32 need more rows: over all of 128 experts 4.25 -> 4.50 at 4096 rows, 5.70 ->
+// 4.79 at 8192, hence 64 rows an expert.  Above 128 experts float32 keeps to a wave a
+// row, which is the faster of the two up to 8192 rows of 256 over all experts (7.41 ->
+// 7.59) and the slower at 16384 (11.80 -> 11.16, renormalised as above).
 constexpr int kGroupFrom = 4096;                         // rows
 
 __device__ __forceinline__ uint64_t group_max(uint64_t v) {
